@@ -11,4 +11,5 @@ from .binding import (PiError, desc_of, layer_desc, lib, library_path, pi_compac
                       pi_sparse_fc2_tiered, pi_ffn_layer_tiered,
                       pi_status_string, pi_workspace_bytes, pi_workspace_layout, ranks_array,
                       weights_array, weights_struct, attn_desc, attn_desc_of, attn_weights_struct,
-                      pi_attn_heads, pi_attn_workspace_bytes)
+                      pi_attn_heads, pi_attn_workspace_bytes, tables_desc, pi_block_tables, rope_plan, page_desc,
+                      pi_rope_store, paged_desc, pi_paged_workspace_bytes, pi_paged_attn)

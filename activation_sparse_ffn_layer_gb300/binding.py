@@ -17,6 +17,7 @@ from .build import LIB
 
 PI_OK, PI_ERR_INVALID_ARG, PI_ERR_UNSUPPORTED, PI_ERR_CUDA, PI_ERR_TIMEOUT, PI_ERR_WORKSPACE = range(6)
 PI_W_F16, PI_W_INT4_G32 = 0, 1
+PI_T_F16, PI_T_BF16, PI_T_F32 = 0, 1, 2
 
 
 class pi_layer_desc(C.Structure):
@@ -50,6 +51,35 @@ class pi_attn_weights(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in ("wqkv", "bqkv", "wot", "bo", "p1", "p2", "bp")]
 
 
+class pi_tables_desc(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("batch", "page_size", "num_pages", "max_pages", "max_tokens")]
+
+
+class pi_page_desc(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("kv_heads", "head_dim", "page_size", "num_pages", "dtype")] + \
+        [(n, C.c_longlong) for n in ("page_stride", "head_stride", "token_stride")]
+
+
+class pi_rope_desc(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("head_dim", "rot_dim", "interleaved", "scaling")] + \
+        [(n, C.c_double) for n in ("base", "factor", "original_max", "low", "high", "mscale")]
+
+
+class pi_rope_plan(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("head_dim", "rot_dim", "interleaved")] + \
+        [("mscale", C.c_float), ("turns", C.c_uint64 * 64)]
+
+
+class pi_qkv_desc(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("tokens", "heads", "dtype")] + \
+        [(n, C.c_longlong) for n in ("q_stride", "k_stride", "v_stride", "out_stride")]
+
+
+class pi_paged_desc(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("heads", "batch", "max_tokens", "max_new", "max_pages", "window")] + \
+        [("scale", C.c_float)]
+
+
 class PiError(RuntimeError):
     def __init__(self, fn: str, status: int, msg: str):
         super().__init__(f"{fn}: {msg} (status {status})")
@@ -63,7 +93,8 @@ EXPORTS = ("pi_workspace_bytes", "pi_workspace_layout", "pi_predict", "pi_compac
            "pi_last_device_status", "pi_launches_per_layer", "pi_ffn_stack", "pi_debug_wait_timeout",
            "pi_sparse_fc2_noalloc", "pi_stack_plan", "pi_stack_plan_for", "pi_debug_set_wait_timeout",
            "pi_sparse_fc1_tiered", "pi_sparse_fc2_tiered", "pi_ffn_layer_tiered", "pi_attn_workspace_bytes",
-           "pi_attn_heads")
+           "pi_attn_heads", "pi_block_tables", "pi_rope_plan_init", "pi_rope_store", "pi_paged_workspace_bytes",
+           "pi_paged_attn")
 
 
 def library_path() -> str:
@@ -107,6 +138,12 @@ def lib(path: Optional[str] = None):
         "pi_attn_workspace_bytes": (S, [C.POINTER(pi_attn_desc)]),
         "pi_attn_heads": (I, [C.POINTER(pi_attn_desc), P, C.POINTER(pi_attn_weights), P, P, P, Fl, P, P, P, S,
                               P]),
+        "pi_block_tables": (I, [C.POINTER(pi_tables_desc)] + [P] * 13),
+        "pi_rope_plan_init": (I, [C.POINTER(pi_rope_desc), C.POINTER(pi_rope_plan)]),
+        "pi_rope_store": (I, [C.POINTER(pi_rope_plan), C.POINTER(pi_page_desc), C.POINTER(pi_qkv_desc)] + [P] * 9),
+        "pi_paged_workspace_bytes": (S, [C.POINTER(pi_paged_desc), C.POINTER(pi_page_desc)]),
+        "pi_paged_attn": (I, [C.POINTER(pi_paged_desc), C.POINTER(pi_page_desc), P, C.c_longlong, P, P, P, P, P, P,
+                              C.c_longlong, P, P, S, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -341,3 +378,139 @@ def pi_attn_heads(desc, x, wstruct, kcache, vcache, pos, tau: float, head_mask, 
                                                 _ptr(vcache), _ptr(pos), float(tau), _ptr(head_mask), _ptr(y),
                                                 _ptr(workspace), workspace.numel() * workspace.element_size(),
                                                 _stream()))
+
+
+# ------------------------------------------------------------------ paged serving
+
+_DTYPES = {torch.float16: PI_T_F16, torch.bfloat16: PI_T_BF16, torch.float32: PI_T_F32}
+_SCALINGS = {"none": 0, "linear": 1, "blend": 2, "ramp": 3}
+
+
+def _flat(t: torch.Tensor, dtype: torch.dtype, least: int, name: str) -> int:
+    """Address of a contiguous CUDA tensor of this type with at least this many elements."""
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.numel() < least:
+        raise ValueError(f"{name}: expected a contiguous CUDA tensor of {least} or more {dtype} values")
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, heads: int, head_dim: int, name: str) -> int:
+    """Checks a [tokens, heads, head_dim] CUDA tensor whose tokens may be apart;
+    returns the elements between tokens."""
+    if not t.is_cuda or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim or t.stride(2) != 1 or \
+            (heads > 1 and t.stride(1) != head_dim):
+        raise ValueError(f"{name}: expected a CUDA tensor [tokens, {heads}, {head_dim}] with its heads one after another")
+    return t.stride(0) if t.shape[0] > 1 else heads * head_dim
+
+
+def tables_desc(batch: int, page_size: int, num_pages: int, max_pages: int, max_tokens: int) -> pi_tables_desc:
+    return pi_tables_desc(batch, page_size, num_pages, max_pages, max_tokens)
+
+
+def pi_block_tables(desc, cached_len, new_len, held, held_out, block_table, free_list, free_count, free_count_out,
+                    cu_new, kv_len, slots, positions):
+    """Page accounting, block tables, slots and positions of one step from the
+    request lengths (`held_out` may be `held`, `free_count_out` may be
+    `free_count`).  Running out of pages shows as kv_len 0 and slots -1."""
+    B, i32 = desc.batch, torch.int32
+    _check("pi_block_tables", lib().pi_block_tables(
+        C.byref(desc), _flat(cached_len, i32, B, "cached_len"), _flat(new_len, i32, B, "new_len"),
+        _flat(held, i32, B, "held"), _flat(held_out, i32, B, "held_out"),
+        _flat(block_table, i32, B * desc.max_pages, "block_table"), _flat(free_list, i32, desc.num_pages, "free_list"),
+        _flat(free_count, i32, 1, "free_count"), _flat(free_count_out, i32, 1, "free_count_out"),
+        _flat(cu_new, i32, B + 1, "cu_new"), _flat(kv_len, i32, B, "kv_len"),
+        _flat(slots, torch.int64, desc.max_tokens, "slots"), _flat(positions, i32, desc.max_tokens, "positions"),
+        _stream()))
+
+
+def rope_plan(head_dim: int, rot_dim: Optional[int] = None, interleaved: bool = False, base: float = 10000.0,
+              scaling: str = "none", factor: float = 1.0, original_max: float = 0.0, low: float = 1.0,
+              high: float = 4.0, mscale: float = 1.0) -> pi_rope_plan:
+    """The plan pi_rope_store takes (host only).  `scaling`: "none", "linear"
+    (positions / factor), "blend" (frequencies between `low` and `high`
+    wavelengths per original_max blended) or "ramp" (pair indices between
+    `high` and `low` turns per original_max blended)."""
+    if scaling not in _SCALINGS:
+        raise ValueError(f"scaling: expected one of {sorted(_SCALINGS)}")
+    d = pi_rope_desc(head_dim, head_dim if rot_dim is None else rot_dim, 1 if interleaved else 0, _SCALINGS[scaling],
+                     float(base), float(factor), float(original_max), float(low), float(high), float(mscale))
+    out = pi_rope_plan()
+    _check("pi_rope_plan_init", lib().pi_rope_plan_init(C.byref(d), C.byref(out)))
+    return out
+
+
+def page_desc(kcache: torch.Tensor, vcache: torch.Tensor) -> pi_page_desc:
+    """The description of two cache tensors [pages, kv_heads, page_size,
+    head_dim] of one shape, type and layout; any order of the first three in
+    memory (a transposed view of a tokens-first tensor, for instance)."""
+    if kcache.dim() != 4 or kcache.shape != vcache.shape or kcache.dtype is not vcache.dtype or \
+            kcache.dtype not in _DTYPES or kcache.stride(3) != 1 or vcache.stride(3) != 1:
+        raise ValueError("expected two [pages, kv_heads, page_size, head_dim] tensors of one shape and type with "
+                         "contiguous heads")
+    pages, heads, page, dh = kcache.shape
+    # a dimension of one element is never stepped along
+    st = [kcache.stride(i) if n > 1 else dh for i, n in enumerate((pages, heads, page))]
+    if st != [vcache.stride(i) if n > 1 else dh for i, n in enumerate((pages, heads, page))]:
+        raise ValueError("expected key and value caches of the same strides")
+    return pi_page_desc(heads, dh, page, pages, _DTYPES[kcache.dtype], st[0], st[1], st[2])
+
+
+def _cache(cache: pi_page_desc, t: torch.Tensor, name: str) -> int:
+    if not t.is_cuda or _DTYPES.get(t.dtype) != cache.dtype or \
+            tuple(t.shape) != (cache.num_pages, cache.kv_heads, cache.page_size, cache.head_dim) or \
+            (t.shape[0] > 1 and t.stride(0) != cache.page_stride) or \
+            (t.shape[1] > 1 and t.stride(1) != cache.head_stride) or t.stride(2) != cache.token_stride or \
+            t.stride(3) != 1:
+        raise ValueError(f"{name}: not the cache that the page_desc describes")
+    return t.data_ptr()
+
+
+def pi_rope_store(plan, cache, q, k, v, positions, slots, q_out, kcache, vcache):
+    """Rotates q [T, heads, dh] into q_out and k [T, kv_heads, dh] into the
+    cache at `slots`, and stores v there.  q and q_out may be None (store
+    only), or k, v, slots, kcache and vcache (rotate only)."""
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("expected q or k")
+    T, dh, d = x.shape[0], cache.head_dim, pi_qkv_desc()
+    d.tokens, d.heads, d.dtype = T, q.shape[1] if q is not None else 1, _DTYPES.get(x.dtype, -1)
+    qp = op = kp = vp = sp = kc = vc = None
+    if q is not None:
+        d.q_stride, d.out_stride = _rows(q, d.heads, dh, "q"), _rows(q_out, d.heads, dh, "q_out")
+        if q_out.shape[0] < T or _DTYPES.get(q_out.dtype) != cache.dtype:
+            raise ValueError("q_out: expected the shape of q and the type of the cache")
+        qp, op = q.data_ptr(), q_out.data_ptr()
+    if k is not None:
+        d.k_stride, d.v_stride = _rows(k, cache.kv_heads, dh, "k"), _rows(v, cache.kv_heads, dh, "v")
+        if k.shape[0] != T or v.shape[0] != T or k.dtype is not x.dtype or v.dtype is not x.dtype:
+            raise ValueError("k, v: expected the tokens and the type of q")
+        kp, vp, sp = k.data_ptr(), v.data_ptr(), _flat(slots, torch.int64, T, "slots")
+        kc, vc = _cache(cache, kcache, "kcache"), _cache(cache, vcache, "vcache")
+    _check("pi_rope_store", lib().pi_rope_store(C.byref(plan), C.byref(cache), C.byref(d), qp, kp, vp,
+                                                _flat(positions, torch.int32, T, "positions"), sp, op, kc, vc,
+                                                _stream()))
+
+
+def paged_desc(heads: int, batch: int, max_tokens: int, max_new: int, max_pages: int, window: int = 0,
+               scale: float = 0.0) -> pi_paged_desc:
+    """`scale` 0: 1 / sqrt(head_dim); `window` 0: none."""
+    return pi_paged_desc(heads, batch, max_tokens, max_new, max_pages, window, scale)
+
+
+def pi_paged_workspace_bytes(desc: pi_paged_desc, cache: pi_page_desc) -> int:
+    return int(lib().pi_paged_workspace_bytes(C.byref(desc), C.byref(cache)))
+
+
+def pi_paged_attn(desc, cache, q, kcache, vcache, block_table, cu_new, kv_len, out, lse, workspace):
+    """Causal attention of the packed new tokens q [max_tokens, heads, dh] over
+    the paged cache into out (same shape and type); lse [max_tokens, heads]
+    fp32 or None; workspace uint8, zero-filled before its first use."""
+    T, H, B, i32 = desc.max_tokens, desc.heads, desc.batch, torch.int32
+    qs, os_ = _rows(q, H, cache.head_dim, "q"), _rows(out, H, cache.head_dim, "out")
+    if q.shape[0] < T or out.shape[0] < T or _DTYPES.get(q.dtype) != cache.dtype or out.dtype is not q.dtype:
+        raise ValueError("q, out: expected max_tokens rows of the cache's type")
+    _check("pi_paged_attn", lib().pi_paged_attn(
+        C.byref(desc), C.byref(cache), q.data_ptr(), qs, _cache(cache, kcache, "kcache"),
+        _cache(cache, vcache, "vcache"), _flat(block_table, i32, B * desc.max_pages, "block_table"),
+        _flat(cu_new, i32, B + 1, "cu_new"), _flat(kv_len, i32, B, "kv_len"), out.data_ptr(), os_,
+        None if lse is None else _flat(lse, torch.float32, T * H, "lse"), _flat(workspace, torch.uint8, 0, "workspace"),
+        workspace.numel(), _stream()))

@@ -238,4 +238,7 @@ bool fc2_args_ok(const Plan& p, const float* h, const int32_t* idx, const int32_
                  const pi_layer_weights* w, const float* y);
 LayerPtrs layer_ptrs(const pi_layer_weights* w);
 
+// Checks of a paged cache's description (sizes, strides, type).
+bool page_desc_ok(const pi_page_desc& c);
+
 }  // namespace pi

@@ -335,6 +335,171 @@ PI_API pi_status pi_attn_heads(const pi_attn_desc *desc, const pi_half *x, const
                                uint32_t *head_mask, float *y, void *workspace, size_t ws_bytes,
                                void *stream);
 
+/* ------------------------------------------------------------------------
+ * Paged serving: block tables, rotary positions with the store into a paged
+ * key/value cache, and attention of new tokens over that cache.
+ *
+ * A request is a row b of a batch.  Its keys and values live in pages of
+ * page_size positions; block_table[b * max_pages + j] is the page of its
+ * positions j * page_size .. (j + 1) * page_size - 1.  The tokens of a step
+ * are packed: those of request b are rows cu_new[b] .. cu_new[b + 1] - 1.  A
+ * slot names a position of the cache: page * page_size + position % page_size.
+ * ---------------------------------------------------------------------- */
+typedef enum { PI_T_F16 = 0, PI_T_BF16 = 1, PI_T_F32 = 2 } pi_dtype;
+
+/* Rows, pages and capacities of a step. */
+typedef struct {
+    int batch;      /* rows B (1 .. 4096)                                              */
+    int page_size;  /* positions per page: 16, 32, 64 or 128                           */
+    int num_pages;  /* pages of the cache = capacity of the free list (1 .. 2^26)       */
+    int max_pages;  /* entries per block-table row (1 .. 2^20; max_pages * page_size   */
+                    /* <= 2^30)                                                        */
+    int max_tokens; /* capacity of slots and positions (0 .. 2^24)                      */
+} pi_tables_desc;
+
+/*
+ * Block tables, page accounting, slots and positions of one step, from the
+ * request lengths alone.  Row b keeps cached_len[b] positions and receives
+ * new_len[b] tokens; it holds held[b] pages now and needs
+ * ceil((cached_len + new_len) / page_size).
+ *   - Pages a row no longer needs (its request ended, was replaced by a
+ *     shorter one, or was rolled back) are pushed on the free list in row
+ *     order, then in column order: free_list[*free_count + i].
+ *   - Rows that need more take theirs off the top in row order.  A row is
+ *     served iff it needs none or the pages wanted up to and including it
+ *     are there; the others keep the pages they hold, get kv_len 0 and their
+ *     tokens slot -1.  Running out of pages is not an error: read kv_len.
+ * Out: held_out [B] (may be held), free_count_out [1] (may be free_count),
+ * cu_new [B + 1], kv_len [B] (cached + new of a served row), slots
+ * [max_tokens] and positions [max_tokens] (cached_len + i of a row's i-th
+ * token; entries past cu_new[B]: slot -1, position 0).  In and out:
+ * block_table [B, max_pages] (only entries of newly taken pages are written)
+ * and free_list [num_pages].  All int32 but slots (int64), on the device.
+ * A row with a negative length or page count, with more positions than a
+ * table row holds, or whose tokens pass max_tokens is not served, keeps its
+ * pages and sets the device status to PI_ERR_INVALID_ARG; its tokens are
+ * counted in cu_new up to max_tokens (none where a length is out of range).
+ * So does a free count outside 0 .. num_pages (taken as the nearest bound)
+ * and a push past num_pages (dropped).  One launch.
+ */
+PI_API pi_status pi_block_tables(const pi_tables_desc *desc, const int32_t *cached_len, const int32_t *new_len,
+                                 const int32_t *held, int32_t *held_out, int32_t *block_table, int32_t *free_list,
+                                 const int32_t *free_count, int32_t *free_count_out, int32_t *cu_new,
+                                 int32_t *kv_len, int64_t *slots, int32_t *positions, void *stream);
+
+/* A paged cache (keys and values are two arrays of this shape).  Element
+ * (page, head, position, i) is at page * page_stride + head * head_stride +
+ * position * token_stride + i (in elements), so both [pages, heads, page_size,
+ * head_dim] and [pages, page_size, heads, head_dim] are described.  Strides
+ * are multiples of 8 and at least head_dim; base pointers 16-byte aligned. */
+typedef struct {
+    int kv_heads;   /* 1 .. 1024                       */
+    int head_dim;   /* 64 or 128                       */
+    int page_size;  /* 16, 32, 64 or 128               */
+    int num_pages;  /* 1 .. 2^26                       */
+    int dtype;      /* PI_T_F16 or PI_T_BF16           */
+    long long page_stride, head_stride, token_stride;
+} pi_page_desc;
+
+/* How the frequencies base^(-2 i / rot_dim) become longer-range ones. */
+typedef enum {
+    PI_ROPE_NONE = 0,
+    PI_ROPE_LINEAR = 1, /* f / factor (positions interpolated)                            */
+    PI_ROPE_BLEND = 2,  /* by wavelengths per original length, r = original_max f / 2 pi:  */
+                        /* f / factor below `low`, f above `high`, linear in r between     */
+    PI_ROPE_RAMP = 3    /* by pair index: f up to the pair that turns `high` times within */
+                        /* original_max positions, f / factor from the one that turns     */
+                        /* `low` times, linear in the index between                        */
+} pi_rope_scaling;
+
+typedef struct {
+    int head_dim;      /* 64 or 128                                               */
+    int rot_dim;       /* leading elements that turn: 0 .. head_dim, multiple of 16 */
+    int interleaved;   /* 0: pairs (i, i + rot_dim/2); 1: pairs (2i, 2i + 1)      */
+    int scaling;       /* pi_rope_scaling                                         */
+    double base;       /* > 1                                                     */
+    double factor;     /* > 0 (scaled forms)                                      */
+    double original_max, low, high; /* blend and ramp: 0 < original_max, 0 < low < high */
+    double mscale;     /* factor on cos and sin (1: none), finite                 */
+} pi_rope_desc;
+
+/* What pi_rope_store needs of a pi_rope_desc: host memory, filled once by
+ * pi_rope_plan_init and passed to every call.  turns[i] is the angle of pair i
+ * per position as a fraction of a turn in 64-bit fixed point, so that position
+ * p turns by p * turns[i] modulo 2^64 with no loss at far positions. */
+typedef struct {
+    int head_dim, rot_dim, interleaved;
+    float mscale;
+    uint64_t turns[64];
+} pi_rope_plan;
+PI_API pi_status pi_rope_plan_init(const pi_rope_desc *desc, pi_rope_plan *plan);
+
+/* The projections of a step: token t's head h starts at t * stride + h *
+ * head_dim (in elements; strides multiples of 8, at least heads * head_dim). */
+typedef struct {
+    int tokens;        /* 0 .. 2^24                                         */
+    int heads;         /* query heads (1 .. 1024)                           */
+    int dtype;         /* of q, k, v: PI_T_F16, PI_T_BF16 or PI_T_F32       */
+    long long q_stride, k_stride, v_stride, out_stride;
+} pi_qkv_desc;
+
+/*
+ * Rotary positions and the store into the cache, one launch.  With a =
+ * positions[t] * f_i, each pair (x1, x2) of a query or key head becomes
+ *   mscale (x1 cos a - x2 sin a), mscale (x2 cos a + x1 sin a);
+ * the rest of the head and the values pass unchanged.  Arithmetic in fp32,
+ * rounded once to the cache's type.  q_out [tokens, heads, head_dim] (type of
+ * the cache; may be q where the types and strides agree); keys and values go
+ * to slots[t] of kcache and vcache.  A token with slot -1 is rotated and not
+ * stored; a slot past the cache or below -1 is not stored and sets the device
+ * status to PI_ERR_INVALID_ARG.  q and q_out may both be NULL (store only), or
+ * k, v, slots, kcache and vcache (rotate only).  All 16-byte aligned.
+ */
+PI_API pi_status pi_rope_store(const pi_rope_plan *plan, const pi_page_desc *cache, const pi_qkv_desc *desc,
+                               const void *q, const void *k, const void *v, const int32_t *positions,
+                               const int64_t *slots, void *q_out, void *kcache, void *vcache, void *stream);
+
+typedef struct {
+    int heads;      /* query heads, a multiple of the cache's kv_heads, at most 128 per KV head */
+    int batch;      /* requests (1 .. 4096)                                                    */
+    int max_tokens; /* rows of q and out (0 .. 2^24)                                            */
+    int max_new;    /* most new tokens of one request (1 .. max_tokens)                         */
+    int max_pages;  /* entries per block-table row (max_pages * page_size <= 2^30)             */
+    int window;     /* 0: none; else a position sees itself and the window - 1 before it        */
+    float scale;    /* of the scores; 0: 1 / sqrt(head_dim)                                    */
+} pi_paged_desc;
+
+/* Bytes of workspace pi_paged_attn needs (0 if a descriptor is invalid). */
+PI_API size_t pi_paged_workspace_bytes(const pi_paged_desc *desc, const pi_page_desc *cache);
+
+/*
+ * Causal attention of the new tokens over the paged cache, which holds their
+ * own keys and values already.  Request b has n = cu_new[b+1] - cu_new[b] new
+ * tokens, the last of its kv_len[b] positions; its i-th token is at position
+ * p = kv_len[b] - n + i and sees t = max(0, p - window + 1) .. p:
+ *   a_t = scale q . k_t,  out = sum_t e^{a_t} v_t / sum_t e^{a_t},
+ *   lse = log sum_t e^{a_t}
+ * for each query head h with key/value head h / (heads / kv_heads).  A token
+ * that sees nothing (its request has fewer positions than tokens, e.g. kv_len
+ * 0) gets zeros and lse -inf.  q [max_tokens, heads, head_dim] and out have the
+ * cache's type, rows q_stride and out_stride elements apart (multiples of 8);
+ * lse [max_tokens, heads] fp32, or NULL.  Rows past cu_new[batch] are left
+ * alone.  Positions that no token of the request sees are not used, whatever
+ * they hold.  Products of 16-bit values are summed in fp32; the weights
+ * e^{a_t - m} enter the second product rounded to the cache's type.  The
+ * result does not depend on timing (bitwise reproducible on one device).
+ * An inconsistent row (cu_new decreasing or past max_tokens, more than max_new
+ * tokens, kv_len outside 0 .. max_pages * page_size) is taken as one without
+ * tokens (kv_len: without keys) and a page id outside the cache reads as
+ * zeros; both set the device status to PI_ERR_INVALID_ARG.
+ * workspace: pi_paged_workspace_bytes, 16-byte aligned, zero-filled before its
+ * first use (and again after a PI_ERR_TIMEOUT).
+ */
+PI_API pi_status pi_paged_attn(const pi_paged_desc *desc, const pi_page_desc *cache, const void *q,
+                               long long q_stride, const void *kcache, const void *vcache,
+                               const int32_t *block_table, const int32_t *cu_new, const int32_t *kv_len, void *out,
+                               long long out_stride, float *lse, void *workspace, size_t ws_bytes, void *stream);
+
 /* How one pi_ffn_stack step of `desc` (n_layers layers with the given ranks,
  * NULL: all desc->rank) is executed on the current device.  Diagnostics: lets a
  * caller or a test see which streaming mode the batch-1 persistent kernel
