@@ -528,19 +528,25 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
     const uint64_t c2 = pair2(c, c);
     int ns = 0, nm = 0;   // tiles of this group so far (all pieces); merges
     for (int n = 0;; ++n) {
-        const Piece p = next_piece<DH>(sh, n, ctl);
-        if (p.nt == 0) return;
+        // the piece stays in its slot until it is done, so that the tile loop's
+        // registers go to the scores
+        if (!warp_wait(&sh.lfull[n % kListDepth], (n / kListDepth) & 1, ctl)) return;
+        const Piece& p = sh.list[n % kListDepth];
+        const int nt = p.nt, j0 = p.j0;
+        if (nt == 0) return;
         const bool pair = p.rows > kKeys;
         const int r = (pair ? w * kKeys : 0) + 32 * quad + lane;   // row of the item
         const bool live = r < p.rows;
-        const int tok = (p.row0 + r) / a.group, h = (p.row0 + r) - tok * a.group;
-        const int pos = p.first + tok;
-        const int hi = live ? max(pos + 1, 0) : 0;
-        const int lo = live && a.window > 0 ? min(max(0, pos - a.window + 1), hi) : 0;
+        int lo, hi;   // keys this row sees
+        {
+            const int pos = p.first + (p.row0 + r) / a.group;
+            hi = live ? max(pos + 1, 0) : 0;
+            lo = live && a.window > 0 ? min(max(0, pos - a.window + 1), hi) : 0;
+        }
         const bool any = __any_sync(FULL, live);
         float m = -INFINITY, l = 0.f;
         int mine = 0;         // tiles of this piece that this group has done
-        for (int t = pair ? 0 : w; t < p.nt; t += pair ? 1 : 2) {
+        for (int t = pair ? 0 : w; t < nt; t += pair ? 1 : 2) {
             if (!warp_wait(&sh.sfull[w], ns & 1, ctl)) return;
             tc_after();
             if (any) {
@@ -549,7 +555,7 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
                 for (int i = 0; i < kKeys; i += 32) tmem_ld32(s_at + (unsigned)i, s + i);
                 tmem_wait_ld();
                 tmem_loaded<kKeys>(s);
-                const int base = (p.j0 + t) * kKeys;
+                const int base = (j0 + t) * kKeys;
                 if (__any_sync(FULL, base < lo || base + kKeys > hi)) {
 #pragma unroll
                     for (int i = 0; i < kKeys; ++i)
@@ -635,6 +641,7 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
             c0 = w * cols;
             ++nm;
         }
+        const int tok = (p.row0 + r) / a.group, h = (p.row0 + r) - tok * a.group;
         const long long orow = (long long)(p.cu + tok);
         const int head = p.g * a.group + h;
         const bool own_any = mine > 0;                  // O_w holds something
@@ -776,6 +783,7 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
             if (!warp_wait(&sh.merged, (nm - 1) & 1, ctl)) return;
             tc_after();
         }
+        warp_arrive(&sh.lempty[n % kListDepth]);
     }
 }
 
@@ -884,16 +892,21 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_paged_attn(const __grid_co
     __syncthreads();
     const Ctl ctl{a.status, a.timeout_ns, &sh.abort_flag};
     if (work) {
-        if (warp < 8)
+        // 384 threads x 168 registers at launch = 256 x 208 + 128 x 88
+        if (warp < 8) {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
             softmax_role<T, DH>(a, sh, tmem, ctl);
-        else if (warp == 8)
-            tile_role<DH>(a, sh, ring, ctl);
-        else if (warp == 9)
-            mma_role<T, DH>(a, sh, qs, ring, tmem, ctl);
-        else if (warp == 10)
-            query_role<T, DH>(a, sh, qs, ctl);
-        else if (lane == 0)
-            list_role<DH>(a, sh, u1, U, G, ctl);
+        } else {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+            if (warp == 8)
+                tile_role<DH>(a, sh, ring, ctl);
+            else if (warp == 9)
+                mma_role<T, DH>(a, sh, qs, ring, tmem, ctl);
+            else if (warp == 10)
+                query_role<T, DH>(a, sh, qs, ctl);
+            else if (lane == 0)
+                list_role<DH>(a, sh, u1, U, G, ctl);
+        }
     }
     tc_before();
     __syncthreads();
