@@ -166,8 +166,15 @@ def _ptr(t: Optional[torch.Tensor]):
     return C.c_void_p(t.data_ptr())
 
 
+# handle of a device's current stream without a torch.cuda.Stream object around
+# it (3 us a call on a Grace core); the public way where torch has no such call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream():
-    return C.c_void_p(torch.cuda.current_stream().cuda_stream)
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _check(fn: str, st: int):
@@ -396,10 +403,11 @@ def _flat(t: torch.Tensor, dtype: torch.dtype, least: int, name: str) -> int:
 def _rows(t: torch.Tensor, heads: int, head_dim: int, name: str) -> int:
     """Checks a [tokens, heads, head_dim] CUDA tensor whose tokens may be apart;
     returns the elements between tokens."""
-    if not t.is_cuda or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim or t.stride(2) != 1 or \
-            (heads > 1 and t.stride(1) != head_dim):
+    shape, stride = t.shape, t.stride()
+    if not t.is_cuda or len(shape) != 3 or shape[1] != heads or shape[2] != head_dim or stride[2] != 1 or \
+            (stride[1] != head_dim and heads > 1):
         raise ValueError(f"{name}: expected a CUDA tensor [tokens, {heads}, {head_dim}] with its heads one after another")
-    return t.stride(0) if t.shape[0] > 1 else heads * head_dim
+    return stride[0] if shape[0] > 1 else heads * head_dim
 
 
 def tables_desc(batch: int, page_size: int, num_pages: int, max_pages: int, max_tokens: int) -> pi_tables_desc:
@@ -451,10 +459,14 @@ def page_desc(kcache: torch.Tensor, vcache: torch.Tensor) -> pi_page_desc:
     st = [kcache.stride(i) if n > 1 else dh for i, n in enumerate((pages, heads, page))]
     if st != [vcache.stride(i) if n > 1 else dh for i, n in enumerate((pages, heads, page))]:
         raise ValueError("expected key and value caches of the same strides")
-    return pi_page_desc(heads, dh, page, pages, _DTYPES[kcache.dtype], st[0], st[1], st[2])
+    d = pi_page_desc(heads, dh, page, pages, _DTYPES[kcache.dtype], st[0], st[1], st[2])
+    d.like = (kcache.dtype, kcache.shape, kcache.stride())   # what _cache compares first
+    return d
 
 
 def _cache(cache: pi_page_desc, t: torch.Tensor, name: str) -> int:
+    if t.is_cuda and getattr(cache, "like", None) == (t.dtype, t.shape, t.stride()):
+        return t.data_ptr()
     if not t.is_cuda or _DTYPES.get(t.dtype) != cache.dtype or \
             tuple(t.shape) != (cache.num_pages, cache.kv_heads, cache.page_size, cache.head_dim) or \
             (t.shape[0] > 1 and t.stride(0) != cache.page_stride) or \
@@ -471,20 +483,22 @@ def pi_rope_store(plan, cache, q, k, v, positions, slots, q_out, kcache, vcache)
     x = q if q is not None else k
     if x is None:
         raise ValueError("expected q or k")
-    T, dh, d = x.shape[0], cache.head_dim, pi_qkv_desc()
-    d.tokens, d.heads, d.dtype = T, q.shape[1] if q is not None else 1, _DTYPES.get(x.dtype, -1)
+    T, dh, kind, heads = x.shape[0], cache.head_dim, _DTYPES.get(x.dtype, -1), 1
+    qs = ks = vs = os_ = 0
     qp = op = kp = vp = sp = kc = vc = None
     if q is not None:
-        d.q_stride, d.out_stride = _rows(q, d.heads, dh, "q"), _rows(q_out, d.heads, dh, "q_out")
+        heads = q.shape[1]
+        qs, os_ = _rows(q, heads, dh, "q"), _rows(q_out, heads, dh, "q_out")
         if q_out.shape[0] < T or _DTYPES.get(q_out.dtype) != cache.dtype:
             raise ValueError("q_out: expected the shape of q and the type of the cache")
         qp, op = q.data_ptr(), q_out.data_ptr()
     if k is not None:
-        d.k_stride, d.v_stride = _rows(k, cache.kv_heads, dh, "k"), _rows(v, cache.kv_heads, dh, "v")
+        ks, vs = _rows(k, cache.kv_heads, dh, "k"), _rows(v, cache.kv_heads, dh, "v")
         if k.shape[0] != T or v.shape[0] != T or k.dtype is not x.dtype or v.dtype is not x.dtype:
             raise ValueError("k, v: expected the tokens and the type of q")
         kp, vp, sp = k.data_ptr(), v.data_ptr(), _flat(slots, torch.int64, T, "slots")
         kc, vc = _cache(cache, kcache, "kcache"), _cache(cache, vcache, "vcache")
+    d = pi_qkv_desc(T, heads, kind, qs, ks, vs, os_)
     _check("pi_rope_store", lib().pi_rope_store(C.byref(plan), C.byref(cache), C.byref(d), qp, kp, vp,
                                                 _flat(positions, torch.int32, T, "positions"), sp, op, kc, vc,
                                                 _stream()))

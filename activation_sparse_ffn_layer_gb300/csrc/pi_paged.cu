@@ -24,18 +24,20 @@ namespace {
 // their row by binary search in a prefix.  The stack after the pushes is never
 // read back: entry x of it is free_list[x] below the old count, else released
 // page x - count, still in its row's table entry (releasing rows' entries are
-// not overwritten, free-list entries below the old count are not written).  So
-// the blocks need one meeting point only: nobody may write held_out or
-// free_count_out, which may alias the inputs, before all have read them.
+// not overwritten, free-list entries below the old count are not written).
 //
-// Bound by latency (a few KB to a MB of traffic): the scan takes two barriers
-// per prefix, the searches log2(rows) shared-memory reads per item.  The rows
-// are scanned by every block of one cluster, whose hardware barrier is the
-// meeting point; one block where there is little to write.
+// Bound by latency (a few KB to a MB of traffic).  Every block scans all rows
+// (three block prefixes) and takes its share of the writes.  Small steps are
+// one block.  Large ones are two grids: kTabMoves, as wide as the writes need,
+// writes pages, slots and positions; kTabState, one block, writes held_out and
+// free_count_out, which may alias the inputs, and the other per-row outputs.
+// The second is a programmatic dependent of the first, which lets it go only
+// once each of its blocks has read all inputs; so it may overwrite them while
+// the first still writes, and waits for the first's end at its own.
 constexpr int kTabThreads = 1024;
-constexpr int kTabCluster = 8;
 constexpr int kTabMaxRows = 4096;
 constexpr int kTabPer = kTabMaxRows / kTabThreads;
+constexpr int kTabAll = 0, kTabMoves = 1, kTabState = 2;
 
 struct TablesArgs {
     const int32_t *cached, *fresh, *held;
@@ -44,7 +46,7 @@ struct TablesArgs {
     int32_t *free_count_out, *cu, *kv;
     int64_t* slots;
     int32_t* positions;
-    int B, page, num_pages, max_pages, max_tokens;
+    int B, page_shift, num_pages, max_pages, max_tokens;
     int* status;
 };
 
@@ -83,9 +85,11 @@ PI_DEV int row_of(const T* first, int n, T x) {
     return lo;
 }
 
+template <int PART>
 __global__ void __launch_bounds__(kTabThreads) k_block_tables(const TablesArgs a) {
-    pdl_entry();
+    if (PART != kTabState) asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ long long warp_sums[32];
+    __shared__ int free_in;
     extern __shared__ long long tab_smem[];
     const int B = a.B;
     // prefixes [B + 1]: tokens, pages given back, pages wanted; then per row
@@ -95,13 +99,13 @@ __global__ void __launch_bounds__(kTabThreads) k_block_tables(const TablesArgs a
     int* scached = tfirst + B + 1;
     int* sheld = scached + B;
     int* sneed = sheld + B;        // pages needed, -1: not served
-    const int rank = blockIdx.x, ranks = gridDim.x;
     const int per = (B + kTabThreads - 1) / kTabThreads;
     int c[kTabPer], n[kTabPer], h[kTabPer];
     bool bad[kTabPer];
     long long tok = 0;
     bool any_bad = false;
-    const long long capacity = (long long)a.max_pages * a.page;
+    const int page = 1 << a.page_shift;
+    const long long capacity = (long long)a.max_pages << a.page_shift;
 #pragma unroll
     for (int i = 0; i < kTabPer; ++i) {
         const int b = threadIdx.x * per + i;
@@ -117,11 +121,11 @@ __global__ void __launch_bounds__(kTabThreads) k_block_tables(const TablesArgs a
         }
         any_bad |= bad[i];
     }
-    const int f0 = *a.free_count;
-    const int f = min(max(f0, 0), a.num_pages);
-    any_bad |= f != f0;
+    if (threadIdx.x == 0) free_in = *a.free_count;
     long long total_tok;
     long long tp = block_prefix(tok, warp_sums, &total_tok);
+    const int f = min(max(free_in, 0), a.num_pages);
+    any_bad |= f != free_in;
     long long give = 0, want = 0;
     int need[kTabPer];
 #pragma unroll
@@ -135,7 +139,7 @@ __global__ void __launch_bounds__(kTabThreads) k_block_tables(const TablesArgs a
             sheld[b] = h[i];
             const bool past = n[i] > 0 && end > a.max_tokens;
             any_bad |= past;
-            if (!bad[i] && !past) need[i] = (c[i] + n[i] + a.page - 1) / a.page;
+            if (!bad[i] && !past) need[i] = (c[i] + n[i] + page - 1) >> a.page_shift;
             if (need[i] >= 0) {
                 give += max(0, h[i] - need[i]);
                 want += max(0, need[i] - h[i]);
@@ -179,10 +183,25 @@ __global__ void __launch_bounds__(kTabThreads) k_block_tables(const TablesArgs a
     long long A = warp_sums[threadIdx.x & 31];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) A = max(A, __shfl_xor_sync(FULL, A, o));
-    // every block of the cluster has read the inputs that the outputs may alias
-    if (ranks > 1) {
-        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    // the block has its inputs: what a thread read went to shared memory or
+    // into a prefix before the barriers above
+    if (PART != kTabState) asm volatile("griddepcontrol.launch_dependents;");
+    if (PART != kTabMoves) {
+        for (int b = threadIdx.x; b < B; b += kTabThreads) {
+            const int t0 = tfirst[b];
+            a.held_out[b] = sneed[b] >= 0 ? sneed[b] : sheld[b];
+            a.kv[b] = sneed[b] >= 0 ? scached[b] + tfirst[b + 1] - t0 : 0;
+            a.cu[b] = t0;
+        }
+        if (threadIdx.x == 0) {
+            a.cu[B] = tfirst[B];
+            *a.free_count_out = (int)min(f + R - A, (long long)a.num_pages);
+        }
+        if (any_bad) atomicExch(a.status, (int)PI_ERR_INVALID_ARG);
+    }
+    if (PART == kTabState) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
     }
 
     // row that gives back released page j, and the table entry it is in
@@ -193,7 +212,7 @@ __global__ void __launch_bounds__(kTabThreads) k_block_tables(const TablesArgs a
     // entry x of the stack once all releases are pushed
     auto stacked = [&](long long x) { return x < f ? a.free_list[x] : released(x - f); };
 
-    const long long t0 = (long long)rank * kTabThreads + threadIdx.x, step = (long long)ranks * kTabThreads;
+    const long long t0 = (long long)blockIdx.x * kTabThreads + threadIdx.x, step = (long long)gridDim.x * kTabThreads;
     bool dropped = false;
     for (long long j = t0; j < R; j += step) {
         if (f + j < a.num_pages) a.free_list[f + j] = released(j);
@@ -211,25 +230,16 @@ __global__ void __launch_bounds__(kTabThreads) k_block_tables(const TablesArgs a
             const int b = row_of(tfirst, B, (int)i);
             pos = scached[b] + (int)(i - tfirst[b]);
             if (sneed[b] >= 0) {
-                const int pi = pos / a.page, held = sheld[b];
-                const int page = pi < held ? a.table[(size_t)b * a.max_pages + pi]
-                                           : stacked(f + R - 1 - (wfirst[b] + pi - held));
-                slot = (long long)page * a.page + pos % a.page;
+                const int pi = pos >> a.page_shift, held = sheld[b];
+                const int id = pi < held ? a.table[(size_t)b * a.max_pages + pi]
+                                         : stacked(f + R - 1 - (wfirst[b] + pi - held));
+                slot = ((long long)id << a.page_shift) + (pos & (page - 1));
             }
         }
         a.slots[i] = slot;
         a.positions[i] = pos;
     }
-    for (long long b = t0; b < B; b += step) {
-        a.held_out[b] = sneed[b] >= 0 ? sneed[b] : sheld[b];
-        a.kv[b] = sneed[b] >= 0 ? scached[b] + tfirst[b + 1] - tfirst[b] : 0;
-        a.cu[b] = tfirst[b];
-    }
-    if (t0 == 0) {
-        a.cu[B] = T;
-        *a.free_count_out = (int)min(f + R - A, (long long)a.num_pages);
-    }
-    if (any_bad || dropped) atomicExch(a.status, (int)PI_ERR_INVALID_ARG);
+    if (dropped) atomicExch(a.status, (int)PI_ERR_INVALID_ARG);
 }
 
 // ------------------------------------------------ rotary positions and store
@@ -418,22 +428,31 @@ bool tables_ok(const pi_tables_desc& d) {
            (long long)d.max_pages * d.page_size <= (1ll << 30) && d.max_tokens >= 0 && d.max_tokens <= (1 << 24);
 }
 
-// The shared memory of the largest batch, allowed once per device.
-bool tables_smem_allowed(size_t bytes) {
+size_t tables_smem(int B) { return 16 * (size_t)(B + 1) + 4 * (size_t)(B + 1) + 12 * (size_t)B; }
+
+// One part of a step on `blocks` blocks; the shared memory of the largest
+// batch is allowed once per device.
+template <int PART>
+cudaError_t launch_tables(const TablesArgs& a, int blocks, cudaStream_t s) {
     static std::mutex mu;
     static bool done[64] = {};
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
-    std::lock_guard<std::mutex> lk(mu);
-    if (!done[dev]) {
-        if (cudaFuncSetAttribute(k_block_tables, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
-            return false;
-        done[dev] = true;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        if (!done[dev]) {
+            e = cudaFuncSetAttribute(k_block_tables<PART>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)tables_smem(kTabMaxRows));
+            if (e != cudaSuccess) return e;
+            done[dev] = true;
+        }
     }
-    return true;
+    return launch_pdl(k_block_tables<PART>, blocks, kTabThreads, tables_smem(a.B), s, a);
 }
 
-size_t tables_smem(int B) { return 16 * (size_t)(B + 1) + 4 * (size_t)(B + 1) + 12 * (size_t)B; }
+int page_shift(int page_size) { return page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7; }
 
 }  // namespace
 
@@ -466,26 +485,21 @@ pi_status pi_block_tables(const pi_tables_desc* desc, const int32_t* cached_len,
                           (const void*)positions})
         if (!aligned(p, 4)) return PI_ERR_INVALID_ARG;
     if (!aligned(slots, 8)) return PI_ERR_INVALID_ARG;
-    TablesArgs a{cached_len,     new_len, held,   held_out, block_table, free_list,      free_count,
-                 free_count_out, cu_new,  kv_len, slots,    positions,   desc->batch,    desc->page_size,
+    TablesArgs a{cached_len,     new_len, held,   held_out, block_table, free_list,   free_count,
+                 free_count_out, cu_new,  kv_len, slots,    positions,   desc->batch, page_shift(desc->page_size),
                  desc->num_pages, desc->max_pages, desc->max_tokens, status_word()};
-    if (a.status == nullptr || !tables_smem_allowed(tables_smem(kTabMaxRows))) return PI_ERR_CUDA;
-    // one block where its threads have a write or two each, else a cluster
-    const int blocks = desc->max_tokens + desc->batch <= 2 * kTabThreads ? 1 : kTabCluster;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(kTabThreads);
-    cfg.dynamicSmemBytes = tables_smem(desc->batch);
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)blocks;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, k_block_tables, a) == cudaSuccess ? PI_OK : PI_ERR_CUDA;
+    if (a.status == nullptr) return PI_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // writes to expect: a token each, and some tens of moved pages a row
+    const long long writes = desc->max_tokens + 32ll * desc->batch;
+    cudaError_t e;
+    if (writes <= 4 * kTabThreads) {
+        e = launch_tables<kTabAll>(a, 1, s);
+    } else {
+        e = launch_tables<kTabMoves>(a, (int)std::min<long long>(128, (writes + kTabThreads - 1) / kTabThreads), s);
+        if (e == cudaSuccess) e = launch_tables<kTabState>(a, 1, s);
+    }
+    return e == cudaSuccess ? PI_OK : PI_ERR_CUDA;
 }
 
 pi_status pi_rope_plan_init(const pi_rope_desc* desc, pi_rope_plan* plan) {
@@ -578,7 +592,7 @@ pi_status pi_rope_store(const pi_rope_plan* plan, const pi_page_desc* cache, con
     a.heads = has_q ? d.heads : 0;
     a.kv_heads = has_kv ? cache->kv_heads : 0;
     a.dh = cache->head_dim;
-    a.page_shift = cache->page_size == 16 ? 4 : cache->page_size == 32 ? 5 : cache->page_size == 64 ? 6 : 7;
+    a.page_shift = page_shift(cache->page_size);
     a.units = (a.heads + 2 * a.kv_heads) * (a.dh / 16);
     a.status = status_word();
     a.plan = *plan;

@@ -1,9 +1,9 @@
 // pi_paged_attn.cu -- causal attention of new tokens over a paged cache.
 //
-// A request's new tokens and the query heads that share a KV head form rows
-// (row = token * group + head in the group), so one pass over the keys serves
-// the whole group.  An item is up to 256 rows of one request and KV head; its
-// keys come in tiles of 128.  For a tile, on the tcgen05 tensor cores,
+// The query heads that share a KV head go through its keys together: a tile of
+// rows is as many whole tokens as fit 128 rows (row = token * group + head in
+// the group), so one pass over the keys serves the whole group.  An item is up
+// to two such tiles of one request and KV head; its keys come in tiles of 128.  For a tile, on the tcgen05 tensor cores,
 //     S = Q K^T         (fp16/bf16 products, fp32 sums in tensor memory)
 //     P = 2^(c S - m)   (a thread per row; running m and l = sum P)
 //     O += P V          (P as the A operand in tensor memory)
@@ -13,11 +13,12 @@
 // weights are then 2^7 .. 2^15, within fp16, and weights down to 2^-31 of the
 // largest survive the rounding.
 //
-// Warps: 0-3 and 4-7 softmax (a thread per row), 8 TMA, 9 MMA issue, 10 query
-// rows, 11 the work list.  Items of more than 128 rows give each softmax group
-// 128 of them (both use every key tile: "pair"); smaller items, decode steps
-// among them, give the two groups alternate key tiles and merge at the end, so
-// that one group's exponentials run beside the other's products.
+// Warps: 0-3 and 4-7 softmax (a thread per row), 8 key and value copies, 9 MMA
+// issue, 10 query copies, 11 the work list.  Items of two
+// tiles of rows give each softmax group one (both use every key tile: "pair");
+// smaller items, decode steps among them, give the two groups alternate key
+// tiles and merge at the end: one group's exponentials run beside the other's
+// products.
 //
 // Work split: the (item x key tile) space is cut into equal contiguous ranges
 // per block, whatever the lengths; an item cut by a border leaves unnormalised
@@ -44,10 +45,11 @@ namespace {
 using namespace pipe;
 
 constexpr int kKeys = 128;             // keys of a tile
-constexpr int kRows = 256;             // rows of an item at most
+constexpr int kTileRows = 128;         // rows of a tile at most
 constexpr int kPagedThreads = 384;
 constexpr int kListDepth = 4;          // pieces the work list runs ahead
 constexpr int kConsumers = 11;         // warps that read the work list
+constexpr int kItemCost = 2;           // an item's fixed cost, in key tiles
 constexpr float kLift = 7.f;           // log2 of the factor that P, l and O share
 constexpr float kSlack = 8.f;          // growth (log2) of a maximum before m follows
 constexpr float kLn2 = 0.69314718055994531f;
@@ -56,7 +58,8 @@ template <int DH>
 struct PagedCfg {
     static constexpr int HALVES = DH / 64;               // 64-element column blocks of a row
     static constexpr int TILE = kKeys * DH * 2;          // bytes of a key or value tile
-    static constexpr int Q = kRows * DH * 2;
+    static constexpr int QTILE = kTileRows * DH * 2;
+    static constexpr int Q = 2 * QTILE;
     static constexpr int S = DH == 128 ? 5 : 12;         // ring slots
     static constexpr int MISC = 3072;
     static constexpr int SMEM = Q + S * TILE + MISC;
@@ -66,6 +69,7 @@ struct PagedCfg {
 
 struct PagedArgs {
     CUtensorMap kmap, vmap;   // {dh, position, head, page}, box 64 x page_size
+    CUtensorMap qmap;         // {dh, head, token}, box 64 x group x tile_tokens
     const void *q, *k, *v;
     const int32_t *table, *cu, *kv;
     void* out;
@@ -73,6 +77,7 @@ struct PagedArgs {
     long long q_stride, o_stride, page_stride, head_stride, token_stride;
     int heads, kv_heads, batch, max_tokens, max_new, max_pages, window, page_size, num_pages;
     int group;                // query heads per KV head
+    int tile_tokens;          // tokens of a tile, 128 / group
     int part_rows;            // rows of a partial
     float scale;
     int* counters;            // [blocks][8] arrivals at a cut item
@@ -88,7 +93,7 @@ struct Piece {
     int j0;          // first key tile
     int lo, hi;      // keys that some row of the item sees: lo <= t < hi
     int b, g;        // request, KV head
-    int row0, rows;  // rows of the request's (token, head in group) rows
+    int tok0, toks;  // tokens of the request
     int first;       // position of the request's first new token (negative: it sees nothing)
     int cu;          // the request's first row of q and out
     int block0;      // first block that holds a part of the item
@@ -97,26 +102,27 @@ struct Piece {
     int pad[3];
 };
 
+struct Request {
+    int cu, n, first;   // first row of q, tokens, position of the first token
+};
+
 template <int DH>
 struct PagedShared {
     unsigned long long full[12], empty[12], qfull, qempty, sfull[2], pready[2], odone[2], lfull[kListDepth],
         lempty[kListDepth], merge[2], merged, drain;
     Piece list[kListDepth];
     float ml[2][kKeys][2];
+    Request start_r;
     long long start_u;   // this block's first unit, and where it is
-    int start_b, start_g, start_row0, start_off;
+    int start_b, start_g, start_tok0, start_off;
     unsigned tmem;
     int abort_flag;
-};
-
-struct Request {
-    int cu, n, first, rows;
 };
 
 PI_DEV Request request(const PagedArgs& a, int b, bool* bad) {
     const int lo = a.cu[b], hi = a.cu[b + 1];
     int kv = a.kv[b];
-    Request r{lo, hi - lo, 0, 0};
+    Request r{lo, hi - lo, 0};
     if (lo < 0 || hi < lo || hi > a.max_tokens || hi - lo > a.max_new) {
         *bad = true;
         r.n = 0;
@@ -126,17 +132,15 @@ PI_DEV Request request(const PagedArgs& a, int b, bool* bad) {
         kv = 0;
     }
     r.first = kv - r.n;
-    r.rows = r.n * a.group;
     return r;
 }
 
-// Keys that rows row0 .. row0 + rows - 1 of a request see, as key tiles (one
-// tile, with nothing to see in it, where they see none: it writes the zeros).
-PI_DEV int item_tiles(const PagedArgs& a, const Request& r, int row0, int* rows, int* lo, int* hi) {
-    *rows = min(kRows, r.rows - row0);
-    const int t0 = row0 / a.group, t1 = (row0 + *rows - 1) / a.group;
-    *hi = r.first + t1 + 1;
-    *lo = a.window > 0 ? max(0, r.first + t0 - a.window + 1) : 0;
+// Keys that an item's tokens (from tok0 on) see, as key tiles (one tile, with
+// nothing to see in it, where they see none: it writes the zeros).
+PI_DEV int item_tiles(const PagedArgs& a, const Request& r, int tok0, int* toks, int* lo, int* hi) {
+    *toks = min(2 * a.tile_tokens, r.n - tok0);
+    *hi = r.first + tok0 + *toks;
+    *lo = a.window > 0 ? max(0, r.first + tok0 - a.window + 1) : 0;
     if (*hi <= *lo) {
         *lo = *hi = 0;
         return 1;
@@ -144,10 +148,12 @@ PI_DEV int item_tiles(const PagedArgs& a, const Request& r, int row0, int* rows,
     return (*hi + kKeys - 1) / kKeys - *lo / kKeys;
 }
 
-PI_DEV long long request_units(const PagedArgs& a, const Request& r) {   // of one KV head
+// Cost of one KV head of a request, in key tiles: the items' tiles and
+// kItemCost for what an item costs besides them.
+PI_DEV long long request_units(const PagedArgs& a, const Request& r) {
     long long u = 0;
-    int rows, lo, hi;
-    for (int row0 = 0; row0 < r.rows; row0 += kRows) u += item_tiles(a, r, row0, &rows, &lo, &hi);
+    int toks, lo, hi;
+    for (int t = 0; t < r.n; t += 2 * a.tile_tokens) u += kItemCost + item_tiles(a, r, t, &toks, &lo, &hi);
     return u;
 }
 
@@ -159,6 +165,11 @@ PI_DEV float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+PI_DEV float max3(float x, float y, float z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
 }
 PI_DEV float to_f(__half v) { return __half2float(v); }
 PI_DEV float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -229,58 +240,66 @@ __device__ __noinline__ void careful_row(const PagedArgs& a, int b, int g, long 
 }
 
 // ------------------------------------------------------------ work list (warp 11)
+//
+// Units u of the block's range run through the items; an item's first
+// kItemCost units hold no tile, the next nt one each.
 template <int DH>
-PI_DEV void list_role(const PagedArgs& a, PagedShared<DH>& sh, long long u1, long long U, int G, const Ctl& ctl) {
-    int b = sh.start_b, g = sh.start_g, row0 = sh.start_row0, off = sh.start_off;
+PI_DEV void list_role(const PagedArgs& a, PagedShared<DH>& sh, Request r, long long u1, long long U, int G,
+                      const Ctl& ctl) {
+    int b = sh.start_b, g = sh.start_g, tok0 = sh.start_tok0, off = sh.start_off;
     long long u = sh.start_u;
     bool bad = false;
-    Request r = request(a, b, &bad);
     int n = 0;
-    for (;; ++n) {
-        const int s = n % kListDepth;
-        if (n >= kListDepth && !bar_wait(&sh.lempty[s], (n / kListDepth - 1) & 1, ctl)) return;
+    for (;;) {
         Piece p{};
-        if (u < u1) {
-            int rows, lo, hi;
-            const int nt = item_tiles(a, r, row0, &rows, &lo, &hi);
-            p.nt = (int)min((long long)(nt - off), u1 - u);
-            p.j0 = lo / kKeys + off;
+        bool end = u >= u1;
+        if (!end) {
+            int toks, lo, hi;
+            const int nt = item_tiles(a, r, tok0, &toks, &lo, &hi);
+            const long long i0 = u - off;   // the item's first unit
+            const int stop = (int)min((long long)(kItemCost + nt), u1 - i0);
+            const int from = max(off - kItemCost, 0), to = max(stop - kItemCost, 0);
+            p.nt = to - from;
+            p.j0 = lo / kKeys + from;
             p.lo = lo;
             p.hi = hi;
             p.b = b;
             p.g = g;
-            p.row0 = row0;
-            p.rows = rows;
+            p.tok0 = tok0;
+            p.toks = toks;
             p.first = r.first;
             p.cu = r.cu;
             p.parts = 1;
-            p.own = off == 0;
-            if (p.nt != nt) {
-                const long long i0 = u - off;   // the item's first unit, and the blocks that own its ends
-                p.block0 = (int)(((i0 + 1) * G - 1) / U);
-                p.parts = (int)(((i0 + nt) * G - 1) / U) - p.block0 + 1;
+            p.own = from == 0;
+            if (p.nt != nt) {   // blocks that own its first and its last tile
+                p.block0 = (int)(((i0 + kItemCost + 1) * G - 1) / U);
+                p.parts = (int)(((i0 + kItemCost + nt) * G - 1) / U) - p.block0 + 1;
             }
-            u += p.nt;
+            u = i0 + stop;
             off = 0;
-            row0 += kRows;
-            if (u < u1 && row0 >= r.rows) {
-                row0 = 0;
+            tok0 += 2 * a.tile_tokens;
+            if (u < u1 && tok0 >= r.n) {
+                tok0 = 0;
                 if (++g == a.kv_heads) {
                     g = 0;
-                    // u < u1 <= U: a later request has rows
+                    // u < u1 <= U: a later request has tokens
                     do {
                         if (++b >= a.batch) {   // the lengths changed under the kernel: stop
                             u = u1;
                             break;
                         }
                         r = request(a, b, &bad);
-                    } while (r.rows == 0);
+                    } while (r.n == 0);
                 }
             }
+            if (p.nt == 0) continue;   // only the item's cost falls into this block
         }
+        const int s = n % kListDepth;
+        if (n >= kListDepth && !bar_wait(&sh.lempty[s], (n / kListDepth - 1) & 1, ctl)) return;
         sh.list[s] = p;
         bar_arrive(&sh.lfull[s]);
-        if (p.nt == 0) return;
+        ++n;
+        if (end) return;
     }
 }
 
@@ -355,85 +374,91 @@ PI_DEV void tile_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* ri
     }
 }
 
-// ------------------------------------------------------------ query rows (warp 10)
+// ------------------------------------------------------------ queries (warp 10)
 //
-// Rows of the item in the MMA's K-major layout (128 bytes per row and column
-// block, 16-byte chunk c of row r at c ^ (r % 8)); rows past the item's stay
-// as they are: a row of S depends on its own query alone.
-template <typename T, int DH>
+// The item's query tiles; tokens past the request's end or the last row come
+// along or read as zeros: a row of S depends on its own query alone.
+template <int DH>
 PI_DEV void query_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* qs, const Ctl& ctl) {
-    constexpr int CH = DH / 8, STEP = 32 / CH;   // 16-byte chunks of a row; rows per step
-    const int lane = threadIdx.x & 31;
-    const int c = lane % CH;
-    for (int n = 0;; ++n) {
+    using C = PagedCfg<DH>;
+    int n = 0;
+    for (;; ++n) {
         const Piece p = next_piece<DH>(sh, n, ctl);
-        if (p.nt == 0) return;
-        if (n >= 1 && !warp_wait(&sh.qempty, (n - 1) & 1, ctl)) return;
-        int tok = (p.row0 + lane / CH) / a.group, h = (p.row0 + lane / CH) % a.group;
-        for (int r = lane / CH; r < p.rows; r += STEP) {
-            const T* src = static_cast<const T*>(a.q) + (long long)(p.cu + tok) * a.q_stride +
-                           (long long)(p.g * a.group + h) * DH + 8 * c;
-            cp16(qs + (r >> 7) * (kKeys * DH * 2) + (c >> 3) * (kKeys * 128) + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4),
-                 src);
-            for (h += STEP; h >= a.group; h -= a.group) ++tok;
+        if (p.nt == 0) break;
+        if (n >= 1 && !warp_wait(&sh.qempty, (n - 1) & 1, ctl)) break;
+        if ((threadIdx.x & 31) == 0) {
+            const int tiles = p.toks > a.tile_tokens ? 2 : 1;
+            bar_arrive_expect_tx(&sh.qfull, (unsigned)(tiles * C::HALVES * a.tile_tokens * a.group) * 128u);
+            for (int w = 0; w < tiles; ++w)
+                for (int h = 0; h < C::HALVES; ++h)
+                    tma_load_3d(qs + w * C::QTILE + h * (kTileRows * 128), &a.qmap, 64 * h, p.g * a.group,
+                                p.cu + p.tok0 + w * a.tile_tokens, &sh.qfull);
         }
-        cp_commit();
-        cp_wait_all();
-        fence_async_smem();
-        warp_arrive(&sh.qfull);
+        __syncwarp();
     }
+    // the last copy has landed before the block may exit
+    if (n > 0) bar_drain(&sh.qfull, (n - 1) & 1, kDrainTimeoutNs);
 }
 
 // ------------------------------------------------------------ products (warp 9)
+//
+// The tensor core takes four or so MMAs ahead of the one it runs, so this warp
+// has about 250 cycles from the last MMA of one product to the first of the
+// next: its waits are for things that are there already.
 template <typename T, int DH>
 PI_DEV void mma_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* qs, unsigned char* ring, unsigned tmem,
                      const Ctl& ctl) {
     using C = PagedCfg<DH>;
-    const int lane = threadIdx.x & 31;
     constexpr unsigned kType = std::is_same<T, __half>::value ? 0u : (1u << 7) | (1u << 10);   // A and B: fp16 or bf16
     const unsigned id_s = idesc_f16(128, kKeys, false) | kType;
     const unsigned id_o = idesc_f16(128, DH, false) | kType | (1u << 16);   // B (values) MN-major
-    int it = 0;               // next ring slot to use
-    int np[2] = {0, 0};       // products P V asked of each softmax group
+    const uint64_t qd = sdesc_sw128(su32(qs)), kd = sdesc_sw128(su32(ring)),
+                   vd = sdesc_sw128_mn(su32(ring), kKeys * 128, 1024);
+    int slot = 0, phase = 0;        // ring slot to use next, and the phase of its copies
+    int np0 = 0, np1 = 0;           // products P V asked of each group
     bool ok = true;
-    auto slot = [&](int i) { return su32(ring) + (unsigned)((i % C::S) * C::TILE); };
-    auto wait_full = [&](int i) {
-        const bool r = warp_wait(&sh.full[i % C::S], (i / C::S) & 1, ctl);
+    // S_w = Q_qw K^T
+    auto scores = [&](int w, int qw, int i) {
+#pragma unroll
+        for (int kk = 0; kk < DH / 16; ++kk) {
+            const unsigned o = (unsigned)((kk >> 2) * (kKeys * 128) + (kk & 3) * 32) >> 4;
+            mma_f16_warp(tmem + (unsigned)(w * kKeys), qd + (uint64_t)(qw * (C::QTILE >> 4) + o),
+                         kd + (uint64_t)(i * (C::TILE >> 4) + o), id_s, kk > 0 ? 1u : 0u);
+        }
+        mma_commit_warp(&sh.sfull[w]);
+    };
+    // O_w (+)= P_w V
+    auto values = [&](int w, int i, bool add) {
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+            mma_f16_ta_warp(tmem + C::O_COL + (unsigned)(w * DH), tmem + (unsigned)(w * kKeys + kk * 8),
+                            vd + (uint64_t)(i * (C::TILE >> 4) + kk * 128), id_o, (add || kk > 0) ? 1u : 0u);
+        mma_commit_warp(&sh.odone[w]);
+    };
+    auto copied = [&](int i, int ph) { return warp_wait(&sh.full[i], ph, ctl); };
+    auto advance = [&]() {
+        if (++slot == C::S) {
+            slot = 0;
+            phase ^= 1;
+        }
+    };
+    auto weights = [&](int w) {
+        int& np = w ? np1 : np0;
+        const bool r = warp_wait(&sh.pready[w], np & 1, ctl);
+        ++np;
         tc_after();
         return r;
     };
-    auto scores = [&](int w, int qw, int i) {   // S_w = Q_qw K^T of slot i
-        if (lane == 0) {
-#pragma unroll
-            for (int kk = 0; kk < DH / 16; ++kk) {
-                const unsigned o = (unsigned)((kk >> 2) * (kKeys * 128) + (kk & 3) * 32);
-                mma_f16(tmem + (unsigned)(w * kKeys), sdesc_sw128(su32(qs) + (unsigned)(qw * kKeys * DH * 2) + o),
-                        sdesc_sw128(slot(i) + o), id_s, kk > 0 ? 1u : 0u);
-            }
-            mma_commit(&sh.sfull[w]);
-        }
-    };
-    auto values = [&](int w, int i, bool add) {   // O_w (+)= P_w V of slot i
-        if (lane == 0) {
-#pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk)
-                mma_f16_ta(tmem + C::O_COL + (unsigned)(w * DH), tmem + (unsigned)(w * kKeys + kk * 8),
-                           sdesc_sw128_mn(slot(i) + (unsigned)(kk * 2048), kKeys * 128, 1024), id_o,
-                           (add || kk > 0) ? 1u : 0u);
-            mma_commit(&sh.odone[w]);
-        }
-    };
-    auto release = [&](unsigned long long* bar) {
-        if (lane == 0) mma_commit(bar);
-    };
-    // value rows outside the keys the item sees: zeros, not what the cache or the slot holds there
+    // value rows outside the keys the item sees (in an item's first and last
+    // tile): zeros, not what the cache or the slot holds there, since 0 x NaN
+    // would reach every row
     auto clear = [&](const Piece& p, int t, int i) {
         const int base = (p.j0 + t) * kKeys;
+        if (base >= p.lo && base + kKeys <= p.hi) return;
         const int z = min(max(p.lo - base, 0), kKeys), e = min(max(p.hi - base, z), kKeys);
-        if (z == 0 && e == kKeys) return;
-        unsigned char* v = ring + (size_t)(i % C::S) * C::TILE;
+        unsigned char* v = ring + (size_t)i * C::TILE;
         const int dead = kKeys - (e - z);
-        for (int x = lane; x < dead * (DH / 8); x += 32) {
+        for (int x = threadIdx.x & 31; x < dead * (DH / 8); x += 32) {
             const int d = x / (DH / 8), c = x % (DH / 8);
             const int r = d < z ? d : d + (e - z);
             *reinterpret_cast<uint4*>(v + (c >> 3) * (kKeys * 128) + r * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -441,76 +466,161 @@ PI_DEV void mma_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* qs,
         fence_async_smem();
         __syncwarp();
     };
-    auto wait_p = [&](int w) {
-        const bool r = warp_wait(&sh.pready[w], np[w] & 1, ctl);
-        ++np[w];
-        tc_after();
-        return r;
-    };
     for (int n = 0; ok; ++n) {
         const Piece p = next_piece<DH>(sh, n, ctl);
         if (p.nt == 0) break;
-        ok = warp_wait(&sh.qfull, n & 1, ctl) && wait_full(it);
-        if (!ok) break;
-        if (p.rows > kKeys) {   // pair: both groups use every tile
-            scores(0, 0, it);
-            scores(1, 1, it);
-            release(&sh.empty[it % C::S]);
-            if (p.nt == 1) release(&sh.qempty);
-            ++it;
-            for (int t = 0; t < p.nt && ok; ++t) {
-                const bool more = t + 1 < p.nt;
-                const int ik = it, iv = more ? it + 1 : it;
-                ok = (!more || wait_full(ik)) && wait_full(iv);
-                if (!ok) break;
-                clear(p, t, iv);
-                for (int w = 0; w < 2; ++w) {
-                    if (!(ok = wait_p(w))) break;
-                    values(w, iv, t > 0);
-                    if (more) scores(w, w, ik);
+        const int nt = __shfl_sync(FULL, p.nt, 0);
+        if (!(ok = warp_wait(&sh.qfull, n & 1, ctl) && copied(slot, phase))) break;
+        if (p.toks > a.tile_tokens) {   // pair: both groups use every tile
+            scores(0, 0, slot);
+            scores(1, 1, slot);
+            mma_commit_warp(&sh.empty[slot]);
+            if (nt == 1) mma_commit_warp(&sh.qempty);
+            advance();
+            for (int t = 0; t < nt; ++t) {
+                const bool more = t + 1 < nt;
+                const int ik = slot;
+                if (more) {
+                    if (!(ok = copied(slot, phase))) break;
+                    advance();
                 }
-                if (!ok) break;
-                if (more) release(&sh.empty[ik % C::S]);
-                release(&sh.empty[iv % C::S]);
-                if (t + 2 == p.nt) release(&sh.qempty);
-                it = iv + 1;
+                const int iv = slot;
+                if (!(ok = copied(slot, phase))) break;
+                clear(p, t, iv);
+                advance();
+                if (!(ok = weights(0))) break;
+                values(0, iv, t > 0);
+                if (more) scores(0, 0, ik);
+                if (!(ok = weights(1))) break;
+                values(1, iv, t > 0);
+                if (more) {
+                    scores(1, 1, ik);
+                    mma_commit_warp(&sh.empty[ik]);
+                }
+                mma_commit_warp(&sh.empty[iv]);
+                if (t + 2 == nt) mma_commit_warp(&sh.qempty);
             }
-        } else {                // the groups take alternate tiles
-            scores(0, 0, it);
-            release(&sh.empty[it % C::S]);
-            ++it;
-            if (p.nt > 1) {
-                if (!(ok = wait_full(it))) break;
-                scores(1, 0, it);
-                release(&sh.empty[it % C::S]);
-                ++it;
+        } else {                        // the groups take alternate tiles
+            scores(0, 0, slot);
+            mma_commit_warp(&sh.empty[slot]);
+            advance();
+            if (nt > 1) {
+                if (!(ok = copied(slot, phase))) break;
+                scores(1, 0, slot);
+                mma_commit_warp(&sh.empty[slot]);
+                advance();
             }
-            if (p.nt <= 2) release(&sh.qempty);
-            for (int t = 0; t < p.nt && ok; ++t) {
+            if (nt <= 2) mma_commit_warp(&sh.qempty);
+            for (int t = 0; t < nt; ++t) {
                 const int w = t & 1;
-                ok = wait_full(it);
-                if (!ok) break;
-                clear(p, t, it);
-                if (!(ok = wait_p(w))) break;
-                values(w, it, t > 1);
-                release(&sh.empty[it % C::S]);
-                ++it;
-                if (t + 2 < p.nt) {
-                    if (!(ok = wait_full(it))) break;
-                    scores(w, 0, it);
-                    release(&sh.empty[it % C::S]);
-                    ++it;
-                    if (t + 3 == p.nt) release(&sh.qempty);
+                if (!(ok = copied(slot, phase))) break;
+                clear(p, t, slot);
+                if (!(ok = weights(w))) break;
+                values(w, slot, t > 1);
+                mma_commit_warp(&sh.empty[slot]);
+                advance();
+                if (t + 2 < nt) {
+                    if (!(ok = copied(slot, phase))) break;
+                    scores(w, 0, slot);
+                    mma_commit_warp(&sh.empty[slot]);
+                    advance();
+                    if (t + 3 == nt) mma_commit_warp(&sh.qempty);
                 }
             }
         }
     }
     // every product has completed before the block may exit
-    if (lane == 0) {
-        mma_commit(&sh.drain);
-        bar_drain(&sh.drain, 0, kDrainTimeoutNs);
-    }
     __syncwarp();
+    mma_commit_warp(&sh.drain);
+    bar_drain(&sh.drain, 0, kDrainTimeoutNs);
+}
+
+PI_DEV int arrive_gpu(int* p) {
+    int old;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(old) : "l"(p) : "memory");
+    return old;
+}
+
+// Adds the parts of rows r0 .. r0 + rows - 1 (at most 32) of an item's tile,
+// whose first token is tok0, columns c0 .. c0 + cols - 1, in block order and
+// writes the outputs: one warp, once all parts have arrived.  A lane keeps one row and every (32 / rows)-th group of 4 columns,
+// so that a few rows still use the whole warp, and asks for eight 16-byte
+// values at a time (the L2 latency is what a join costs).
+template <typename T, int DH>
+PI_DEV void join_parts(const PagedArgs& a, const Piece& p, bool pair, int w, int r0, int rows, int tok0, int c0, int cols) {
+    const int lane = threadIdx.x & 31;
+    const int span = rows > 16 ? 32 : rows > 8 ? 16 : rows > 4 ? 8 : rows > 2 ? 4 : rows;   // power of two
+    const int tr = r0 + (lane & (span - 1));   // row of the tile
+    const int cg = lane / span, step = 32 / span;
+    if ((lane & (span - 1)) >= rows) return;
+    const int r = (pair ? w * kTileRows : 0) + tr;
+    const size_t ml_step = (size_t)2 * 2 * a.part_rows, o_step = (size_t)2 * DH / 4 * a.part_rows;
+    // partial of block block0 + k: its second slot (k = 0, where the item starts) or its first
+    const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + (size_t)p.block0 * ml_step +
+                       (size_t)(pair ? 0 : w) * a.part_rows + r;
+    const float4* po = reinterpret_cast<const float4*>(a.part_o) + (size_t)p.block0 * o_step + r;
+    const size_t ml_first = (size_t)2 * a.part_rows, o_first = (size_t)DH / 4 * a.part_rows;
+    float M = -INFINITY, L = 0.f;
+    for (int k0 = 0; k0 < p.parts; k0 += 8) {
+        float2 x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int k = k0 + i;
+            x[i] = k < p.parts ? __ldcg(ml + k * ml_step + (k == 0 ? ml_first : 0)) : make_float2(-INFINITY, 0.f);
+        }
+        float top = M;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, x[i].x);
+        const float use = top == -INFINITY ? 0.f : top;
+        L *= ex2(M - use);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) L = fmaf(x[i].y, ex2(x[i].x - use), L);
+        M = top;
+    }
+    const float use = M == -INFINITY ? 0.f : M;
+    const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+    const int tok = tr / a.group, head = p.g * a.group + tr - tok * a.group;
+    const long long orow = p.cu + tok0 + tok;
+    T* dst = static_cast<T*>(a.out) + orow * a.o_stride + (long long)head * DH;
+    const int end = (c0 + cols) / 4;
+    for (int c = c0 / 4 + cg; c < end; c += 4 * step) {
+        float4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = 0; k0 < p.parts; k0 += 2) {
+            float f[2];
+            float4 x[2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int k = k0 + i;
+                const bool in = k < p.parts;
+                f[i] = in ? __ldcg(ml + k * ml_step + (k == 0 ? ml_first : 0)).x : -INFINITY;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    x[i][j] = in && c + j * step < end
+                                  ? __ldcg(po + k * o_step + (k == 0 ? o_first : 0) + (size_t)(c + j * step) * a.part_rows)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float g = ex2(f[i] - use);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    v[j].x = fmaf(x[i][j].x, g, v[j].x);
+                    v[j].y = fmaf(x[i][j].y, g, v[j].y);
+                    v[j].z = fmaf(x[i][j].z, g, v[j].z);
+                    v[j].w = fmaf(x[i][j].w, g, v[j].w);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (c + j * step < end)
+                *reinterpret_cast<uint2*>(dst + 4 * (c + j * step)) =
+                    make_uint2(pack2(v[j].x * inv, v[j].y * inv, T()), pack2(v[j].z * inv, v[j].w * inv, T()));
+    }
+    if (a.lse != nullptr && c0 == 0 && cg == 0)
+        a.lse[orow * a.heads + head] = L == 0.f ? -INFINITY : (M - kLift + log2f(L)) * kLn2;
 }
 
 // ------------------------------------------------------------ softmax (warps 0-7)
@@ -534,16 +644,19 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
         const Piece& p = sh.list[n % kListDepth];
         const int nt = p.nt, j0 = p.j0;
         if (nt == 0) return;
-        const bool pair = p.rows > kKeys;
-        const int r = (pair ? w * kKeys : 0) + 32 * quad + lane;   // row of the item
-        const bool live = r < p.rows;
-        int lo, hi;   // keys this row sees
-        {
-            const int pos = p.first + (p.row0 + r) / a.group;
-            hi = live ? max(pos + 1, 0) : 0;
-            lo = live && a.window > 0 ? min(max(0, pos - a.window + 1), hi) : 0;
+        const bool pair = p.toks > a.tile_tokens;
+        const int tok0 = p.tok0 + (pair ? w * a.tile_tokens : 0);              // of this group's tile of rows
+        const int tile_rows = min(a.tile_tokens, p.tok0 + p.toks - tok0) * a.group;
+        const int tr = 32 * quad + lane;                                       // row of the tile
+        const bool live = tr < tile_rows;
+        const bool any = 32 * quad < tile_rows;
+        // keys this row sees (a row of nothing: all, so that it does not ask for masking)
+        int lo = 0, hi = 0x7fffffff;
+        if (live) {
+            const int pos = p.first + tok0 + tr / a.group;
+            hi = max(pos + 1, 0);
+            lo = a.window > 0 ? min(max(0, pos - a.window + 1), hi) : 0;
         }
-        const bool any = __any_sync(FULL, live);
         float m = -INFINITY, l = 0.f;
         int mine = 0;         // tiles of this piece that this group has done
         for (int t = pair ? 0 : w; t < nt; t += pair ? 1 : 2) {
@@ -561,14 +674,50 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
                     for (int i = 0; i < kKeys; ++i)
                         if (base + i < lo || base + i >= hi) s[i] = 0xff800000u;   // -inf
                 }
-                float mx[4];
+                if (mine == 0) {
+                    float mx[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(s[i]);
+                    for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(s[i]);
 #pragma unroll
-                for (int i = 4; i < kKeys; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-                const bool grow = top > m + kSlack || (m == -INFINITY && top > m);
-                if (__any_sync(FULL, grow)) {
+                    for (int i = 4; i < kKeys; i += 8)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mx[k] = i + 4 + k < kKeys
+                                        ? max3(mx[k], __uint_as_float(s[i + k]), __uint_as_float(s[i + 4 + k]))
+                                        : fmaxf(mx[k], __uint_as_float(s[i + k]));
+                    m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                }
+                // the weights with m as it stands, and the maximum beside them; once
+                // more only if some row's has grown past the slack
+                for (;;) {
+                    const float bias = kLift - (m == -INFINITY ? 0.f : m);
+                    const uint64_t bias2 = pair2(bias, bias);
+                    uint64_t sum[2] = {0, 0};
+                    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                    for (int i = 0; i < kKeys; i += 64) {
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int e = 0; e < 64; e += 2) {
+                            const float s0 = __uint_as_float(s[i + e]), s1 = __uint_as_float(s[i + e + 1]);
+                            mx[(e >> 1) & 1] = max3(mx[(e >> 1) & 1], s0, s1);
+                            float x, y;
+                            split2(fma2(pair2(s0, s1), c2, bias2), x, y);
+                            x = ex2(x);
+                            y = ex2(y);
+                            sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair2(x, y));
+                            pk[e >> 1] = pack2(x, y, T());
+                        }
+                        tmem_st32(s_at + (unsigned)(i >> 1), pk);
+                    }
+                    const float top = fmaxf(mx[0], mx[1]) * c;
+                    const bool grow = live && top > m + kSlack;
+                    if (!__any_sync(FULL, grow)) {
+                        float x, y;
+                        split2(add2(sum[0], sum[1]), x, y);
+                        l += x + y;
+                        break;
+                    }
                     const float f = grow ? ex2(m - top) : 1.f;
                     if (grow) m = top;
                     l *= f;
@@ -576,38 +725,19 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
                         // O holds the sums over this group's earlier tiles
                         if (!warp_wait(&sh.odone[w], (ns - 1) & 1, ctl)) return;
                         tc_after();
-#pragma unroll
-                        for (int i = 0; i < DH; i += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(o_at + (unsigned)i, o);
+#pragma unroll 1
+                        for (int i = 0; i < DH; i += 16) {
+                            float o[16];
+                            tmem_ld16(o_at + (unsigned)i, o);
                             tmem_wait_ld();
-                            tmem_loaded<32>(o);
+                            tmem_loaded<16>(o);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tmem_st32(o_at + (unsigned)i, o);
+                            for (int e = 0; e < 16; ++e) o[e] *= f;
+                            tmem_st16(o_at + (unsigned)i, o);
                         }
+                        tmem_wait_st();
                     }
                 }
-                const float bias = kLift - (m == -INFINITY ? 0.f : m);
-                const uint64_t bias2 = pair2(bias, bias);
-                uint64_t sum[2] = {0, 0};
-#pragma unroll
-                for (int i = 0; i < kKeys; i += 64) {
-                    uint32_t pk[32];
-#pragma unroll
-                    for (int e = 0; e < 64; e += 2) {
-                        float x, y;
-                        split2(fma2(pair2(__uint_as_float(s[i + e]), __uint_as_float(s[i + e + 1])), c2, bias2), x, y);
-                        x = ex2(x);
-                        y = ex2(y);
-                        sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair2(x, y));
-                        pk[e >> 1] = pack2(x, y, T());
-                    }
-                    tmem_st32(s_at + (unsigned)(i >> 1), pk);
-                }
-                float x, y;
-                split2(add2(sum[0], sum[1]), x, y);
-                l += x + y;
                 tmem_wait_st();
             }
             tc_before();
@@ -641,7 +771,8 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
             c0 = w * cols;
             ++nm;
         }
-        const int tok = (p.row0 + r) / a.group, h = (p.row0 + r) - tok * a.group;
+        const int r = (pair ? w * kTileRows : 0) + tr;   // row of a partial
+        const int tok = tok0 + tr / a.group, h = tr % a.group;
         const long long orow = (long long)(p.cu + tok);
         const int head = p.g * a.group + h;
         const bool own_any = mine > 0;                  // O_w holds something
@@ -721,58 +852,15 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
             } else {
                 float* ml = a.part_ml + ((size_t)(blk * 2 + (pair ? 0 : w)) * a.part_rows + r) * 2;
                 if (live) *reinterpret_cast<float2*>(ml) = make_float2(m, l);
-                __threadfence();
+                // the lanes' stores happen before lane 0's arrival (__syncwarp, then
+                // release), the other blocks' before what follows it (acquire)
                 __syncwarp();
                 int seen = 0;
-                if (lane == 0) seen = atomicAdd(a.counters + p.block0 * 8 + warp, 1);
+                if (lane == 0) seen = arrive_gpu(a.counters + p.block0 * 8 + warp);
                 seen = __shfl_sync(FULL, seen, 0);
                 if (seen == p.parts - 1) {
-                    // all parts are there: add them in block order
-                    __threadfence();
                     if (lane == 0) a.counters[p.block0 * 8 + warp] = 0;
-                    if (live) {
-                        const size_t ml_step = (size_t)2 * 2 * a.part_rows * 2, o_step = (size_t)2 * DH * a.part_rows;
-                        // partial of block block0 + k: its second slot (k = 0, where the item starts) or its first
-                        auto ml_at = [&](int k) {
-                            return a.part_ml + (size_t)(p.block0 + k) * ml_step +
-                                   ((size_t)((k == 0 ? 2 : 0) + (pair ? 0 : w)) * a.part_rows + r) * 2;
-                        };
-                        float M = -INFINITY, L = 0.f;
-                        for (int k = 0; k < p.parts; ++k) M = fmaxf(M, __ldcg(ml_at(k)));
-                        const float use = M == -INFINITY ? 0.f : M;
-                        for (int k = 0; k < p.parts; ++k) {
-                            const float2 x = __ldcg(reinterpret_cast<const float2*>(ml_at(k)));
-                            L = fmaf(x.y, ex2(x.x - use), L);
-                        }
-                        inv = L > 0.f || L != L ? 1.f / L : 0.f;
-                        T* dst = static_cast<T*>(a.out) + orow * a.o_stride + (long long)head * DH;
-                        for (int i = c0; i < c0 + cols; i += 16) {
-                            float v[16];
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) v[e] = 0.f;
-                            for (int k = 0; k < p.parts; ++k) {
-                                const float f = ex2(__ldcg(ml_at(k)) - use);
-                                const float* src = a.part_o + (size_t)(p.block0 + k) * o_step +
-                                                   (k == 0 ? (size_t)DH * a.part_rows : 0);
-#pragma unroll
-                                for (int e = 0; e < 16; e += 4) {
-                                    const float4 x = __ldcg(
-                                        reinterpret_cast<const float4*>(src + ((size_t)((i + e) / 4) * a.part_rows + r) * 4));
-                                    v[e] = fmaf(x.x, f, v[e]);
-                                    v[e + 1] = fmaf(x.y, f, v[e + 1]);
-                                    v[e + 2] = fmaf(x.z, f, v[e + 2]);
-                                    v[e + 3] = fmaf(x.w, f, v[e + 3]);
-                                }
-                            }
-#pragma unroll
-                            for (int e = 0; e < 16; e += 8)
-                                *reinterpret_cast<uint4*>(dst + i + e) = make_uint4(
-                                    pack2(v[e] * inv, v[e + 1] * inv, T()), pack2(v[e + 2] * inv, v[e + 3] * inv, T()),
-                                    pack2(v[e + 4] * inv, v[e + 5] * inv, T()), pack2(v[e + 6] * inv, v[e + 7] * inv, T()));
-                        }
-                        if (a.lse != nullptr && c0 == 0)
-                            a.lse[orow * a.heads + head] = L == 0.f ? -INFINITY : (M - kLift + log2f(L)) * kLn2;
-                    }
+                    join_parts<T, DH>(a, p, pair, w, 32 * quad, min(32, tile_rows - 32 * quad), tok0, c0, cols);
                 }
             }
         }
@@ -829,7 +917,12 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_paged_attn(const __grid_co
     }
     if (tid == 0) {   // no work, unless a thread finds this block's start below
         sh.start_u = 0x7fffffffffffffffll;
-        sh.start_b = sh.start_g = sh.start_row0 = sh.start_off = 0;
+        sh.start_b = sh.start_g = sh.start_tok0 = sh.start_off = 0;
+    }
+    if (warp == 8 && lane == 0) {
+        tma_prefetch_map(&a.kmap);
+        tma_prefetch_map(&a.vmap);
+        tma_prefetch_map(&a.qmap);
     }
     // units of all requests: each thread sums a run of them, then a prefix over
     // the threads (scratch in the ring, which nothing uses yet)
@@ -857,7 +950,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_paged_attn(const __grid_co
     }
     pre += before - own;   // units before this thread's requests
     const unsigned tmem = sh.tmem;
-    const int G = (int)min((long long)gridDim.x, U);   // blocks with work
+    // blocks with work: at least two tiles each, one for each softmax group (a
+    // part costs a join, the second tile runs beside the first)
+    const int G = (int)min((long long)gridDim.x, (U + 1) / 2);
     const int blk = blockIdx.x;
     const long long u0 = G > 0 ? U * blk / G : 0, u1 = G > 0 ? U * (blk + 1) / G : 0;
     const bool work = blk < G;
@@ -874,17 +969,18 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_paged_attn(const __grid_co
             }
             const int g = (int)(left / u);
             left -= g * u;
-            int row0 = 0, rows, lo, hi;
-            for (;; row0 += kRows) {
-                const int nt = item_tiles(a, r, row0, &rows, &lo, &hi);
-                if (left < nt) break;
-                left -= nt;
+            int tok0 = 0, toks, lo, hi;
+            for (;; tok0 += 2 * a.tile_tokens) {
+                const int cost = kItemCost + item_tiles(a, r, tok0, &toks, &lo, &hi);
+                if (left < cost) break;
+                left -= cost;
             }
             sh.start_u = u0;
             sh.start_b = b;
             sh.start_g = g;
-            sh.start_row0 = row0;
+            sh.start_tok0 = tok0;
             sh.start_off = (int)left;
+            sh.start_r = r;
             break;
         }
     }
@@ -903,9 +999,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_paged_attn(const __grid_co
             else if (warp == 9)
                 mma_role<T, DH>(a, sh, qs, ring, tmem, ctl);
             else if (warp == 10)
-                query_role<T, DH>(a, sh, qs, ctl);
+                query_role<DH>(a, sh, qs, ctl);
             else if (lane == 0)
-                list_role<DH>(a, sh, u1, U, G, ctl);
+                list_role<DH>(a, sh, sh.start_r, u1, U, G, ctl);
         }
     }
     tc_before();
@@ -938,8 +1034,8 @@ struct PagedLayout {
     size_t ml, o, total;
     int rows;
     PagedLayout(const pi_paged_desc& d, const pi_page_desc& c, int blocks) {
-        const long long need = (long long)d.max_new * (d.heads / c.kv_heads);
-        rows = (int)std::min<long long>(kRows, (need + 31) / 32 * 32);
+        const int group = d.heads / c.kv_heads, tile_tokens = kTileRows / group;
+        rows = d.max_new > tile_tokens ? 2 * kTileRows : (d.max_new * group + 31) / 32 * 32;
         auto up = [](size_t v) { return (v + 255) / 256 * 256; };
         ml = up((size_t)blocks * 8 * sizeof(int));
         o = up(ml + (size_t)blocks * 2 * 2 * rows * 2 * sizeof(float));
@@ -957,6 +1053,18 @@ bool cache_map(CUtensorMap* m, const void* base, const pi_page_desc& c) {
     const cuuint32_t box[4] = {64u, (cuuint32_t)c.page_size, 1u, 1u};
     const cuuint32_t es[4] = {1u, 1u, 1u, 1u};
     return fn(m, c.dtype == PI_T_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+              const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool query_map(CUtensorMap* m, const void* base, const PagedArgs& a, int dh, int dtype) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)dh, (cuuint64_t)a.heads, (cuuint64_t)a.max_tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)dh * 2, (cuuint64_t)a.q_stride * 2};
+    const cuuint32_t box[3] = {64u, (cuuint32_t)a.group, (cuuint32_t)a.tile_tokens};
+    const cuuint32_t es[3] = {1u, 1u, 1u};
+    return fn(m, dtype == PI_T_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
               const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1033,6 +1141,7 @@ pi_status pi_paged_attn(const pi_paged_desc* desc, const pi_page_desc* cache, co
     a.page_size = cache->page_size;
     a.num_pages = cache->num_pages;
     a.group = desc->heads / cache->kv_heads;
+    a.tile_tokens = kTileRows / a.group;
     a.part_rows = lay.rows;
     a.scale = desc->scale > 0.f ? desc->scale : 1.0f / sqrtf((float)cache->head_dim);
     a.counters = reinterpret_cast<int*>(ws);
@@ -1040,7 +1149,8 @@ pi_status pi_paged_attn(const pi_paged_desc* desc, const pi_page_desc* cache, co
     a.part_o = reinterpret_cast<float*>(ws + lay.o);
     a.status = status_word();
     a.timeout_ns = wait_timeout_ns();
-    if (blocks < 1 || a.status == nullptr || !cache_map(&a.kmap, kcache, *cache) || !cache_map(&a.vmap, vcache, *cache))
+    if (blocks < 1 || a.status == nullptr || !cache_map(&a.kmap, kcache, *cache) || !cache_map(&a.vmap, vcache, *cache) ||
+        !query_map(&a.qmap, q, a, cache->head_dim, cache->dtype))
         return PI_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;

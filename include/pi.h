@@ -380,7 +380,7 @@ typedef struct {
  * pages and sets the device status to PI_ERR_INVALID_ARG; its tokens are
  * counted in cu_new up to max_tokens (none where a length is out of range).
  * So does a free count outside 0 .. num_pages (taken as the nearest bound)
- * and a push past num_pages (dropped).  One launch.
+ * and a push past num_pages (dropped).
  */
 PI_API pi_status pi_block_tables(const pi_tables_desc *desc, const int32_t *cached_len, const int32_t *new_len,
                                  const int32_t *held, int32_t *held_out, int32_t *block_table, int32_t *free_list,
