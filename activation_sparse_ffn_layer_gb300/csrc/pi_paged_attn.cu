@@ -8,10 +8,11 @@
 //     P = 2^(c S - m)   (a thread per row; running m and l = sum P)
 //     O += P V          (P as the A operand in tensor memory)
 // where c = scale / ln 2 and m trails the running maximum: it moves only when
-// a row's maximum has grown by more than 2^8 (then O and l are scaled), so O is
-// touched rarely.  P carries a factor 2^7, which l and O share: the largest
-// weights are then 2^7 .. 2^15, within fp16, and weights down to 2^-31 of the
-// largest survive the rounding.
+// the weights taken with it add up to more than 2^15 over 64 keys, which no
+// other row needs to know (then O and l are scaled), so O is touched rarely and
+// no maximum is taken on the way.  P carries a factor 2^7, which l and O share:
+// no weight is above 2^15, within fp16, the largest are 2^7 or more unless a
+// later tile's are, and weights down to 2^-31 of those survive the rounding.
 //
 // Warps: 0-3 and 4-7 softmax (a thread per row), 8 key and value copies, 9 MMA
 // issue, 10 query copies, 11 the work list.  Items of two
@@ -51,7 +52,8 @@ constexpr int kListDepth = 4;          // pieces the work list runs ahead
 constexpr int kConsumers = 11;         // warps that read the work list
 constexpr int kItemCost = 2;           // an item's fixed cost, in key tiles
 constexpr float kLift = 7.f;           // log2 of the factor that P, l and O share
-constexpr float kSlack = 8.f;          // growth (log2) of a maximum before m follows
+constexpr int kHalf = 64;              // keys whose weights are taken and handed over at once
+constexpr float kFull = 32768.f;       // sum of their weights from which m follows the maximum
 constexpr float kLn2 = 0.69314718055994531f;
 
 template <int DH>
@@ -108,7 +110,7 @@ struct Request {
 
 template <int DH>
 struct PagedShared {
-    unsigned long long full[12], empty[12], qfull, qempty, sfull[2], pready[2], odone[2], lfull[kListDepth],
+    unsigned long long full[12], empty[12], qfull, qempty, sfull[2], pready[2][2], odone[2][2], lfull[kListDepth],
         lempty[kListDepth], merge[2], merged, drain;
     Piece list[kListDepth];
     float ml[2][kKeys][2];
@@ -158,6 +160,7 @@ PI_DEV long long request_units(const PagedArgs& a, const Request& r) {
 }
 
 PI_DEV bool warp_wait(unsigned long long* b, unsigned parity, const Ctl& c) {
+    if (__all_sync(FULL, bar_test(b, parity))) return true;
     return __all_sync(FULL, bar_wait(b, parity, c));
 }
 
@@ -170,6 +173,19 @@ PI_DEV float max3(float x, float y, float z) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
     return r;
+}
+// the lowest n bits (none below 0, all from 32 on)
+PI_DEV uint32_t low_bits(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
+template <int N>
+PI_DEV float largest(const uint32_t* s) {
+    float m[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m[k] = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < N; i += 8)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m[k] = max3(m[k], __uint_as_float(s[i + k]), __uint_as_float(s[i + 4 + k]));
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 PI_DEV float to_f(__half v) { return __half2float(v); }
 PI_DEV float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -415,7 +431,7 @@ PI_DEV void mma_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* qs,
     const uint64_t qd = sdesc_sw128(su32(qs)), kd = sdesc_sw128(su32(ring)),
                    vd = sdesc_sw128_mn(su32(ring), kKeys * 128, 1024);
     int slot = 0, phase = 0;        // ring slot to use next, and the phase of its copies
-    int np0 = 0, np1 = 0;           // products P V asked of each group
+    int np0 = 0, np1 = 0;           // tiles whose weights each group has handed over
     bool ok = true;
     // S_w = Q_qw K^T
     auto scores = [&](int w, int qw, int i) {
@@ -427,13 +443,23 @@ PI_DEV void mma_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* qs,
         }
         mma_commit_warp(&sh.sfull[w]);
     };
-    // O_w (+)= P_w V
+    // O_w (+)= P_w V, half of the keys at a time as their weights arrive
     auto values = [&](int w, int i, bool add) {
+        int& np = w ? np1 : np0;
 #pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-            mma_f16_ta_warp(tmem + C::O_COL + (unsigned)(w * DH), tmem + (unsigned)(w * kKeys + kk * 8),
-                            vd + (uint64_t)(i * (C::TILE >> 4) + kk * 128), id_o, (add || kk > 0) ? 1u : 0u);
-        mma_commit_warp(&sh.odone[w]);
+        for (int half = 0; half < 2; ++half) {
+            if (!warp_wait(&sh.pready[w][half], np & 1, ctl)) return false;
+            tc_after();
+#pragma unroll
+            for (int k = 0; k < kHalf / 16; ++k) {
+                const int kk = half * (kHalf / 16) + k;
+                mma_f16_ta_warp(tmem + C::O_COL + (unsigned)(w * DH), tmem + (unsigned)(w * kKeys + kk * 8),
+                                vd + (uint64_t)(i * (C::TILE >> 4) + kk * 128), id_o, (add || kk > 0) ? 1u : 0u);
+            }
+            mma_commit_warp(&sh.odone[w][half]);
+        }
+        ++np;
+        return true;
     };
     auto copied = [&](int i, int ph) { return warp_wait(&sh.full[i], ph, ctl); };
     auto advance = [&]() {
@@ -441,13 +467,6 @@ PI_DEV void mma_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* qs,
             slot = 0;
             phase ^= 1;
         }
-    };
-    auto weights = [&](int w) {
-        int& np = w ? np1 : np0;
-        const bool r = warp_wait(&sh.pready[w], np & 1, ctl);
-        ++np;
-        tc_after();
-        return r;
     };
     // value rows outside the keys the item sees (in an item's first and last
     // tile): zeros, not what the cache or the slot holds there, since 0 x NaN
@@ -477,25 +496,43 @@ PI_DEV void mma_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* qs,
             mma_commit_warp(&sh.empty[slot]);
             if (nt == 1) mma_commit_warp(&sh.qempty);
             advance();
+            // step t uses V(t) and K(t + 1); theirs of step t + 1 are looked for
+            // between the two groups' products, waited for after them
+            int ik = slot;
+            bool there = false;
             for (int t = 0; t < nt; ++t) {
                 const bool more = t + 1 < nt;
-                const int ik = slot;
-                if (more) {
+                if (!there) {
+                    ik = slot;
+                    if (more) {
+                        if (!(ok = copied(slot, phase))) break;
+                        advance();
+                    }
                     if (!(ok = copied(slot, phase))) break;
-                    advance();
                 }
-                const int iv = slot;
-                if (!(ok = copied(slot, phase))) break;
-                clear(p, t, iv);
+                const int iv = slot, jk = ik;
                 advance();
-                if (!(ok = weights(0))) break;
-                values(0, iv, t > 0);
-                if (more) scores(0, 0, ik);
-                if (!(ok = weights(1))) break;
-                values(1, iv, t > 0);
+                clear(p, t, iv);
+                if (!(ok = values(0, iv, t > 0))) break;
+                if (more) scores(0, 0, jk);
+                there = false;
                 if (more) {
-                    scores(1, 1, ik);
-                    mma_commit_warp(&sh.empty[ik]);
+                    const int s1 = slot, p1 = phase, s2 = s1 + 1 == C::S ? 0 : s1 + 1, p2 = s1 + 1 == C::S ? p1 ^ 1 : p1;
+                    if (t + 2 < nt) {
+                        there = __all_sync(FULL, bar_test(&sh.full[s1], p1) & bar_test(&sh.full[s2], p2));
+                        if (there) {
+                            ik = s1;
+                            slot = s2;
+                            phase = p2;
+                        }
+                    } else {
+                        there = __all_sync(FULL, bar_test(&sh.full[s1], p1));
+                    }
+                }
+                if (!(ok = values(1, iv, t > 0))) break;
+                if (more) {
+                    scores(1, 1, jk);
+                    mma_commit_warp(&sh.empty[jk]);
                 }
                 mma_commit_warp(&sh.empty[iv]);
                 if (t + 2 == nt) mma_commit_warp(&sh.qempty);
@@ -515,8 +552,7 @@ PI_DEV void mma_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* qs,
                 const int w = t & 1;
                 if (!(ok = copied(slot, phase))) break;
                 clear(p, t, slot);
-                if (!(ok = weights(w))) break;
-                values(w, slot, t > 1);
+                if (!(ok = values(w, slot, t > 1))) break;
                 mma_commit_warp(&sh.empty[slot]);
                 advance();
                 if (t + 2 < nt) {
@@ -544,7 +580,7 @@ PI_DEV int arrive_gpu(int* p) {
 // Adds the parts of rows r0 .. r0 + rows - 1 (at most 32) of an item's tile,
 // whose first token is tok0, columns c0 .. c0 + cols - 1, in block order and
 // writes the outputs: one warp, once all parts have arrived.  A lane keeps one row and every (32 / rows)-th group of 4 columns,
-// so that a few rows still use the whole warp, and asks for eight 16-byte
+// so that a few rows still use the whole warp, and asks for sixteen 16-byte
 // values at a time (the L2 latency is what a join costs).
 template <typename T, int DH>
 PI_DEV void join_parts(const PagedArgs& a, const Piece& p, bool pair, int w, int r0, int rows, int tok0, int c0, int cols) {
@@ -583,29 +619,30 @@ PI_DEV void join_parts(const PagedArgs& a, const Piece& p, bool pair, int w, int
     const long long orow = p.cu + tok0 + tok;
     T* dst = static_cast<T*>(a.out) + orow * a.o_stride + (long long)head * DH;
     const int end = (c0 + cols) / 4;
-    for (int c = c0 / 4 + cg; c < end; c += 4 * step) {
-        float4 v[4];
+    constexpr int CS = 4, KS = 4;   // column groups and parts asked for at once
+    for (int c = c0 / 4 + cg; c < end; c += CS * step) {
+        float4 v[CS];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k0 = 0; k0 < p.parts; k0 += 2) {
-            float f[2];
-            float4 x[2][4];
+        for (int j = 0; j < CS; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = 0; k0 < p.parts; k0 += KS) {
+            float f[KS];
+            float4 x[KS][CS];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < KS; ++i) {
                 const int k = k0 + i;
                 const bool in = k < p.parts;
                 f[i] = in ? __ldcg(ml + k * ml_step + (k == 0 ? ml_first : 0)).x : -INFINITY;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < CS; ++j)
                     x[i][j] = in && c + j * step < end
                                   ? __ldcg(po + k * o_step + (k == 0 ? o_first : 0) + (size_t)(c + j * step) * a.part_rows)
                                   : make_float4(0.f, 0.f, 0.f, 0.f);
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < KS; ++i) {
                 const float g = ex2(f[i] - use);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < CS; ++j) {
                     v[j].x = fmaf(x[i][j].x, g, v[j].x);
                     v[j].y = fmaf(x[i][j].y, g, v[j].y);
                     v[j].z = fmaf(x[i][j].z, g, v[j].z);
@@ -614,7 +651,7 @@ PI_DEV void join_parts(const PagedArgs& a, const Piece& p, bool pair, int w, int
             }
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < CS; ++j)
             if (c + j * step < end)
                 *reinterpret_cast<uint2*>(dst + 4 * (c + j * step)) =
                     make_uint2(pack2(v[j].x * inv, v[j].y * inv, T()), pack2(v[j].z * inv, v[j].w * inv, T()));
@@ -638,8 +675,7 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
     const uint64_t c2 = pair2(c, c);
     int ns = 0, nm = 0;   // tiles of this group so far (all pieces); merges
     for (int n = 0;; ++n) {
-        // the piece stays in its slot until it is done, so that the tile loop's
-        // registers go to the scores
+        // the piece stays in its slot until it is done
         if (!warp_wait(&sh.lfull[n % kListDepth], (n / kListDepth) & 1, ctl)) return;
         const Piece& p = sh.list[n % kListDepth];
         const int nt = p.nt, j0 = p.j0;
@@ -662,91 +698,83 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
         for (int t = pair ? 0 : w; t < nt; t += pair ? 1 : 2) {
             if (!warp_wait(&sh.sfull[w], ns & 1, ctl)) return;
             tc_after();
-            if (any) {
-                uint32_t s[kKeys];
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                if (any) {
+                    uint32_t s[kHalf];
 #pragma unroll
-                for (int i = 0; i < kKeys; i += 32) tmem_ld32(s_at + (unsigned)i, s + i);
-                tmem_wait_ld();
-                tmem_loaded<kKeys>(s);
-                const int base = (j0 + t) * kKeys;
-                if (__any_sync(FULL, base < lo || base + kKeys > hi)) {
+                    for (int i = 0; i < kHalf; i += 32) tmem_ld32(s_at + (unsigned)(half * kHalf + i), s + i);
+                    tmem_wait_ld();
+                    tmem_loaded<kHalf>(s);
+                    const int base = (j0 + t) * kKeys + half * kHalf;
+                    if (__any_sync(FULL, base < lo || base + kHalf > hi)) {
 #pragma unroll
-                    for (int i = 0; i < kKeys; ++i)
-                        if (base + i < lo || base + i >= hi) s[i] = 0xff800000u;   // -inf
-                }
-                if (mine == 0) {
-                    float mx[4];
+                        for (int i = 0; i < kHalf; i += 32) {
+                            // bits of the keys that the row sees
+                            const uint32_t see = low_bits(hi - base - i) & ~low_bits(lo - base - i);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(s[i]);
+                            for (int e = 0; e < 32; ++e)
+                                if (!(see & (1u << e))) s[i + e] = 0xff800000u;   // -inf
+                        }
+                    }
+                    if (__any_sync(FULL, m == -INFINITY)) {   // the first keys that some row sees
+                        const float top = largest<kHalf>(s) * c;
+                        if (m == -INFINITY) m = top;
+                    }
+                    for (int pass = 0;; ++pass) {   // a second one with the true maximum: it is enough
+                        const float bias = kLift - (m == -INFINITY ? 0.f : m);
+                        const uint64_t bias2 = pair2(bias, bias);
+                        uint64_t sum[2] = {0, 0};
+                        uint32_t pk[kHalf / 2];
 #pragma unroll
-                    for (int i = 4; i < kKeys; i += 8)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mx[k] = i + 4 + k < kKeys
-                                        ? max3(mx[k], __uint_as_float(s[i + k]), __uint_as_float(s[i + 4 + k]))
-                                        : fmaxf(mx[k], __uint_as_float(s[i + k]));
-                    m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-                }
-                // the weights with m as it stands, and the maximum beside them; once
-                // more only if some row's has grown past the slack
-                for (;;) {
-                    const float bias = kLift - (m == -INFINITY ? 0.f : m);
-                    const uint64_t bias2 = pair2(bias, bias);
-                    uint64_t sum[2] = {0, 0};
-                    float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                    for (int i = 0; i < kKeys; i += 64) {
-                        uint32_t pk[32];
-#pragma unroll
-                        for (int e = 0; e < 64; e += 2) {
-                            const float s0 = __uint_as_float(s[i + e]), s1 = __uint_as_float(s[i + e + 1]);
-                            mx[(e >> 1) & 1] = max3(mx[(e >> 1) & 1], s0, s1);
+                        for (int e = 0; e < kHalf; e += 2) {
                             float x, y;
-                            split2(fma2(pair2(s0, s1), c2, bias2), x, y);
+                            split2(fma2(pair2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, bias2), x, y);
                             x = ex2(x);
                             y = ex2(y);
                             sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair2(x, y));
                             pk[e >> 1] = pack2(x, y, T());
                         }
-                        tmem_st32(s_at + (unsigned)(i >> 1), pk);
-                    }
-                    const float top = fmaxf(mx[0], mx[1]) * c;
-                    const bool grow = live && top > m + kSlack;
-                    if (!__any_sync(FULL, grow)) {
+                        tmem_st32(s_at + (unsigned)(half * (kHalf / 2)), pk);
                         float x, y;
                         split2(add2(sum[0], sum[1]), x, y);
-                        l += x + y;
-                        break;
-                    }
-                    const float f = grow ? ex2(m - top) : 1.f;
-                    if (grow) m = top;
-                    l *= f;
-                    if (mine > 0) {
-                        // O holds the sums over this group's earlier tiles
-                        if (!warp_wait(&sh.odone[w], (ns - 1) & 1, ctl)) return;
-                        tc_after();
-#pragma unroll 1
-                        for (int i = 0; i < DH; i += 16) {
-                            float o[16];
-                            tmem_ld16(o_at + (unsigned)i, o);
-                            tmem_wait_ld();
-                            tmem_loaded<16>(o);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] *= f;
-                            tmem_st16(o_at + (unsigned)i, o);
+                        x += y;
+                        if (pass == 1 || !__any_sync(FULL, live && x > kFull)) {
+                            l += x;
+                            break;
                         }
-                        tmem_wait_st();
+                        // m follows, and with it what this row has so far
+                        const float top = largest<kHalf>(s) * c;
+                        const float f = live && x > kFull ? ex2(m - top) : 1.f;
+                        if (live && x > kFull) m = top;
+                        l *= f;
+                        if (mine > 0 || half > 0) {
+                            // O holds the sums over this group's earlier keys: the tile
+                            // before (second half), or this tile's first half
+                            if (!warp_wait(&sh.odone[w][half ^ 1], (ns - 1 + half) & 1, ctl)) return;
+                            tc_after();
+#pragma unroll 1
+                            for (int i = 0; i < DH; i += 16) {
+                                float o[16];
+                                tmem_ld16(o_at + (unsigned)i, o);
+                                tmem_wait_ld();
+                                tmem_loaded<16>(o);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) o[e] *= f;
+                                tmem_st16(o_at + (unsigned)i, o);
+                            }
+                        }
                     }
+                    tmem_wait_st();
                 }
-                tmem_wait_st();
+                tc_before();
+                warp_arrive(&sh.pready[w][half]);
             }
-            tc_before();
-            warp_arrive(&sh.pready[w]);
             ++ns;
             ++mine;
         }
         if (mine > 0) {
-            if (!warp_wait(&sh.odone[w], (ns - 1) & 1, ctl)) return;
+            if (!warp_wait(&sh.odone[w][1], (ns - 1) & 1, ctl)) return;
             tc_after();
         }
         // what the merge adds: this group's columns [c0, c0 + cols) of O_w, and of the other group's O
@@ -899,8 +927,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_paged_attn(const __grid_co
             bar_init(&sh.qempty, 1);
             for (int w = 0; w < 2; ++w) {
                 bar_init(&sh.sfull[w], 1);
-                bar_init(&sh.pready[w], 4);
-                bar_init(&sh.odone[w], 1);
+                for (int half = 0; half < 2; ++half) {
+                    bar_init(&sh.pready[w][half], 4);
+                    bar_init(&sh.odone[w][half], 1);
+                }
                 bar_init(&sh.merge[w], 4);
             }
             for (int s = 0; s < kListDepth; ++s) {
@@ -988,21 +1018,16 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_paged_attn(const __grid_co
     __syncthreads();
     const Ctl ctl{a.status, a.timeout_ns, &sh.abort_flag};
     if (work) {
-        // 384 threads x 168 registers at launch = 256 x 208 + 128 x 88
-        if (warp < 8) {
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        if (warp < 8)
             softmax_role<T, DH>(a, sh, tmem, ctl);
-        } else {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-            if (warp == 8)
-                tile_role<DH>(a, sh, ring, ctl);
-            else if (warp == 9)
-                mma_role<T, DH>(a, sh, qs, ring, tmem, ctl);
-            else if (warp == 10)
-                query_role<DH>(a, sh, qs, ctl);
-            else if (lane == 0)
-                list_role<DH>(a, sh, sh.start_r, u1, U, G, ctl);
-        }
+        else if (warp == 8)
+            tile_role<DH>(a, sh, ring, ctl);
+        else if (warp == 9)
+            mma_role<T, DH>(a, sh, qs, ring, tmem, ctl);
+        else if (warp == 10)
+            query_role<DH>(a, sh, qs, ctl);
+        else if (lane == 0)
+            list_role<DH>(a, sh, sh.start_r, u1, U, G, ctl);
     }
     tc_before();
     __syncthreads();

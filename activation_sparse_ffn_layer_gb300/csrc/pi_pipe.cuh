@@ -48,6 +48,17 @@ PI_DEV bool bar_try(unsigned long long* b, unsigned parity) {
     return ok != 0;
 }
 
+// The same without waiting at all (try_wait may suspend the thread a while)
+PI_DEV bool bar_test(unsigned long long* b, unsigned parity) {
+    unsigned ok;
+    asm volatile(
+        "{\n .reg .pred q;\n mbarrier.test_wait.parity.shared::cta.b64 q, [%1], %2;\n selp.u32 %0, 1, 0, q;\n}"
+        : "=r"(ok)
+        : "r"(su32(b)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 struct Ctl {
     int* status;
     long long timeout_ns;
