@@ -8,11 +8,11 @@
 //     P = 2^(c S - m)   (a thread per row; running m and l = sum P)
 //     O += P V          (P as the A operand in tensor memory)
 // where c = scale / ln 2 and m trails the running maximum: it moves only when
-// the weights taken with it add up to more than 2^15 over 64 keys, which no
-// other row needs to know (then O and l are scaled), so O is touched rarely and
-// no maximum is taken on the way.  P carries a factor 2^7, which l and O share:
-// no weight is above 2^15, within fp16, the largest are 2^7 or more unless a
-// later tile's are, and weights down to 2^-31 of those survive the rounding.
+// the weights taken with it add up to more than 2^15 (bf16: 2^30) over a tile
+// (then O and l are scaled), so O is touched rarely and no maximum is taken on
+// the way.  P carries a factor 2^7, which l and O share: no fp16 weight is above
+// 2^15, those of the largest scores are 2^7 or more, and weights down to 2^-31
+// of theirs survive the rounding.
 //
 // Warps: 0-3 and 4-7 softmax (a thread per row), 8 key and value copies, 9 MMA
 // issue, 10 query copies, 11 the work list.  Items of two
@@ -50,10 +50,13 @@ constexpr int kTileRows = 128;         // rows of a tile at most
 constexpr int kPagedThreads = 384;
 constexpr int kListDepth = 4;          // pieces the work list runs ahead
 constexpr int kConsumers = 11;         // warps that read the work list
+constexpr int kWalk = 16;              // items of a request that are counted one by one, not by formula
 constexpr int kItemCost = 2;           // an item's fixed cost, in key tiles
 constexpr float kLift = 7.f;           // log2 of the factor that P, l and O share
-constexpr int kHalf = 64;              // keys whose weights are taken and handed over at once
-constexpr float kFull = 32768.f;       // sum of their weights from which m follows the maximum
+// Sum of a tile's weights from which m follows the maximum: no fp16 weight may
+// pass 65504; bf16 ones may grow further (O and l stay within fp32 for values to 2^80).
+PI_DEV float most_sum(__half) { return 32768.f; }
+PI_DEV float most_sum(__nv_bfloat16) { return 1073741824.f; }
 constexpr float kLn2 = 0.69314718055994531f;
 
 template <int DH>
@@ -110,7 +113,7 @@ struct Request {
 
 template <int DH>
 struct PagedShared {
-    unsigned long long full[12], empty[12], qfull, qempty, sfull[2], pready[2][2], odone[2][2], lfull[kListDepth],
+    unsigned long long full[12], empty[12], qfull, qempty, sfull[2], pready[2], odone[2], lfull[kListDepth],
         lempty[kListDepth], merge[2], merged, drain;
     Piece list[kListDepth];
     float ml[2][kKeys][2];
@@ -150,15 +153,64 @@ PI_DEV int item_tiles(const PagedArgs& a, const Request& r, int tok0, int* toks,
     return (*hi + kKeys - 1) / kKeys - *lo / kKeys;
 }
 
-// Cost of one KV head of a request, in key tiles: the items' tiles and
-// kItemCost for what an item costs besides them.
-PI_DEV long long request_units(const PagedArgs& a, const Request& r) {
+// sum of floor((a i + b) / m) over 0 <= i < n, for a, b >= 0 (Euclid's steps)
+PI_DEV long long floor_sum(long long n, long long m, long long a, long long b) {
+    long long sum = 0;
+    for (;;) {
+        if (a >= m) {
+            sum += n * (n - 1) / 2 * (a / m);
+            a %= m;
+        }
+        if (b >= m) {
+            sum += n * (b / m);
+            b %= m;
+        }
+        const long long y = a * n + b;
+        if (y < m) return sum;
+        n = y / m;
+        b = y % m;
+        const long long t = m;
+        m = a;
+        a = t;
+    }
+}
+
+// Cost, in key tiles, of the first x items of one KV head of a request: the
+// items' tiles (as item_tiles counts them), and kItemCost for what an item
+// costs besides them.
+__device__ __noinline__ long long units_before(const PagedArgs& a, const Request& r, int x) {
+    const int d = 2 * a.tile_tokens, items = (r.n + d - 1) / d;
+    if (x <= 0) return 0;
+    long long u = (long long)kItemCost * x;
+    int y = x;   // items before the last of all, which may be shorter
+    if (x == items) {
+        int toks, lo, hi;
+        u += item_tiles(a, r, (x - 1) * d, &toks, &lo, &hi);
+        --y;
+    }
+    // items whose last token sees nothing: a tile each
+    const int none = r.first < 0 ? min(y, -r.first / d) : 0;
+    u += none;
+    // ceil(hi / 128) with hi = first + (i + 1) d
+    u += floor_sum(y - none, kKeys, d, (long long)r.first + (long long)(none + 1) * d + kKeys - 1);
+    if (a.window > 0) {
+        // floor(lo / 128) with lo = first + i d - window + 1 once that is positive
+        const int gap = a.window - 1 - r.first;
+        const int from = max(none, gap < 0 ? 0 : gap / d + 1);
+        if (from < y) u -= floor_sum(y - from, kKeys, d, (long long)from * d - gap);
+    }
+    return u;
+}
+PI_DEV long long request_units(const PagedArgs& a, const Request& r) {   // of one KV head
+    const int d = 2 * a.tile_tokens;
+    if (r.n > kWalk * d) return units_before(a, r, (r.n + d - 1) / d);
     long long u = 0;
     int toks, lo, hi;
-    for (int t = 0; t < r.n; t += 2 * a.tile_tokens) u += kItemCost + item_tiles(a, r, t, &toks, &lo, &hi);
+    for (int t = 0; t < r.n; t += d) u += kItemCost + item_tiles(a, r, t, &toks, &lo, &hi);
     return u;
 }
 
+// The whole warp waits (bounded); every lane gets the same answer.
 PI_DEV bool warp_wait(unsigned long long* b, unsigned parity, const Ctl& c) {
     if (__all_sync(FULL, bar_test(b, parity))) return true;
     return __all_sync(FULL, bar_wait(b, parity, c));
@@ -430,53 +482,19 @@ PI_DEV void mma_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* qs,
     const unsigned id_o = idesc_f16(128, DH, false) | kType | (1u << 16);   // B (values) MN-major
     const uint64_t qd = sdesc_sw128(su32(qs)), kd = sdesc_sw128(su32(ring)),
                    vd = sdesc_sw128_mn(su32(ring), kKeys * 128, 1024);
-    int slot = 0, phase = 0;        // ring slot to use next, and the phase of its copies
-    int np0 = 0, np1 = 0;           // tiles whose weights each group has handed over
+    int it = 0;         // ring slots used by earlier pieces
+    int np[2] = {0, 0}; // tiles whose weights each group has handed over
     bool ok = true;
-    // S_w = Q_qw K^T
-    auto scores = [&](int w, int qw, int i) {
-#pragma unroll
-        for (int kk = 0; kk < DH / 16; ++kk) {
-            const unsigned o = (unsigned)((kk >> 2) * (kKeys * 128) + (kk & 3) * 32) >> 4;
-            mma_f16_warp(tmem + (unsigned)(w * kKeys), qd + (uint64_t)(qw * (C::QTILE >> 4) + o),
-                         kd + (uint64_t)(i * (C::TILE >> 4) + o), id_s, kk > 0 ? 1u : 0u);
-        }
-        mma_commit_warp(&sh.sfull[w]);
-    };
-    // O_w (+)= P_w V, half of the keys at a time as their weights arrive
-    auto values = [&](int w, int i, bool add) {
-        int& np = w ? np1 : np0;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            if (!warp_wait(&sh.pready[w][half], np & 1, ctl)) return false;
-            tc_after();
-#pragma unroll
-            for (int k = 0; k < kHalf / 16; ++k) {
-                const int kk = half * (kHalf / 16) + k;
-                mma_f16_ta_warp(tmem + C::O_COL + (unsigned)(w * DH), tmem + (unsigned)(w * kKeys + kk * 8),
-                                vd + (uint64_t)(i * (C::TILE >> 4) + kk * 128), id_o, (add || kk > 0) ? 1u : 0u);
-            }
-            mma_commit_warp(&sh.odone[w][half]);
-        }
-        ++np;
-        return true;
-    };
-    auto copied = [&](int i, int ph) { return warp_wait(&sh.full[i], ph, ctl); };
-    auto advance = [&]() {
-        if (++slot == C::S) {
-            slot = 0;
-            phase ^= 1;
-        }
-    };
     // value rows outside the keys the item sees (in an item's first and last
     // tile): zeros, not what the cache or the slot holds there, since 0 x NaN
     // would reach every row
-    auto clear = [&](const Piece& p, int t, int i) {
+    auto clear = [&](const Piece& p, int t, int slot) {
         const int base = (p.j0 + t) * kKeys;
         if (base >= p.lo && base + kKeys <= p.hi) return;
         const int z = min(max(p.lo - base, 0), kKeys), e = min(max(p.hi - base, z), kKeys);
-        unsigned char* v = ring + (size_t)i * C::TILE;
+        unsigned char* v = ring + (size_t)slot * C::TILE;
         const int dead = kKeys - (e - z);
+#pragma unroll 1
         for (int x = threadIdx.x & 31; x < dead * (DH / 8); x += 32) {
             const int d = x / (DH / 8), c = x % (DH / 8);
             const int r = d < z ? d : d + (e - z);
@@ -489,81 +507,56 @@ PI_DEV void mma_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* qs,
         const Piece p = next_piece<DH>(sh, n, ctl);
         if (p.nt == 0) break;
         const int nt = __shfl_sync(FULL, p.nt, 0);
-        if (!(ok = warp_wait(&sh.qfull, n & 1, ctl) && copied(slot, phase))) break;
-        if (p.toks > a.tile_tokens) {   // pair: both groups use every tile
-            scores(0, 0, slot);
-            scores(1, 1, slot);
-            mma_commit_warp(&sh.empty[slot]);
-            if (nt == 1) mma_commit_warp(&sh.qempty);
-            advance();
-            // step t uses V(t) and K(t + 1); theirs of step t + 1 are looked for
-            // between the two groups' products, waited for after them
-            int ik = slot;
-            bool there = false;
-            for (int t = 0; t < nt; ++t) {
-                const bool more = t + 1 < nt;
-                if (!there) {
-                    ik = slot;
-                    if (more) {
-                        if (!(ok = copied(slot, phase))) break;
-                        advance();
-                    }
-                    if (!(ok = copied(slot, phase))) break;
+        const bool pair = __shfl_sync(FULL, (int)(p.toks > a.tile_tokens), 0);
+        if (!(ok = warp_wait(&sh.qfull, n & 1, ctl))) break;
+        // Half a step: group w's P V of tile t, then its next S = Q K^T, of tile
+        // tk.  Both groups go through every tile (pair), or through alternate
+        // ones; the first two half steps have no weights yet.
+        const int end = pair ? 2 * nt : nt;
+#pragma unroll 1
+        for (int h = -2; h < end; ++h) {
+            const int w = h & 1;
+            const int t = pair ? h >> 1 : h, tk = pair ? t + 1 : h + 2;
+            const bool opens = !pair || w == 0, closes = !pair || w == 1;   // first and last use of the tiles
+            if (h >= 0) {
+                const int i = it + (t + 1 < nt ? 2 * t + 2 : 2 * nt - 1);
+                const int slot = i % C::S, phase = (i / C::S) & 1;
+                // copied, and the weights are there
+                if (!__all_sync(FULL, bar_test(&sh.full[slot], phase) & bar_test(&sh.pready[w], np[w] & 1))) {
+                    if (opens && !(ok = warp_wait(&sh.full[slot], phase, ctl))) break;
+                    if (!(ok = warp_wait(&sh.pready[w], np[w] & 1, ctl))) break;
                 }
-                const int iv = slot, jk = ik;
-                advance();
-                clear(p, t, iv);
-                if (!(ok = values(0, iv, t > 0))) break;
-                if (more) scores(0, 0, jk);
-                there = false;
-                if (more) {
-                    const int s1 = slot, p1 = phase, s2 = s1 + 1 == C::S ? 0 : s1 + 1, p2 = s1 + 1 == C::S ? p1 ^ 1 : p1;
-                    if (t + 2 < nt) {
-                        there = __all_sync(FULL, bar_test(&sh.full[s1], p1) & bar_test(&sh.full[s2], p2));
-                        if (there) {
-                            ik = s1;
-                            slot = s2;
-                            phase = p2;
-                        }
-                    } else {
-                        there = __all_sync(FULL, bar_test(&sh.full[s1], p1));
-                    }
-                }
-                if (!(ok = values(1, iv, t > 0))) break;
-                if (more) {
-                    scores(1, 1, jk);
-                    mma_commit_warp(&sh.empty[jk]);
-                }
-                mma_commit_warp(&sh.empty[iv]);
-                if (t + 2 == nt) mma_commit_warp(&sh.qempty);
+                ++np[w];
+                tc_after();
+                if (opens) clear(p, t, slot);
+                const unsigned d = tmem + C::O_COL + (unsigned)(w * DH), x = tmem + (unsigned)(w * kKeys);
+                const uint64_t y = vd + (uint64_t)(slot * (C::TILE >> 4));
+                const unsigned add = pair ? t > 0 : t > 1;
+#pragma unroll
+                for (int kk = 0; kk < kKeys / 16; ++kk)
+                    mma_f16_ta_warp(d, x + (unsigned)(kk * 8), y + (uint64_t)(kk * 128), id_o, kk > 0 ? 1u : add);
+                mma_commit_warp(&sh.odone[w]);
+                if (closes) mma_commit_warp(&sh.empty[slot]);
             }
-        } else {                        // the groups take alternate tiles
-            scores(0, 0, slot);
-            mma_commit_warp(&sh.empty[slot]);
-            advance();
-            if (nt > 1) {
-                if (!(ok = copied(slot, phase))) break;
-                scores(1, 0, slot);
-                mma_commit_warp(&sh.empty[slot]);
-                advance();
-            }
-            if (nt <= 2) mma_commit_warp(&sh.qempty);
-            for (int t = 0; t < nt; ++t) {
-                const int w = t & 1;
-                if (!(ok = copied(slot, phase))) break;
-                clear(p, t, slot);
-                if (!(ok = values(w, slot, t > 1))) break;
-                mma_commit_warp(&sh.empty[slot]);
-                advance();
-                if (t + 2 < nt) {
-                    if (!(ok = copied(slot, phase))) break;
-                    scores(w, 0, slot);
+            if (tk < nt) {
+                const int i = it + (tk > 0 ? 2 * tk - 1 : 0);
+                const int slot = i % C::S, phase = (i / C::S) & 1;
+                if (opens && !(ok = warp_wait(&sh.full[slot], phase, ctl))) break;
+                const unsigned d = tmem + (unsigned)(w * kKeys);
+                const uint64_t x = qd + (uint64_t)(pair ? w * (C::QTILE >> 4) : 0), y = kd + (uint64_t)(slot * (C::TILE >> 4));
+#pragma unroll
+                for (int kk = 0; kk < DH / 16; ++kk) {
+                    const unsigned o = (unsigned)((kk >> 2) * (kKeys * 128) + (kk & 3) * 32) >> 4;
+                    mma_f16_warp(d, x + o, y + o, id_s, kk > 0 ? 1u : 0u);
+                }
+                mma_commit_warp(&sh.sfull[w]);
+                if (closes) {
                     mma_commit_warp(&sh.empty[slot]);
-                    advance();
-                    if (t + 3 == nt) mma_commit_warp(&sh.qempty);
+                    if (tk + 1 == nt) mma_commit_warp(&sh.qempty);
                 }
             }
         }
+        it += 2 * nt;
     }
     // every product has completed before the block may exit
     __syncwarp();
@@ -580,10 +573,11 @@ PI_DEV int arrive_gpu(int* p) {
 // Adds the parts of rows r0 .. r0 + rows - 1 (at most 32) of an item's tile,
 // whose first token is tok0, columns c0 .. c0 + cols - 1, in block order and
 // writes the outputs: one warp, once all parts have arrived.  A lane keeps one row and every (32 / rows)-th group of 4 columns,
-// so that a few rows still use the whole warp, and asks for sixteen 16-byte
-// values at a time (the L2 latency is what a join costs).
+// so that a few rows still use the whole warp, and asks for four column groups
+// of four parts, sixteen 16-byte values, at a time (the L2 latency is what a
+// join costs).
 template <typename T, int DH>
-PI_DEV void join_parts(const PagedArgs& a, const Piece& p, bool pair, int w, int r0, int rows, int tok0, int c0, int cols) {
+__device__ __noinline__ void join_parts(const PagedArgs& a, const Piece& p, bool pair, int w, int r0, int rows, int tok0, int c0, int cols) {
     const int lane = threadIdx.x & 31;
     const int span = rows > 16 ? 32 : rows > 8 ? 16 : rows > 4 ? 8 : rows > 2 ? 4 : rows;   // power of two
     const int tr = r0 + (lane & (span - 1));   // row of the tile
@@ -619,7 +613,7 @@ PI_DEV void join_parts(const PagedArgs& a, const Piece& p, bool pair, int w, int
     const long long orow = p.cu + tok0 + tok;
     T* dst = static_cast<T*>(a.out) + orow * a.o_stride + (long long)head * DH;
     const int end = (c0 + cols) / 4;
-    constexpr int CS = 4, KS = 4;   // column groups and parts asked for at once
+    constexpr int CS = 4, KS = 4;
     for (int c = c0 / 4 + cg; c < end; c += CS * step) {
         float4 v[CS];
 #pragma unroll
@@ -693,65 +687,45 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
             hi = max(pos + 1, 0);
             lo = a.window > 0 ? min(max(0, pos - a.window + 1), hi) : 0;
         }
+        const int lo_most = __reduce_max_sync(FULL, lo), hi_least = __reduce_min_sync(FULL, hi);
         float m = -INFINITY, l = 0.f;
+        bool fresh = true;    // some row of the warp has seen nothing yet
         int mine = 0;         // tiles of this piece that this group has done
         for (int t = pair ? 0 : w; t < nt; t += pair ? 1 : 2) {
             if (!warp_wait(&sh.sfull[w], ns & 1, ctl)) return;
             tc_after();
+            if (any) {
+                uint32_t s[kKeys];
+#pragma unroll
+                for (int i = 0; i < kKeys; i += 32) tmem_ld32(s_at + (unsigned)i, s + i);
+                tmem_wait_ld();
+                tmem_loaded<kKeys>(s);
+                const int base = (j0 + t) * kKeys;
+                if (base < lo_most || base + kKeys > hi_least) {
+#pragma unroll
+                    for (int i = 0; i < kKeys; i += 32) {
+                        // bits of the keys that the row sees
+                        const uint32_t see = low_bits(hi - base - i) & ~low_bits(lo - base - i);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!(see & (1u << e))) s[i + e] = 0xff800000u;   // -inf
+                    }
+                }
+                // The weights with m as it stands; m is moved first where some row
+                // has seen nothing yet, and before a second pass where the weights
+                // of some row add up to too much.
+                bool move = fresh;
 #pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-                if (any) {
-                    uint32_t s[kHalf];
-#pragma unroll
-                    for (int i = 0; i < kHalf; i += 32) tmem_ld32(s_at + (unsigned)(half * kHalf + i), s + i);
-                    tmem_wait_ld();
-                    tmem_loaded<kHalf>(s);
-                    const int base = (j0 + t) * kKeys + half * kHalf;
-                    if (__any_sync(FULL, base < lo || base + kHalf > hi)) {
-#pragma unroll
-                        for (int i = 0; i < kHalf; i += 32) {
-                            // bits of the keys that the row sees
-                            const uint32_t see = low_bits(hi - base - i) & ~low_bits(lo - base - i);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!(see & (1u << e))) s[i + e] = 0xff800000u;   // -inf
-                        }
-                    }
-                    if (__any_sync(FULL, m == -INFINITY)) {   // the first keys that some row sees
-                        const float top = largest<kHalf>(s) * c;
-                        if (m == -INFINITY) m = top;
-                    }
-                    for (int pass = 0;; ++pass) {   // a second one with the true maximum: it is enough
-                        const float bias = kLift - (m == -INFINITY ? 0.f : m);
-                        const uint64_t bias2 = pair2(bias, bias);
-                        uint64_t sum[2] = {0, 0};
-                        uint32_t pk[kHalf / 2];
-#pragma unroll
-                        for (int e = 0; e < kHalf; e += 2) {
-                            float x, y;
-                            split2(fma2(pair2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, bias2), x, y);
-                            x = ex2(x);
-                            y = ex2(y);
-                            sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair2(x, y));
-                            pk[e >> 1] = pack2(x, y, T());
-                        }
-                        tmem_st32(s_at + (unsigned)(half * (kHalf / 2)), pk);
-                        float x, y;
-                        split2(add2(sum[0], sum[1]), x, y);
-                        x += y;
-                        if (pass == 1 || !__any_sync(FULL, live && x > kFull)) {
-                            l += x;
-                            break;
-                        }
-                        // m follows, and with it what this row has so far
-                        const float top = largest<kHalf>(s) * c;
-                        const float f = live && x > kFull ? ex2(m - top) : 1.f;
-                        if (live && x > kFull) m = top;
+                for (int pass = 0;; ++pass) {
+                    if (move) {
+                        const float top = largest<kKeys>(s) * c;
+                        const float f = top > m ? ex2(m - top) : 1.f;
+                        m = fmaxf(m, top);
                         l *= f;
-                        if (mine > 0 || half > 0) {
-                            // O holds the sums over this group's earlier keys: the tile
-                            // before (second half), or this tile's first half
-                            if (!warp_wait(&sh.odone[w][half ^ 1], (ns - 1 + half) & 1, ctl)) return;
+                        fresh = __any_sync(FULL, live && m == -INFINITY);
+                        if (mine > 0) {
+                            // O holds the sums over this group's earlier tiles
+                            if (!warp_wait(&sh.odone[w], (ns - 1) & 1, ctl)) return;
                             tc_after();
 #pragma unroll 1
                             for (int i = 0; i < DH; i += 16) {
@@ -765,16 +739,42 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
                             }
                         }
                     }
-                    tmem_wait_st();
+                    const float bias = kLift - (m == -INFINITY ? 0.f : m);
+                    const uint64_t bias2 = pair2(bias, bias);
+                    uint64_t sum[2] = {0, 0};
+#pragma unroll
+                    for (int i = 0; i < kKeys; i += 32) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float u, v;
+                            split2(fma2(pair2(__uint_as_float(s[i + e]), __uint_as_float(s[i + e + 1])), c2, bias2), u, v);
+                            u = ex2(u);
+                            v = ex2(v);
+                            sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair2(u, v));
+                            pk[e >> 1] = pack2(u, v, T());
+                        }
+                        tmem_st16(s_at + (unsigned)(i >> 1), pk);
+                    }
+                    float u, v;
+                    split2(add2(sum[0], sum[1]), u, v);
+                    u += v;
+                    // with the true maximum a second pass is enough
+                    if (pass == 1 || !__any_sync(FULL, live && u > most_sum(T()))) {
+                        l += u;
+                        break;
+                    }
+                    move = true;
                 }
-                tc_before();
-                warp_arrive(&sh.pready[w][half]);
+                tmem_wait_st();
             }
+            tc_before();
+            warp_arrive(&sh.pready[w]);
             ++ns;
             ++mine;
         }
         if (mine > 0) {
-            if (!warp_wait(&sh.odone[w][1], (ns - 1) & 1, ctl)) return;
+            if (!warp_wait(&sh.odone[w], (ns - 1) & 1, ctl)) return;
             tc_after();
         }
         // what the merge adds: this group's columns [c0, c0 + cols) of O_w, and of the other group's O
@@ -888,7 +888,8 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
                 seen = __shfl_sync(FULL, seen, 0);
                 if (seen == p.parts - 1) {
                     if (lane == 0) a.counters[p.block0 * 8 + warp] = 0;
-                    join_parts<T, DH>(a, p, pair, w, 32 * quad, min(32, tile_rows - 32 * quad), tok0, c0, cols);
+                    const int rows = min(32, tile_rows - 32 * quad);
+                    join_parts<T, DH>(a, p, pair, w, 32 * quad, rows, tok0, c0, cols);
                 }
             }
         }
@@ -927,10 +928,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_paged_attn(const __grid_co
             bar_init(&sh.qempty, 1);
             for (int w = 0; w < 2; ++w) {
                 bar_init(&sh.sfull[w], 1);
-                for (int half = 0; half < 2; ++half) {
-                    bar_init(&sh.pready[w][half], 4);
-                    bar_init(&sh.odone[w][half], 1);
-                }
+                bar_init(&sh.pready[w], 4);
+                bar_init(&sh.odone[w], 1);
                 bar_init(&sh.merge[w], 4);
             }
             for (int s = 0; s < kListDepth; ++s) {
@@ -999,12 +998,25 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_paged_attn(const __grid_co
             }
             const int g = (int)(left / u);
             left -= g * u;
-            int tok0 = 0, toks, lo, hi;
-            for (;; tok0 += 2 * a.tile_tokens) {
-                const int cost = kItemCost + item_tiles(a, r, tok0, &toks, &lo, &hi);
-                if (left < cost) break;
-                left -= cost;
+            // the item: the last one that starts at or before `left`
+            const int d = 2 * a.tile_tokens;
+            int i0 = 0, i1 = (r.n + d - 1) / d;
+            if (i1 > kWalk) {
+                while (i1 - i0 > 1) {
+                    const int mid = (i0 + i1) / 2;
+                    if (units_before(a, r, mid) <= left) i0 = mid;
+                    else i1 = mid;
+                }
+                left -= units_before(a, r, i0);
+            } else {
+                int toks, lo, hi;
+                for (;; ++i0) {
+                    const int cost = kItemCost + item_tiles(a, r, i0 * d, &toks, &lo, &hi);
+                    if (left < cost) break;
+                    left -= cost;
+                }
             }
+            const int tok0 = i0 * d;
             sh.start_u = u0;
             sh.start_b = b;
             sh.start_g = g;
@@ -1018,16 +1030,21 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_paged_attn(const __grid_co
     __syncthreads();
     const Ctl ctl{a.status, a.timeout_ns, &sh.abort_flag};
     if (work) {
-        if (warp < 8)
+        // 384 threads x 168 registers at launch = 256 x 208 + 128 x 88
+        if (warp < 8) {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
             softmax_role<T, DH>(a, sh, tmem, ctl);
-        else if (warp == 8)
-            tile_role<DH>(a, sh, ring, ctl);
-        else if (warp == 9)
-            mma_role<T, DH>(a, sh, qs, ring, tmem, ctl);
-        else if (warp == 10)
-            query_role<DH>(a, sh, qs, ctl);
-        else if (lane == 0)
-            list_role<DH>(a, sh, sh.start_r, u1, U, G, ctl);
+        } else {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+            if (warp == 8)
+                tile_role<DH>(a, sh, ring, ctl);
+            else if (warp == 9)
+                mma_role<T, DH>(a, sh, qs, ring, tmem, ctl);
+            else if (warp == 10)
+                query_role<DH>(a, sh, qs, ctl);
+            else if (lane == 0)
+                list_role<DH>(a, sh, sh.start_r, u1, U, G, ctl);
+        }
     }
     tc_before();
     __syncthreads();
