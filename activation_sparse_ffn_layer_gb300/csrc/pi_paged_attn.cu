@@ -8,7 +8,7 @@
 //     P = 2^(c S - m)   (a thread per row; running m and l = sum P)
 //     O += P V          (P as the A operand in tensor memory)
 // where c = scale / ln 2 and m trails the running maximum: it moves only when
-// the weights taken with it add up to more than 2^15 (bf16: 2^30) over a tile
+// the weights taken with it add up to more than 2^15 (bf16: 2^30) over 64 keys
 // (then O and l are scaled), so O is touched rarely and no maximum is taken on
 // the way.  P carries a factor 2^7, which l and O share: no fp16 weight is above
 // 2^15, those of the largest scores are 2^7 or more, and weights down to 2^-31
@@ -53,7 +53,7 @@ constexpr int kConsumers = 11;         // warps that read the work list
 constexpr int kWalk = 16;              // items of a request that are counted one by one, not by formula
 constexpr int kItemCost = 2;           // an item's fixed cost, in key tiles
 constexpr float kLift = 7.f;           // log2 of the factor that P, l and O share
-// Sum of a tile's weights from which m follows the maximum: no fp16 weight may
+// Sum of half a tile's weights from which m follows the maximum: no fp16 weight may
 // pass 65504; bf16 ones may grow further (O and l stay within fp32 for values to 2^80).
 PI_DEV float most_sum(__half) { return 32768.f; }
 PI_DEV float most_sum(__nv_bfloat16) { return 1073741824.f; }
@@ -113,7 +113,7 @@ struct Request {
 
 template <int DH>
 struct PagedShared {
-    unsigned long long full[12], empty[12], qfull, qempty, sfull[2], pready[2], odone[2], lfull[kListDepth],
+    unsigned long long full[12], empty[12], qfull, qempty, sfull[2], pready[2][2], odone[2][2], lfull[kListDepth],
         lempty[kListDepth], merge[2], merged, drain;
     Piece list[kListDepth];
     float ml[2][kKeys][2];
@@ -483,7 +483,7 @@ PI_DEV void mma_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* qs,
     const uint64_t qd = sdesc_sw128(su32(qs)), kd = sdesc_sw128(su32(ring)),
                    vd = sdesc_sw128_mn(su32(ring), kKeys * 128, 1024);
     int it = 0;         // ring slots used by earlier pieces
-    int np[2] = {0, 0}; // tiles whose weights each group has handed over
+    int done0 = 0, done1 = 0;   // tiles of each group in earlier pieces
     bool ok = true;
     // value rows outside the keys the item sees (in an item's first and last
     // tile): zeros, not what the cache or the slot holds there, since 0 x NaN
@@ -521,21 +521,27 @@ PI_DEV void mma_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* qs,
             if (h >= 0) {
                 const int i = it + (t + 1 < nt ? 2 * t + 2 : 2 * nt - 1);
                 const int slot = i % C::S, phase = (i / C::S) & 1;
-                // copied, and the weights are there
-                if (!__all_sync(FULL, bar_test(&sh.full[slot], phase) & bar_test(&sh.pready[w], np[w] & 1))) {
-                    if (opens && !(ok = warp_wait(&sh.full[slot], phase, ctl))) break;
-                    if (!(ok = warp_wait(&sh.pready[w], np[w] & 1, ctl))) break;
-                }
-                ++np[w];
-                tc_after();
-                if (opens) clear(p, t, slot);
                 const unsigned d = tmem + C::O_COL + (unsigned)(w * DH), x = tmem + (unsigned)(w * kKeys);
                 const uint64_t y = vd + (uint64_t)(slot * (C::TILE >> 4));
                 const unsigned add = pair ? t > 0 : t > 1;
+                const unsigned turn = (unsigned)((w ? done1 : done0) + (pair ? t : t >> 1)) & 1u;
+                // the values are copied, and the first half of the weights is there
+                if (!__all_sync(FULL, bar_test(&sh.full[slot], phase) & bar_test(&sh.pready[w][0], turn))) {
+                    if (opens && !(ok = warp_wait(&sh.full[slot], phase, ctl))) break;
+                    if (!(ok = warp_wait(&sh.pready[w][0], turn, ctl))) break;
+                }
+                tc_after();
+                if (opens) clear(p, t, slot);
 #pragma unroll
-                for (int kk = 0; kk < kKeys / 16; ++kk)
+                for (int kk = 0; kk < kKeys / 32; ++kk)
                     mma_f16_ta_warp(d, x + (unsigned)(kk * 8), y + (uint64_t)(kk * 128), id_o, kk > 0 ? 1u : add);
-                mma_commit_warp(&sh.odone[w]);
+                mma_commit_warp(&sh.odone[w][0]);
+                if (!(ok = warp_wait(&sh.pready[w][1], turn, ctl))) break;
+                tc_after();
+#pragma unroll
+                for (int kk = kKeys / 32; kk < kKeys / 16; ++kk)
+                    mma_f16_ta_warp(d, x + (unsigned)(kk * 8), y + (uint64_t)(kk * 128), id_o, 1u);
+                mma_commit_warp(&sh.odone[w][1]);
                 if (closes) mma_commit_warp(&sh.empty[slot]);
             }
             if (tk < nt) {
@@ -557,6 +563,8 @@ PI_DEV void mma_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* qs,
             }
         }
         it += 2 * nt;
+        done0 += pair ? nt : (nt + 1) / 2;
+        done1 += pair ? nt : nt / 2;
     }
     // every product has completed before the block may exit
     __syncwarp();
@@ -564,10 +572,39 @@ PI_DEV void mma_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* qs,
     bar_drain(&sh.drain, 0, kDrainTimeoutNs);
 }
 
+// The weights 2^(c s + bias) of 64 scores into P (32 columns at `at`), and their sum.
+template <typename T>
+PI_DEV float take_weights(const uint32_t* s, unsigned at, uint64_t c2, uint64_t bias2) {
+    uint64_t sum[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < kKeys / 2; i += 32) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+            float u, v;
+            split2(fma2(pair2(__uint_as_float(s[i + e]), __uint_as_float(s[i + e + 1])), c2, bias2), u, v);
+            u = ex2(u);
+            v = ex2(v);
+            sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair2(u, v));
+            pk[e >> 1] = pack2(u, v, T());
+        }
+        tmem_st16(at + (unsigned)(i >> 1), pk);
+    }
+    float u, v;
+    split2(add2(sum[0], sum[1]), u, v);
+    return u + v;
+}
+
 PI_DEV int arrive_gpu(int* p) {
     int old;
     asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(old) : "l"(p) : "memory");
     return old;
+}
+
+PI_DEV int peek_gpu(const int* p) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
 }
 
 // Adds the parts of rows r0 .. r0 + rows - 1 (at most 32) of an item's tile,
@@ -595,8 +632,9 @@ __device__ __noinline__ void join_parts(const PagedArgs& a, const Piece& p, bool
         float2 x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int k = k0 + i;
-            x[i] = k < p.parts ? __ldcg(ml + k * ml_step + (k == 0 ? ml_first : 0)) : make_float2(-INFINITY, 0.f);
+            const int k = min(k0 + i, p.parts - 1);
+            x[i] = __ldcg(ml + k * ml_step + (k == 0 ? ml_first : 0));
+            if (k0 + i >= p.parts) x[i] = make_float2(-INFINITY, 0.f);
         }
         float top = M;
 #pragma unroll
@@ -619,21 +657,21 @@ __device__ __noinline__ void join_parts(const PagedArgs& a, const Piece& p, bool
 #pragma unroll
         for (int j = 0; j < CS; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k0 = 0; k0 < p.parts; k0 += KS) {
+            // loads without conditions, so that all of them are in flight at once
+            // (past the end: once more the last one, left out below)
             float f[KS];
             float4 x[KS][CS];
 #pragma unroll
             for (int i = 0; i < KS; ++i) {
-                const int k = k0 + i;
-                const bool in = k < p.parts;
-                f[i] = in ? __ldcg(ml + k * ml_step + (k == 0 ? ml_first : 0)).x : -INFINITY;
+                const int k = min(k0 + i, p.parts - 1);
+                f[i] = __ldcg(ml + k * ml_step + (k == 0 ? ml_first : 0)).x;
+                const float4* src = po + k * o_step + (k == 0 ? o_first : 0);
 #pragma unroll
-                for (int j = 0; j < CS; ++j)
-                    x[i][j] = in && c + j * step < end
-                                  ? __ldcg(po + k * o_step + (k == 0 ? o_first : 0) + (size_t)(c + j * step) * a.part_rows)
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int j = 0; j < CS; ++j) x[i][j] = __ldcg(src + (size_t)min(c + j * step, end - 1) * a.part_rows);
             }
 #pragma unroll
             for (int i = 0; i < KS; ++i) {
+                if (k0 + i >= p.parts) break;
                 const float g = ex2(f[i] - use);
 #pragma unroll
                 for (int j = 0; j < CS; ++j) {
@@ -711,21 +749,24 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
                             if (!(see & (1u << e))) s[i + e] = 0xff800000u;   // -inf
                     }
                 }
-                // The weights with m as it stands; m is moved first where some row
-                // has seen nothing yet, and before a second pass where the weights
-                // of some row add up to too much.
+                // The weights with m as it stands, half of the keys at a time, each
+                // handed over once done; m is moved first where some row has seen
+                // nothing yet, and where the weights of some row add up to too much
+                // (they are taken again: with the true maximum once is enough).
                 bool move = fresh;
+                int from = 0, again = 0;
 #pragma unroll 1
-                for (int pass = 0;; ++pass) {
+                for (;;) {
                     if (move) {
                         const float top = largest<kKeys>(s) * c;
                         const float f = top > m ? ex2(m - top) : 1.f;
                         m = fmaxf(m, top);
                         l *= f;
                         fresh = __any_sync(FULL, live && m == -INFINITY);
-                        if (mine > 0) {
-                            // O holds the sums over this group's earlier tiles
-                            if (!warp_wait(&sh.odone[w], (ns - 1) & 1, ctl)) return;
+                        if (mine > 0 || from > 0) {
+                            // O holds the sums over this group's earlier keys: up to the
+                            // tile before, or to this tile's first half
+                            if (!warp_wait(&sh.odone[w][from ^ 1], (ns - 1 + from) & 1, ctl)) return;
                             tc_after();
 #pragma unroll 1
                             for (int i = 0; i < DH; i += 16) {
@@ -738,43 +779,43 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
                                 tmem_st16(o_at + (unsigned)i, o);
                             }
                         }
+                        move = false;
                     }
                     const float bias = kLift - (m == -INFINITY ? 0.f : m);
                     const uint64_t bias2 = pair2(bias, bias);
-                    uint64_t sum[2] = {0, 0};
-#pragma unroll
-                    for (int i = 0; i < kKeys; i += 32) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            float u, v;
-                            split2(fma2(pair2(__uint_as_float(s[i + e]), __uint_as_float(s[i + e + 1])), c2, bias2), u, v);
-                            u = ex2(u);
-                            v = ex2(v);
-                            sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair2(u, v));
-                            pk[e >> 1] = pack2(u, v, T());
+                    if (from == 0) {
+                        const float u = take_weights<T>(s, s_at, c2, bias2);
+                        if (again == 0 && __any_sync(FULL, live && u > most_sum(T()))) {
+                            move = true;
+                            again = 1;
+                            continue;
                         }
-                        tmem_st16(s_at + (unsigned)(i >> 1), pk);
-                    }
-                    float u, v;
-                    split2(add2(sum[0], sum[1]), u, v);
-                    u += v;
-                    // with the true maximum a second pass is enough
-                    if (pass == 1 || !__any_sync(FULL, live && u > most_sum(T()))) {
                         l += u;
-                        break;
+                        tmem_wait_st();
+                        tc_before();
+                        warp_arrive(&sh.pready[w][0]);
+                        again = 0;
                     }
-                    move = true;
+                    const float u = take_weights<T>(s + kKeys / 2, s_at + kKeys / 4, c2, bias2);
+                    if (again == 0 && __any_sync(FULL, live && u > most_sum(T()))) {
+                        move = true;
+                        from = again = 1;
+                        continue;
+                    }
+                    l += u;
+                    tmem_wait_st();
+                    break;
                 }
-                tmem_wait_st();
+            } else {
+                warp_arrive(&sh.pready[w][0]);
             }
             tc_before();
-            warp_arrive(&sh.pready[w]);
+            warp_arrive(&sh.pready[w][1]);
             ++ns;
             ++mine;
         }
         if (mine > 0) {
-            if (!warp_wait(&sh.odone[w], (ns - 1) & 1, ctl)) return;
+            if (!warp_wait(&sh.odone[w][1], (ns - 1) & 1, ctl)) return;
             tc_after();
         }
         // what the merge adds: this group's columns [c0, c0 + cols) of O_w, and of the other group's O
@@ -809,44 +850,89 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
             const bool whole = p.parts == 1;
             const int blk = (int)blockIdx.x * 2 + p.own;
             float* po = a.part_o + (size_t)blk * DH * a.part_rows;
-            float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+            int* const arrivals = a.counters + p.block0 * 8 + warp;
+            // With two parts, and the other there already, nothing is written for
+            // others to read: the two are added on the spot (in block order, as
+            // join_parts does).
+            bool last = false;
+            if (p.parts == 2) {
+                int seen = 0;
+                if (lane == 0) seen = peek_gpu(arrivals);
+                last = __shfl_sync(FULL, seen, 0) == 1;
+            }
+            const int mine_k = (int)blockIdx.x - p.block0;
+            const int there = (p.block0 + 1 - mine_k) * 2 + mine_k;   // the other's partial: its second slot is of part 0
+            const float m_own = m, l_own = l;
+            float f_here = 1.f, f_there = 0.f;
+            if (last) {
+                const float2 x = __ldcg(reinterpret_cast<const float2*>(
+                    a.part_ml + ((size_t)(there * 2 + (pair ? 0 : w)) * a.part_rows + (live ? r : 0)) * 2));
+                const float M = fmaxf(m, x.x), use = M == -INFINITY ? 0.f : M;
+                f_here = ex2(m - use);
+                f_there = ex2(x.x - use);
+                l = mine_k == 0 ? fmaf(x.y, f_there, l * f_here) : fmaf(l, f_here, x.y * f_there);
+                m = M;
+            }
             bool odd = false;
-            for (int i = c0; i < c0 + cols; i += 32) {
-                float v[32];
-                uint32_t o[32];
+            for (;;) {
+                const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+                const float4* pt = reinterpret_cast<const float4*>(a.part_o + (size_t)there * DH * a.part_rows) + (live ? r : 0);
+#pragma unroll 1
+                for (int i = c0; i < c0 + cols; i += 32) {
+                    float v[32];
+                    float4 y[8];
+                    uint32_t o[32];
+                    if (last) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = 0.f;
-                if (own_any) {
-                    tmem_ld32(o_at + (unsigned)i, o);
-                    tmem_wait_ld();
-                    tmem_loaded<32>(o);
+                        for (int e = 0; e < 8; ++e) y[e] = __ldcg(pt + (size_t)(i / 4 + e) * a.part_rows);
+                    }
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * f_own;
+                    for (int e = 0; e < 32; ++e) v[e] = 0.f;
+                    if (own_any) {
+                        tmem_ld32(o_at + (unsigned)i, o);
+                        tmem_wait_ld();
+                        tmem_loaded<32>(o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * f_own;
+                    }
+                    if (other_any) {
+                        tmem_ld32(o_other + (unsigned)i, o);
+                        tmem_wait_ld();
+                        tmem_loaded<32>(o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = fmaf(__uint_as_float(o[e]), f_other, v[e]);
+                    }
+                    float check = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) check = fmaf(v[e], 0.f, check);
+                    odd |= check != 0.f;   // NaN: some value is not finite
+                    if (last) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float z = e % 4 == 0 ? y[e / 4].x : e % 4 == 1 ? y[e / 4].y : e % 4 == 2 ? y[e / 4].z : y[e / 4].w;
+                            v[e] = mine_k == 0 ? fmaf(z, f_there, fmaf(v[e], f_here, 0.f))
+                                               : fmaf(v[e], f_here, fmaf(z, f_there, 0.f));
+                        }
+                    }
+                    if (live && (whole || last)) {
+                        T* dst = static_cast<T*>(a.out) + orow * a.o_stride + (long long)head * DH + i;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            *reinterpret_cast<uint4*>(dst + e) = make_uint4(
+                                pack2(v[e] * inv, v[e + 1] * inv, T()), pack2(v[e + 2] * inv, v[e + 3] * inv, T()),
+                                pack2(v[e + 4] * inv, v[e + 5] * inv, T()), pack2(v[e + 6] * inv, v[e + 7] * inv, T()));
+                    } else if (live) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4*>(po + ((size_t)((i + e) / 4) * a.part_rows + r) * 4) =
+                                make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                    }
                 }
-                if (other_any) {
-                    tmem_ld32(o_other + (unsigned)i, o);
-                    tmem_wait_ld();
-                    tmem_loaded<32>(o);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = fmaf(__uint_as_float(o[e]), f_other, v[e]);
-                }
-                float check = 0.f;
-#pragma unroll
-                for (int e = 0; e < 32; ++e) check = fmaf(v[e], 0.f, check);
-                odd |= check != 0.f;   // NaN: some value is not finite
-                if (live && whole) {
-                    T* dst = static_cast<T*>(a.out) + orow * a.o_stride + (long long)head * DH + i;
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        *reinterpret_cast<uint4*>(dst + e) =
-                            make_uint4(pack2(v[e] * inv, v[e + 1] * inv, T()), pack2(v[e + 2] * inv, v[e + 3] * inv, T()),
-                                       pack2(v[e + 4] * inv, v[e + 5] * inv, T()), pack2(v[e + 6] * inv, v[e + 7] * inv, T()));
-                } else if (live) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<float4*>(po + ((size_t)((i + e) / 4) * a.part_rows + r) * 4) =
-                            make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-                }
+                if (!last || !__any_sync(FULL, live && odd)) break;
+                // a sum to be looked at row by row: the way over the workspace
+                last = false;
+                m = m_own;
+                l = l_own;
             }
             // rows whose sums are not finite, once more without the keys they do not see
             const unsigned redo = __ballot_sync(FULL, live && odd);
@@ -875,8 +961,9 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
                 }
             }
             float out_lse = l == 0.f ? -INFINITY : (m - kLift + log2f(l)) * kLn2;
-            if (whole) {
+            if (whole || last) {
                 if (live && a.lse != nullptr && c0 == 0) a.lse[orow * a.heads + head] = out_lse;
+                if (last && lane == 0) *arrivals = 0;
             } else {
                 float* ml = a.part_ml + ((size_t)(blk * 2 + (pair ? 0 : w)) * a.part_rows + r) * 2;
                 if (live) *reinterpret_cast<float2*>(ml) = make_float2(m, l);
@@ -884,10 +971,10 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
                 // release), the other blocks' before what follows it (acquire)
                 __syncwarp();
                 int seen = 0;
-                if (lane == 0) seen = arrive_gpu(a.counters + p.block0 * 8 + warp);
+                if (lane == 0) seen = arrive_gpu(arrivals);
                 seen = __shfl_sync(FULL, seen, 0);
                 if (seen == p.parts - 1) {
-                    if (lane == 0) a.counters[p.block0 * 8 + warp] = 0;
+                    if (lane == 0) *arrivals = 0;
                     const int rows = min(32, tile_rows - 32 * quad);
                     join_parts<T, DH>(a, p, pair, w, 32 * quad, rows, tok0, c0, cols);
                 }
@@ -928,8 +1015,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_paged_attn(const __grid_co
             bar_init(&sh.qempty, 1);
             for (int w = 0; w < 2; ++w) {
                 bar_init(&sh.sfull[w], 1);
-                bar_init(&sh.pready[w], 4);
-                bar_init(&sh.odone[w], 1);
+                for (int half = 0; half < 2; ++half) {
+                    bar_init(&sh.pready[w][half], 4);
+                    bar_init(&sh.odone[w][half], 1);
+                }
                 bar_init(&sh.merge[w], 4);
             }
             for (int s = 0; s < kListDepth; ++s) {
