@@ -462,7 +462,8 @@ bool page_desc_ok(const pi_page_desc& c) {
         return false;
     for (long long s : {c.page_stride, c.head_stride, c.token_stride})
         if (s < c.head_dim || s % 8 != 0 || s > (1ll << 36)) return false;
-    return true;
+    // a head starts on a block of 64 elements, and its last block has a 31-bit number
+    return c.head_stride % 64 == 0 && (c.kv_heads - 1) * (c.head_stride / 64) < (1ll << 31) - 2;
 }
 
 }  // namespace pi

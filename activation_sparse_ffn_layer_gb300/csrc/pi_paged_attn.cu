@@ -8,14 +8,15 @@
 //     P = 2^(c S - m)   (a thread per row; running m and l = sum P)
 //     O += P V          (P as the A operand in tensor memory)
 // where c = scale / ln 2 and m trails the running maximum: it moves only when
-// the weights taken with it add up to more than 2^15 (bf16: 2^30) over 64 keys
-// (then O and l are scaled), so O is touched rarely and no maximum is taken on
-// the way.  P carries a factor 2^7, which l and O share: no fp16 weight is above
-// 2^15, those of the largest scores are 2^7 or more, and weights down to 2^-31
-// of theirs survive the rounding.
+// the weights of some row outgrow it (fp16: a score 2^8 above it, looked for in
+// every tile, since a weight must fit 16 bits; bf16: a tile's weights adding up
+// to more than 2^30, seen after the tile), and then O and l are scaled.  P
+// carries a factor 2^7, which l and O share: no fp16 weight is above 2^15, those
+// of the largest scores are 2^7 or more, and weights down to 2^-31 of theirs
+// survive the rounding.
 //
-// Warps: 0-3 and 4-7 softmax (a thread per row), 8 key and value copies, 9 MMA
-// issue, 10 query copies, 11 the work list.  Items of two
+// Warps: 0-3 and 4-7 softmax (a thread per row), 8 key copies, 9 MMA issue, 10
+// value copies, 11 the work list and the query copies.  Items of two
 // tiles of rows give each softmax group one (both use every key tile: "pair");
 // smaller items, decode steps among them, give the two groups alternate key
 // tiles and merge at the end: one group's exponentials run beside the other's
@@ -49,14 +50,12 @@ constexpr int kKeys = 128;             // keys of a tile
 constexpr int kTileRows = 128;         // rows of a tile at most
 constexpr int kPagedThreads = 384;
 constexpr int kListDepth = 4;          // pieces the work list runs ahead
-constexpr int kConsumers = 11;         // warps that read the work list
+constexpr int kConsumers = 11;         // warps that read the work list: all but the one that writes it
 constexpr int kWalk = 16;              // items of a request that are counted one by one, not by formula
 constexpr int kItemCost = 2;           // an item's fixed cost, in key tiles
 constexpr float kLift = 7.f;           // log2 of the factor that P, l and O share
-// Sum of half a tile's weights from which m follows the maximum: no fp16 weight may
-// pass 65504; bf16 ones may grow further (O and l stay within fp32 for values to 2^80).
-PI_DEV float most_sum(__half) { return 32768.f; }
-PI_DEV float most_sum(__nv_bfloat16) { return 1073741824.f; }
+constexpr float kGrow = 8.f;           // fp16: growth (log2) of a maximum before m follows
+constexpr float kSum = 1073741824.f;   // bf16: sum of a tile's weights from which m follows
 constexpr float kLn2 = 0.69314718055994531f;
 
 template <int DH>
@@ -65,15 +64,19 @@ struct PagedCfg {
     static constexpr int TILE = kKeys * DH * 2;          // bytes of a key or value tile
     static constexpr int QTILE = kTileRows * DH * 2;
     static constexpr int Q = 2 * QTILE;
-    static constexpr int S = DH == 128 ? 5 : 12;         // ring slots
+    static constexpr int SK = DH == 128 ? 3 : 6;         // ring slots for keys: one more than for values, since
+    static constexpr int SV = DH == 128 ? 2 : 6;         // a key tile is used a step before its values
+    static constexpr int GROUP = HALVES * 1024;          // bytes of 8 keys or values: a 64-element block after the other
     static constexpr int MISC = 3072;
-    static constexpr int SMEM = Q + S * TILE + MISC;
+    static constexpr int SMEM = Q + (SK + SV) * TILE + MISC;
     static constexpr unsigned O_COL = 2 * kKeys;         // tensor memory: S0 S1 | O0 O1
     static_assert(SMEM <= 232448, "shared memory of a block");
 };
 
 struct PagedArgs {
-    CUtensorMap kmap, vmap;   // {dh, position, head, page}, box 64 x page_size
+    // a page as {64 elements, 8 positions, 64-element blocks, groups of 8 positions, page}:
+    // a head is dh / 64 blocks from block head * head_blocks on, the box the head's part of a page
+    CUtensorMap kmap, vmap;
     CUtensorMap qmap;         // {dh, head, token}, box 64 x group x tile_tokens
     const void *q, *k, *v;
     const int32_t *table, *cu, *kv;
@@ -83,6 +86,7 @@ struct PagedArgs {
     int heads, kv_heads, batch, max_tokens, max_new, max_pages, window, page_size, num_pages;
     int group;                // query heads per KV head
     int tile_tokens;          // tokens of a tile, 128 / group
+    int head_blocks;          // head stride in blocks of 64 elements
     int part_rows;            // rows of a partial
     float scale;
     int* counters;            // [blocks][8] arrivals at a cut item
@@ -113,7 +117,7 @@ struct Request {
 
 template <int DH>
 struct PagedShared {
-    unsigned long long full[12], empty[12], qfull, qempty, sfull[2], pready[2][2], odone[2][2], lfull[kListDepth],
+    unsigned long long kfull[6], kempty[6], vfull[6], vempty[6], qfull, qempty, sfull[2], pready[2][2], odone[2], lfull[kListDepth],
         lempty[kListDepth], merge[2], merged, drain;
     Piece list[kListDepth];
     float ml[2][kKeys][2];
@@ -310,10 +314,14 @@ __device__ __noinline__ void careful_row(const PagedArgs& a, int b, int g, long 
 // ------------------------------------------------------------ work list (warp 11)
 //
 // Units u of the block's range run through the items; an item's first
-// kItemCost units hold no tile, the next nt one each.
+// kItemCost units hold no tile, the next nt one each.  With a piece go its
+// query tiles, once the scores of the piece before are done; tokens past the
+// request's end or the last row come along or read as zeros: a row of S depends
+// on its own query alone.
 template <int DH>
-PI_DEV void list_role(const PagedArgs& a, PagedShared<DH>& sh, Request r, long long u1, long long U, int G,
-                      const Ctl& ctl) {
+PI_DEV void list_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* qs, Request r, long long u1, long long U,
+                      int G, const Ctl& ctl) {
+    using C = PagedCfg<DH>;
     int b = sh.start_b, g = sh.start_g, tok0 = sh.start_tok0, off = sh.start_off;
     long long u = sh.start_u;
     bool bad = false;
@@ -363,12 +371,21 @@ PI_DEV void list_role(const PagedArgs& a, PagedShared<DH>& sh, Request r, long l
             if (p.nt == 0) continue;   // only the item's cost falls into this block
         }
         const int s = n % kListDepth;
-        if (n >= kListDepth && !bar_wait(&sh.lempty[s], (n / kListDepth - 1) & 1, ctl)) return;
+        if (n >= kListDepth && !bar_wait(&sh.lempty[s], (n / kListDepth - 1) & 1, ctl)) break;
         sh.list[s] = p;
         bar_arrive(&sh.lfull[s]);
+        if (end) break;
+        if (n >= 1 && !bar_wait(&sh.qempty, (n - 1) & 1, ctl)) break;
+        const int tiles = p.toks > a.tile_tokens ? 2 : 1;
+        bar_arrive_expect_tx(&sh.qfull, (unsigned)(tiles * C::HALVES * a.tile_tokens * a.group) * 128u);
+        for (int w = 0; w < tiles; ++w)
+            for (int h = 0; h < C::HALVES; ++h)
+                tma_load_3d(qs + w * C::QTILE + h * (kTileRows * 128), &a.qmap, 64 * h, p.g * a.group,
+                            p.cu + p.tok0 + w * a.tile_tokens, &sh.qfull);
         ++n;
-        if (end) return;
     }
+    // the last copy has landed before the block may exit
+    if (n > 0) bar_drain(&sh.qfull, (n - 1) & 1, kDrainTimeoutNs);
 }
 
 // Next piece for a consumer warp; nt = 0 at the end or after an abort.
@@ -385,87 +402,64 @@ PI_DEV Piece next_piece(PagedShared<DH>& sh, int n, const Ctl& ctl) {
     return p;
 }
 
-// ------------------------------------------------------------ key and value tiles (warp 8)
+// ------------------------------------------------------------ key tiles (warp 8), value tiles (warp 10)
 //
-// Slots go out in the order the products need them: K0, then K(t+1), V(t).  A
-// lane per (page, column block) of a tile; pages outside the keys the item
-// sees are not read (their rows of the slot are stale: scores there are
-// masked, value rows are cleared by the MMA warp).
-template <int DH>
+// A lane per page of a tile, one copy each (70 cycles to issue, so a warp for
+// each ring: 8 pages of 16 positions and their table entries take most of the
+// time that a tile's products do).  Pages outside the keys the item sees are not
+// read (their rows of the slot are stale: scores there are masked, value rows
+// are cleared by the MMA warp).
+template <int DH, bool VALUES>
 PI_DEV void tile_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* ring, const Ctl& ctl) {
     using C = PagedCfg<DH>;
+    constexpr int S = VALUES ? C::SV : C::SK;
+    unsigned long long* const full = VALUES ? sh.vfull : sh.kfull;
+    unsigned long long* const empty = VALUES ? sh.vempty : sh.kempty;
+    const CUtensorMap* const map = VALUES ? &a.vmap : &a.kmap;
     const int lane = threadIdx.x & 31;
-    const int ppt = kKeys / a.page_size;
-    const int pl = lane % ppt, half = lane / ppt;
-    const bool has = half < C::HALVES;
-    int it = 0;
+    const int pages = kKeys / a.page_size;   // of a tile
+    int slot = 0, phase = 1, used = 0;       // phase of the slot's release before this use (none before the first)
     bool ok = true;
     for (int n = 0; ok; ++n) {
         const Piece p = next_piece<DH>(sh, n, ctl);
         if (p.nt == 0) break;
         const int32_t* row = a.table + (size_t)p.b * a.max_pages;
-        // page of this lane in tile t: -1 where it is not needed
-        auto page_of = [&](int t) {
-            const int key = (p.j0 + t) * kKeys + pl * a.page_size;
-            if (t >= p.nt || !has || key >= p.hi || key + a.page_size <= p.lo) return -1;
-            const int id = row[key / a.page_size];
-            if (id >= 0 && id < a.num_pages) return id;
-            atomicExch(a.status, (int)PI_ERR_INVALID_ARG);
-            return a.num_pages;   // past the last page: the copy fills zeros
+        // this lane's page in tile t: whether it is needed, and its table entry
+        auto need = [&](int t) {
+            const int key = (p.j0 + t) * kKeys + lane * a.page_size;
+            return t < p.nt && lane < pages && key < p.hi && key + a.page_size > p.lo;
         };
-        auto issue = [&](const CUtensorMap* map, int id) {
-            const int s = it % C::S;
-            if (it >= C::S && !warp_wait(&sh.empty[s], (it / C::S - 1) & 1, ctl)) return false;
-            const unsigned boxes = __popc(__ballot_sync(FULL, id >= 0));
-            if (lane == 0) bar_arrive_expect_tx(&sh.full[s], boxes * (unsigned)a.page_size * 128u);
+        auto entry = [&](int t) { return need(t) ? row[(p.j0 + t) * pages + lane] : 0; };
+        int id = entry(0), id1 = entry(1), id2 = entry(2);   // on their way two tiles ahead
+        for (int t = 0; t < p.nt; ++t) {
+            if (used >= S && !(ok = warp_wait(&empty[slot], phase, ctl))) break;
+            const bool copy = need(t);
+            const unsigned boxes = __popc(__ballot_sync(FULL, copy));
+            if (lane == 0) bar_arrive_expect_tx(&full[slot], boxes * (unsigned)(a.page_size * DH * 2));
             __syncwarp();
-            if (id >= 0)
-                tma_load_4d(ring + (size_t)s * C::TILE + half * (kKeys * 128) + pl * a.page_size * 128, map, 64 * half, 0,
-                            p.g, id, &sh.full[s]);
-            ++it;
-            return true;
-        };
-        int cur = page_of(0), nxt = page_of(1);
-        ok = issue(&a.kmap, cur);
-        for (int t = 0; t < p.nt && ok; ++t) {
-            const int after = page_of(t + 2);
-            if (t + 1 < p.nt) ok = issue(&a.kmap, nxt);
-            if (ok) ok = issue(&a.vmap, cur);
-            cur = nxt;
-            nxt = after;
+            if (copy) {
+                if (id < 0 || id >= a.num_pages) {
+                    atomicExch(a.status, (int)PI_ERR_INVALID_ARG);
+                    id = a.num_pages;   // past the last page: the copy fills zeros
+                }
+                tma_load_5d(ring + (size_t)slot * C::TILE + lane * (a.page_size >> 3) * C::GROUP, map, 0, 0,
+                            p.g * a.head_blocks, 0, id, &full[slot]);
+            }
+            id = id1;
+            id1 = id2;
+            id2 = entry(t + 3);
+            ++used;
+            if (++slot == S) {
+                slot = 0;
+                phase ^= 1;
+            }
         }
     }
     // every copy issued has landed before the block may exit
-    for (int s = 0; s < C::S && s < it; ++s) {
-        const int last = s + ((it - 1 - s) / C::S) * C::S;
-        bar_drain(&sh.full[s], (last / C::S) & 1, kDrainTimeoutNs);
+    for (int s = 0; s < S && s < used; ++s) {
+        const int last = s + ((used - 1 - s) / S) * S;
+        bar_drain(&full[s], (last / S) & 1, kDrainTimeoutNs);
     }
-}
-
-// ------------------------------------------------------------ queries (warp 10)
-//
-// The item's query tiles; tokens past the request's end or the last row come
-// along or read as zeros: a row of S depends on its own query alone.
-template <int DH>
-PI_DEV void query_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* qs, const Ctl& ctl) {
-    using C = PagedCfg<DH>;
-    int n = 0;
-    for (;; ++n) {
-        const Piece p = next_piece<DH>(sh, n, ctl);
-        if (p.nt == 0) break;
-        if (n >= 1 && !warp_wait(&sh.qempty, (n - 1) & 1, ctl)) break;
-        if ((threadIdx.x & 31) == 0) {
-            const int tiles = p.toks > a.tile_tokens ? 2 : 1;
-            bar_arrive_expect_tx(&sh.qfull, (unsigned)(tiles * C::HALVES * a.tile_tokens * a.group) * 128u);
-            for (int w = 0; w < tiles; ++w)
-                for (int h = 0; h < C::HALVES; ++h)
-                    tma_load_3d(qs + w * C::QTILE + h * (kTileRows * 128), &a.qmap, 64 * h, p.g * a.group,
-                                p.cu + p.tok0 + w * a.tile_tokens, &sh.qfull);
-        }
-        __syncwarp();
-    }
-    // the last copy has landed before the block may exit
-    if (n > 0) bar_drain(&sh.qfull, (n - 1) & 1, kDrainTimeoutNs);
 }
 
 // ------------------------------------------------------------ products (warp 9)
@@ -474,31 +468,75 @@ PI_DEV void query_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* q
 // has about 250 cycles from the last MMA of one product to the first of the
 // next: its waits are for things that are there already.
 template <typename T, int DH>
-PI_DEV void mma_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* qs, unsigned char* ring, unsigned tmem,
-                     const Ctl& ctl) {
+PI_DEV void mma_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* qs, unsigned char* kring,
+                     unsigned char* vring, unsigned tmem, const Ctl& ctl) {
     using C = PagedCfg<DH>;
     constexpr unsigned kType = std::is_same<T, __half>::value ? 0u : (1u << 7) | (1u << 10);   // A and B: fp16 or bf16
     const unsigned id_s = idesc_f16(128, kKeys, false) | kType;
     const unsigned id_o = idesc_f16(128, DH, false) | kType | (1u << 16);   // B (values) MN-major
-    const uint64_t qd = sdesc_sw128(su32(qs)), kd = sdesc_sw128(su32(ring)),
-                   vd = sdesc_sw128_mn(su32(ring), kKeys * 128, 1024);
-    int it = 0;         // ring slots used by earlier pieces
-    int done0 = 0, done1 = 0;   // tiles of each group in earlier pieces
+    const uint64_t qd = sdesc_sw128(su32(qs)), kd = sdesc_sw128(su32(kring), C::GROUP),
+                   vd = sdesc_sw128_mn(su32(vring), 1024, C::GROUP);
+    int ks = 0, kph = 0, vs = 0, vph = 0;   // ring slots to use next, and the phases of their copies
+    int done0 = 0, done1 = 0;               // tiles of each group so far
     bool ok = true;
+    auto next_k = [&]() {
+        if (++ks == C::SK) {
+            ks = 0;
+            kph ^= 1;
+        }
+    };
+    auto next_v = [&]() {
+        if (++vs == C::SV) {
+            vs = 0;
+            vph ^= 1;
+        }
+    };
+    auto keys_in = [&]() { return warp_wait(&sh.kfull[ks], kph, ctl); };
+    auto values_in = [&]() { return warp_wait(&sh.vfull[vs], vph, ctl); };
+    // S_w = Q_qw K^T
+    auto scores = [&](int w, int qw, int i) {
+        const uint64_t x = qd + (uint64_t)(qw * (C::QTILE >> 4)), y = kd + (uint64_t)(i * (C::TILE >> 4));
+#pragma unroll
+        for (int kk = 0; kk < DH / 16; ++kk) {
+            const unsigned b = (unsigned)((kk & 3) * 32);
+            mma_f16_warp(tmem + (unsigned)(w * kKeys), x + (((unsigned)((kk >> 2) * (kTileRows * 128)) + b) >> 4),
+                         y + (((unsigned)((kk >> 2) * 1024) + b) >> 4), id_s, kk > 0 ? 1u : 0u);
+        }
+        mma_commit_warp(&sh.sfull[w]);
+    };
+    // O_w (+)= P_w V, half of the keys at a time as their weights arrive
+    auto values = [&](int w, int i, unsigned add, int& done, bool last) {
+        const unsigned d = tmem + C::O_COL + (unsigned)(w * DH), x = tmem + (unsigned)(w * kKeys);
+        const uint64_t y = vd + (uint64_t)(i * (C::TILE >> 4));
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            if (!warp_wait(&sh.pready[w][half], done & 1, ctl)) return false;
+            tc_after();
+#pragma unroll
+            for (int k = 0; k < kKeys / 32; ++k) {
+                const int kk = half * (kKeys / 32) + k;
+                mma_f16_ta_warp(d, x + (unsigned)(kk * 8), y + (uint64_t)(kk * (2 * C::GROUP >> 4)), id_o, kk > 0 ? 1u : add);
+            }
+        }
+        ++done;
+        if (last) mma_commit_warp(&sh.odone[w]);
+        return true;
+    };
     // value rows outside the keys the item sees (in an item's first and last
     // tile): zeros, not what the cache or the slot holds there, since 0 x NaN
     // would reach every row
-    auto clear = [&](const Piece& p, int t, int slot) {
+    auto clear = [&](const Piece& p, int t, int i) {
         const int base = (p.j0 + t) * kKeys;
         if (base >= p.lo && base + kKeys <= p.hi) return;
         const int z = min(max(p.lo - base, 0), kKeys), e = min(max(p.hi - base, z), kKeys);
-        unsigned char* v = ring + (size_t)slot * C::TILE;
+        unsigned char* v = vring + (size_t)i * C::TILE;
         const int dead = kKeys - (e - z);
 #pragma unroll 1
         for (int x = threadIdx.x & 31; x < dead * (DH / 8); x += 32) {
             const int d = x / (DH / 8), c = x % (DH / 8);
             const int r = d < z ? d : d + (e - z);
-            *reinterpret_cast<uint4*>(v + (c >> 3) * (kKeys * 128) + r * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(v + (r >> 3) * C::GROUP + (c >> 3) * 1024 + (r & 7) * 128 + (c & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
         }
         fence_async_smem();
         __syncwarp();
@@ -509,62 +547,59 @@ PI_DEV void mma_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* qs,
         const int nt = __shfl_sync(FULL, p.nt, 0);
         const bool pair = __shfl_sync(FULL, (int)(p.toks > a.tile_tokens), 0);
         if (!(ok = warp_wait(&sh.qfull, n & 1, ctl))) break;
-        // Half a step: group w's P V of tile t, then its next S = Q K^T, of tile
-        // tk.  Both groups go through every tile (pair), or through alternate
-        // ones; the first two half steps have no weights yet.
-        const int end = pair ? 2 * nt : nt;
+        if (!(ok = keys_in())) break;
+        if (pair) {
+            // both groups use every tile; step t takes V(t) and K(t + 1), and
+            // looks for the next step's between the two groups' products
+            scores(0, 0, ks);
+            scores(1, 1, ks);
+            mma_commit_warp(&sh.kempty[ks]);
+            if (nt == 1) mma_commit_warp(&sh.qempty);
+            next_k();
+            bool there = false;
 #pragma unroll 1
-        for (int h = -2; h < end; ++h) {
-            const int w = h & 1;
-            const int t = pair ? h >> 1 : h, tk = pair ? t + 1 : h + 2;
-            const bool opens = !pair || w == 0, closes = !pair || w == 1;   // first and last use of the tiles
-            if (h >= 0) {
-                const int i = it + (t + 1 < nt ? 2 * t + 2 : 2 * nt - 1);
-                const int slot = i % C::S, phase = (i / C::S) & 1;
-                const unsigned d = tmem + C::O_COL + (unsigned)(w * DH), x = tmem + (unsigned)(w * kKeys);
-                const uint64_t y = vd + (uint64_t)(slot * (C::TILE >> 4));
-                const unsigned add = pair ? t > 0 : t > 1;
-                const unsigned turn = (unsigned)((w ? done1 : done0) + (pair ? t : t >> 1)) & 1u;
-                // the values are copied, and the first half of the weights is there
-                if (!__all_sync(FULL, bar_test(&sh.full[slot], phase) & bar_test(&sh.pready[w][0], turn))) {
-                    if (opens && !(ok = warp_wait(&sh.full[slot], phase, ctl))) break;
-                    if (!(ok = warp_wait(&sh.pready[w][0], turn, ctl))) break;
+            for (int t = 0; t < nt; ++t) {
+                const bool more = t + 1 < nt;
+                if (!there && !((ok = values_in()) && (!more || (ok = keys_in())))) break;
+                clear(p, t, vs);
+                if (!(ok = values(0, vs, t > 0, done0, !more))) break;
+                const int iv = vs, ik = ks;
+                next_v();
+                if (more) {
+                    scores(0, 0, ik);
+                    next_k();
+                    there = __all_sync(FULL, bar_test(&sh.vfull[vs], vph) & (t + 2 >= nt || bar_test(&sh.kfull[ks], kph)));
                 }
-                tc_after();
-                if (opens) clear(p, t, slot);
-#pragma unroll
-                for (int kk = 0; kk < kKeys / 32; ++kk)
-                    mma_f16_ta_warp(d, x + (unsigned)(kk * 8), y + (uint64_t)(kk * 128), id_o, kk > 0 ? 1u : add);
-                mma_commit_warp(&sh.odone[w][0]);
-                if (!(ok = warp_wait(&sh.pready[w][1], turn, ctl))) break;
-                tc_after();
-#pragma unroll
-                for (int kk = kKeys / 32; kk < kKeys / 16; ++kk)
-                    mma_f16_ta_warp(d, x + (unsigned)(kk * 8), y + (uint64_t)(kk * 128), id_o, 1u);
-                mma_commit_warp(&sh.odone[w][1]);
-                if (closes) mma_commit_warp(&sh.empty[slot]);
+                if (!(ok = values(1, iv, t > 0, done1, !more))) break;
+                mma_commit_warp(&sh.vempty[iv]);
+                if (more) {
+                    scores(1, 1, ik);
+                    mma_commit_warp(&sh.kempty[ik]);
+                    if (t + 2 == nt) mma_commit_warp(&sh.qempty);
+                }
             }
-            if (tk < nt) {
-                const int i = it + (tk > 0 ? 2 * tk - 1 : 0);
-                const int slot = i % C::S, phase = (i / C::S) & 1;
-                if (opens && !(ok = warp_wait(&sh.full[slot], phase, ctl))) break;
-                const unsigned d = tmem + (unsigned)(w * kKeys);
-                const uint64_t x = qd + (uint64_t)(pair ? w * (C::QTILE >> 4) : 0), y = kd + (uint64_t)(slot * (C::TILE >> 4));
-#pragma unroll
-                for (int kk = 0; kk < DH / 16; ++kk) {
-                    const unsigned o = (unsigned)((kk >> 2) * (kKeys * 128) + (kk & 3) * 32) >> 4;
-                    mma_f16_warp(d, x + o, y + o, id_s, kk > 0 ? 1u : 0u);
+        } else {
+            // the groups take alternate tiles
+#pragma unroll 1
+            for (int t = -2; t < nt; ++t) {
+                const int w = t & 1;
+                if (t >= 0) {
+                    if (!(ok = values_in())) break;
+                    clear(p, t, vs);
+                    int& done = w ? done1 : done0;
+                    if (!(ok = values(w, vs, t > 1, done, t + 2 >= nt))) break;
+                    mma_commit_warp(&sh.vempty[vs]);
+                    next_v();
                 }
-                mma_commit_warp(&sh.sfull[w]);
-                if (closes) {
-                    mma_commit_warp(&sh.empty[slot]);
-                    if (tk + 1 == nt) mma_commit_warp(&sh.qempty);
+                if (t + 2 < nt) {
+                    if (!(ok = keys_in())) break;
+                    scores(w, 0, ks);
+                    mma_commit_warp(&sh.kempty[ks]);
+                    next_k();
+                    if (t + 3 == nt) mma_commit_warp(&sh.qempty);
                 }
             }
         }
-        it += 2 * nt;
-        done0 += pair ? nt : (nt + 1) / 2;
-        done1 += pair ? nt : nt / 2;
     }
     // every product has completed before the block may exit
     __syncwarp();
@@ -705,7 +740,7 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
     const unsigned s_at = lanes + (unsigned)(w * kKeys), o_at = lanes + C::O_COL + (unsigned)(w * DH);
     const float c = a.scale / kLn2;
     const uint64_t c2 = pair2(c, c);
-    int ns = 0, nm = 0;   // tiles of this group so far (all pieces); merges
+    int ns = 0, np = 0, nm = 0;   // tiles of this group so far, pieces with any, merges
     for (int n = 0;; ++n) {
         // the piece stays in its slot until it is done
         if (!warp_wait(&sh.lfull[n % kListDepth], (n / kListDepth) & 1, ctl)) return;
@@ -728,6 +763,7 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
         const int lo_most = __reduce_max_sync(FULL, lo), hi_least = __reduce_min_sync(FULL, hi);
         float m = -INFINITY, l = 0.f;
         bool fresh = true;    // some row of the warp has seen nothing yet
+        float over = 0.f;     // bf16: the last tile's weights, if they add up to too much
         int mine = 0;         // tiles of this piece that this group has done
         for (int t = pair ? 0 : w; t < nt; t += pair ? 1 : 2) {
             if (!warp_wait(&sh.sfull[w], ns & 1, ctl)) return;
@@ -749,73 +785,63 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
                             if (!(see & (1u << e))) s[i + e] = 0xff800000u;   // -inf
                     }
                 }
-                // The weights with m as it stands, half of the keys at a time, each
-                // handed over once done; m is moved first where some row has seen
-                // nothing yet, and where the weights of some row add up to too much
-                // (they are taken again: with the true maximum once is enough).
+                // m, where it has to move: to the maximum where some row has seen
+                // nothing yet and for fp16 weights, above the last tile's for bf16
+                constexpr bool kHalfType = std::is_same<T, __half>::value;
+                float to = m;
                 bool move = fresh;
-                int from = 0, again = 0;
-#pragma unroll 1
-                for (;;) {
-                    if (move) {
-                        const float top = largest<kKeys>(s) * c;
-                        const float f = top > m ? ex2(m - top) : 1.f;
-                        m = fmaxf(m, top);
-                        l *= f;
-                        fresh = __any_sync(FULL, live && m == -INFINITY);
-                        if (mine > 0 || from > 0) {
-                            // O holds the sums over this group's earlier keys: up to the
-                            // tile before, or to this tile's first half
-                            if (!warp_wait(&sh.odone[w][from ^ 1], (ns - 1 + from) & 1, ctl)) return;
-                            tc_after();
-#pragma unroll 1
-                            for (int i = 0; i < DH; i += 16) {
-                                float o[16];
-                                tmem_ld16(o_at + (unsigned)i, o);
-                                tmem_wait_ld();
-                                tmem_loaded<16>(o);
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) o[e] *= f;
-                                tmem_st16(o_at + (unsigned)i, o);
-                            }
-                        }
-                        move = false;
-                    }
-                    const float bias = kLift - (m == -INFINITY ? 0.f : m);
-                    const uint64_t bias2 = pair2(bias, bias);
-                    if (from == 0) {
-                        const float u = take_weights<T>(s, s_at, c2, bias2);
-                        if (again == 0 && __any_sync(FULL, live && u > most_sum(T()))) {
-                            move = true;
-                            again = 1;
-                            continue;
-                        }
-                        l += u;
-                        tmem_wait_st();
-                        tc_before();
-                        warp_arrive(&sh.pready[w][0]);
-                        again = 0;
-                    }
-                    const float u = take_weights<T>(s + kKeys / 2, s_at + kKeys / 4, c2, bias2);
-                    if (again == 0 && __any_sync(FULL, live && u > most_sum(T()))) {
-                        move = true;
-                        from = again = 1;
-                        continue;
-                    }
-                    l += u;
-                    tmem_wait_st();
-                    break;
+                if (kHalfType || fresh) {
+                    to = fmaxf(m, largest<kKeys>(s) * c);
+                    if (!fresh) move = __any_sync(FULL, live && to > m + kGrow);
                 }
-            } else {
+                if (!kHalfType && __any_sync(FULL, over > kSum)) {
+                    if (over > kSum) to = fmaxf(to, m + log2f(over) - kLift);
+                    move = true;
+                }
+                if (move) {
+                    const float f = to > m ? ex2(m - to) : 1.f;
+                    m = to;
+                    l *= f;
+                    fresh = __any_sync(FULL, live && m == -INFINITY);
+                    if (mine > 0) {
+                        // O holds the sums over this group's earlier tiles: all in,
+                        // since their products came before this tile's S
+#pragma unroll 1
+                        for (int i = 0; i < DH; i += 16) {
+                            float o[16];
+                            tmem_ld16(o_at + (unsigned)i, o);
+                            tmem_wait_ld();
+                            tmem_loaded<16>(o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] *= f;
+                            tmem_st16(o_at + (unsigned)i, o);
+                        }
+                    }
+                }
+                // the weights, half of the keys at a time, each handed over once done
+                const float bias = kLift - (m == -INFINITY ? 0.f : m);
+                const uint64_t bias2 = pair2(bias, bias);
+                const float u = take_weights<T>(s, s_at, c2, bias2);
+                tmem_wait_st();
+                tc_before();
                 warp_arrive(&sh.pready[w][0]);
+                const float v = take_weights<T>(s + kKeys / 2, s_at + kKeys / 4, c2, bias2);
+                tmem_wait_st();
+                tc_before();
+                warp_arrive(&sh.pready[w][1]);
+                l += u + v;
+                if (!kHalfType) over = live ? u + v : 0.f;
+            } else {
+                tc_before();
+                warp_arrive(&sh.pready[w][0]);
+                warp_arrive(&sh.pready[w][1]);
             }
-            tc_before();
-            warp_arrive(&sh.pready[w][1]);
             ++ns;
             ++mine;
         }
         if (mine > 0) {
-            if (!warp_wait(&sh.odone[w][1], (ns - 1) & 1, ctl)) return;
+            if (!warp_wait(&sh.odone[w], np & 1, ctl)) return;
+            ++np;
             tc_after();
         }
         // what the merge adds: this group's columns [c0, c0 + cols) of O_w, and of the other group's O
@@ -998,7 +1024,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_paged_attn(const __grid_co
     extern __shared__ __align__(1024) unsigned char paged_smem[];
     unsigned char* qs = paged_smem;
     unsigned char* ring = qs + C::Q;
-    PagedShared<DH>& sh = *reinterpret_cast<PagedShared<DH>*>(ring + C::S * C::TILE);
+    unsigned char* vring = ring + C::SK * C::TILE;
+    PagedShared<DH>& sh = *reinterpret_cast<PagedShared<DH>*>(vring + C::SV * C::TILE);
     static_assert(sizeof(PagedShared<DH>) <= C::MISC, "bookkeeping");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if ((su32(paged_smem) & 1023u) != 0) {   // the tiles' swizzle needs it; the whole block leaves
@@ -1007,18 +1034,19 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_paged_attn(const __grid_co
     }
     if (warp == 9) {
         if (lane == 0) {
-            for (int s = 0; s < C::S; ++s) {
-                bar_init(&sh.full[s], 1);
-                bar_init(&sh.empty[s], 1);
+            for (int s = 0; s < 6; ++s) {
+                bar_init(&sh.kfull[s], 1);
+                bar_init(&sh.kempty[s], 1);
+                bar_init(&sh.vfull[s], 1);
+                bar_init(&sh.vempty[s], 1);
             }
             bar_init(&sh.qfull, 1);
             bar_init(&sh.qempty, 1);
             for (int w = 0; w < 2; ++w) {
                 bar_init(&sh.sfull[w], 1);
-                for (int half = 0; half < 2; ++half) {
-                    bar_init(&sh.pready[w][half], 4);
-                    bar_init(&sh.odone[w][half], 1);
-                }
+                bar_init(&sh.pready[w][0], 4);
+                bar_init(&sh.pready[w][1], 4);
+                bar_init(&sh.odone[w], 1);
                 bar_init(&sh.merge[w], 4);
             }
             for (int s = 0; s < kListDepth; ++s) {
@@ -1119,20 +1147,20 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_paged_attn(const __grid_co
     __syncthreads();
     const Ctl ctl{a.status, a.timeout_ns, &sh.abort_flag};
     if (work) {
-        // 384 threads x 168 registers at launch = 256 x 208 + 128 x 88
+        // 384 threads x 168 registers at launch = 256 x 200 + 128 x 104
         if (warp < 8) {
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
             softmax_role<T, DH>(a, sh, tmem, ctl);
         } else {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
             if (warp == 8)
-                tile_role<DH>(a, sh, ring, ctl);
+                tile_role<DH, false>(a, sh, ring, ctl);
             else if (warp == 9)
-                mma_role<T, DH>(a, sh, qs, ring, tmem, ctl);
+                mma_role<T, DH>(a, sh, qs, ring, vring, tmem, ctl);
             else if (warp == 10)
-                query_role<DH>(a, sh, qs, ctl);
+                tile_role<DH, true>(a, sh, vring, ctl);
             else if (lane == 0)
-                list_role<DH>(a, sh, sh.start_r, u1, U, G, ctl);
+                list_role<DH>(a, sh, qs, sh.start_r, u1, U, G, ctl);
         }
     }
     tc_before();
@@ -1177,13 +1205,13 @@ struct PagedLayout {
 bool cache_map(CUtensorMap* m, const void* base, const pi_page_desc& c) {
     PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
     if (fn == nullptr) return false;
-    const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.kv_heads,
-                                (cuuint64_t)c.num_pages};
-    const cuuint64_t strides[3] = {(cuuint64_t)c.token_stride * 2, (cuuint64_t)c.head_stride * 2,
+    const cuuint64_t blocks = (cuuint64_t)((c.kv_heads - 1) * (c.head_stride / 64) + c.head_dim / 64);
+    const cuuint64_t dims[5] = {64, 8, blocks, (cuuint64_t)(c.page_size / 8), (cuuint64_t)c.num_pages};
+    const cuuint64_t strides[4] = {(cuuint64_t)c.token_stride * 2, 128, (cuuint64_t)c.token_stride * 16,
                                    (cuuint64_t)c.page_stride * 2};
-    const cuuint32_t box[4] = {64u, (cuuint32_t)c.page_size, 1u, 1u};
-    const cuuint32_t es[4] = {1u, 1u, 1u, 1u};
-    return fn(m, c.dtype == PI_T_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+    const cuuint32_t box[5] = {64u, 8u, (cuuint32_t)(c.head_dim / 64), (cuuint32_t)(c.page_size / 8), 1u};
+    const cuuint32_t es[5] = {1u, 1u, 1u, 1u, 1u};
+    return fn(m, c.dtype == PI_T_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
               const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1273,6 +1301,7 @@ pi_status pi_paged_attn(const pi_paged_desc* desc, const pi_page_desc* cache, co
     a.num_pages = cache->num_pages;
     a.group = desc->heads / cache->kv_heads;
     a.tile_tokens = kTileRows / a.group;
+    a.head_blocks = (int)(cache->head_stride / 64);
     a.part_rows = lay.rows;
     a.scale = desc->scale > 0.f ? desc->scale : 1.0f / sqrtf((float)cache->head_dim);
     a.counters = reinterpret_cast<int*>(ws);

@@ -33,8 +33,9 @@ PI_DEV uint64_t sdesc(unsigned addr, unsigned lbo, unsigned sbo) {
 // Same for the 128-byte-swizzled K-major layout: rows of 128 bytes (64 fp16
 // of K), 8-row atoms of 1024 bytes (1024-byte aligned), 16-byte chunk c of row
 // r stored at chunk position c ^ (r % 8); K-steps advance the start by 32 bytes.
-PI_DEV uint64_t sdesc_sw128(unsigned addr) {
-    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
+// Atoms adjacent in M/N are sbo bytes apart.
+PI_DEV uint64_t sdesc_sw128(unsigned addr, unsigned sbo = 1024) {
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)(sbo >> 4) << 32) |
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 // 128-byte-swizzled MN-major layout (the W2t tile of FC2): atoms of 8 K-rows x
@@ -114,12 +115,12 @@ PI_DEV void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, 
 PI_DEV void tma_prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
-// The same with a 4-D map: the box at (x, y, z, w), innermost first
-PI_DEV void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, unsigned long long* bar) {
+// The same with a 5-D map: the box at (x, y, z, w, v), innermost first
+PI_DEV void tma_load_5d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, int v, unsigned long long* bar) {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-        "[%6];" ::"r"(su32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(su32(bar))
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], "
+        "[%7];" ::"r"(su32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(su32(bar))
         : "memory");
 }
 // 16 consecutive fp32 columns of this thread's TMEM lane

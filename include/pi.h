@@ -391,7 +391,8 @@ PI_API pi_status pi_block_tables(const pi_tables_desc *desc, const int32_t *cach
  * (page, head, position, i) is at page * page_stride + head * head_stride +
  * position * token_stride + i (in elements), so both [pages, heads, page_size,
  * head_dim] and [pages, page_size, heads, head_dim] are described.  Strides
- * are multiples of 8 and at least head_dim; base pointers 16-byte aligned. */
+ * are at least head_dim and multiples of 8 (head_stride of 64); base pointers
+ * 16-byte aligned. */
 typedef struct {
     int kv_heads;   /* 1 .. 1024                       */
     int head_dim;   /* 64 or 128                       */

@@ -46,7 +46,7 @@ def _page(P, **kw):
 
 BAD_PAGES = [dict(kv_heads=0), dict(kv_heads=1025), dict(head_dim=96), dict(page_size=8), dict(page_size=256),
              dict(num_pages=0), dict(dtype=2), dict(dtype=-1), dict(token_stride=60), dict(token_stride=68),
-             dict(head_stride=0), dict(page_stride=-2048)]
+             dict(head_stride=0), dict(head_stride=1032), dict(page_stride=-2048)]
 
 
 def test_rope_refusals(P):
