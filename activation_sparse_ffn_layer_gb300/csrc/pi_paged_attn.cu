@@ -928,10 +928,10 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
 #pragma unroll
                         for (int e = 0; e < 32; ++e) v[e] = fmaf(__uint_as_float(o[e]), f_other, v[e]);
                     }
-                    float check = 0.f;
+                    float check[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) check = fmaf(v[e], 0.f, check);
-                    odd |= check != 0.f;   // NaN: some value is not finite
+                    for (int e = 0; e < 32; ++e) check[e & 3] = fmaf(v[e], 0.f, check[e & 3]);
+                    odd |= (check[0] + check[1]) + (check[2] + check[3]) != 0.f;   // NaN: some value is not finite
                     if (last) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
