@@ -52,7 +52,10 @@ constexpr int kPagedThreads = 384;
 constexpr int kListDepth = 4;          // pieces the work list runs ahead
 constexpr int kConsumers = 11;         // warps that read the work list: all but the one that writes it
 constexpr int kWalk = 16;              // items of a request that are counted one by one, not by formula
-constexpr int kItemCost = 2;           // an item's fixed cost, in key tiles
+// What the work split counts, in units of half a microsecond or so: a key tile
+// for one tile of rows (memory), for two (products), an item besides its tiles.
+constexpr int kTileCost = 2, kPairCost = 3, kItemCost = 6;
+constexpr int kMinUnits = 5;           // of a block
 constexpr float kLift = 7.f;           // log2 of the factor that P, l and O share
 constexpr float kGrow = 8.f;           // fp16: growth (log2) of a maximum before m follows
 constexpr float kSum = 1073741824.f;   // bf16: sum of a tile's weights from which m follows
@@ -179,9 +182,10 @@ PI_DEV long long floor_sum(long long n, long long m, long long a, long long b) {
     }
 }
 
-// Cost, in key tiles, of the first x items of one KV head of a request: the
-// items' tiles (as item_tiles counts them), and kItemCost for what an item
-// costs besides them.
+PI_DEV int tile_cost(const PagedArgs& a, int toks) { return toks > a.tile_tokens ? kPairCost : kTileCost; }
+
+// Cost of the first x items of one KV head of a request: kItemCost each, and
+// their tiles (as item_tiles counts them).
 __device__ __noinline__ long long units_before(const PagedArgs& a, const Request& r, int x) {
     const int d = 2 * a.tile_tokens, items = (r.n + d - 1) / d;
     if (x <= 0) return 0;
@@ -189,32 +193,34 @@ __device__ __noinline__ long long units_before(const PagedArgs& a, const Request
     int y = x;   // items before the last of all, which may be shorter
     if (x == items) {
         int toks, lo, hi;
-        u += item_tiles(a, r, (x - 1) * d, &toks, &lo, &hi);
+        const int nt = item_tiles(a, r, (x - 1) * d, &toks, &lo, &hi);
+        u += nt * tile_cost(a, toks);
         --y;
     }
     // items whose last token sees nothing: a tile each
     const int none = r.first < 0 ? min(y, -r.first / d) : 0;
-    u += none;
     // ceil(hi / 128) with hi = first + (i + 1) d
-    u += floor_sum(y - none, kKeys, d, (long long)r.first + (long long)(none + 1) * d + kKeys - 1);
+    long long tiles = none + floor_sum(y - none, kKeys, d, (long long)r.first + (long long)(none + 1) * d + kKeys - 1);
     if (a.window > 0) {
         // floor(lo / 128) with lo = first + i d - window + 1 once that is positive
         const int gap = a.window - 1 - r.first;
         const int from = max(none, gap < 0 ? 0 : gap / d + 1);
-        if (from < y) u -= floor_sum(y - from, kKeys, d, (long long)from * d - gap);
+        if (from < y) tiles -= floor_sum(y - from, kKeys, d, (long long)from * d - gap);
     }
-    return u;
+    return u + kPairCost * tiles;
 }
 PI_DEV long long request_units(const PagedArgs& a, const Request& r) {   // of one KV head
     const int d = 2 * a.tile_tokens;
     if (r.n > kWalk * d) return units_before(a, r, (r.n + d - 1) / d);
     long long u = 0;
     int toks, lo, hi;
-    for (int t = 0; t < r.n; t += d) u += kItemCost + item_tiles(a, r, t, &toks, &lo, &hi);
+    for (int t = 0; t < r.n; t += d) {
+        const int nt = item_tiles(a, r, t, &toks, &lo, &hi);
+        u += kItemCost + nt * tile_cost(a, toks);
+    }
     return u;
 }
 
-// The whole warp waits (bounded); every lane gets the same answer.
 PI_DEV bool warp_wait(unsigned long long* b, unsigned parity, const Ctl& c) {
     if (__all_sync(FULL, bar_test(b, parity))) return true;
     return __all_sync(FULL, bar_wait(b, parity, c));
@@ -313,8 +319,10 @@ __device__ __noinline__ void careful_row(const PagedArgs& a, int b, int g, long 
 
 // ------------------------------------------------------------ work list (warp 11)
 //
-// Units u of the block's range run through the items; an item's first
-// kItemCost units hold no tile, the next nt one each.  With a piece go its
+// Units u of the block's range run through the items: kItemCost, then its
+// tiles' costs.  A block does the tiles that begin in its range (a range is
+// longer than a tile's cost, so every block between an item's first and last
+// has one).  With a piece go its
 // query tiles, once the scores of the piece before are done; tokens past the
 // request's end or the last row come along or read as zeros: a row of S depends
 // on its own query alone.
@@ -332,9 +340,10 @@ PI_DEV void list_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* qs
         if (!end) {
             int toks, lo, hi;
             const int nt = item_tiles(a, r, tok0, &toks, &lo, &hi);
+            const int c = tile_cost(a, toks);
             const long long i0 = u - off;   // the item's first unit
-            const int stop = (int)min((long long)(kItemCost + nt), u1 - i0);
-            const int from = max(off - kItemCost, 0), to = max(stop - kItemCost, 0);
+            const int stop = (int)min((long long)(kItemCost + nt * c), u1 - i0);
+            const int from = (max(off - kItemCost, 0) + c - 1) / c, to = (max(stop - kItemCost, 0) + c - 1) / c;
             p.nt = to - from;
             p.j0 = lo / kKeys + from;
             p.lo = lo;
@@ -349,7 +358,7 @@ PI_DEV void list_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* qs
             p.own = from == 0;
             if (p.nt != nt) {   // blocks that own its first and its last tile
                 p.block0 = (int)(((i0 + kItemCost + 1) * G - 1) / U);
-                p.parts = (int)(((i0 + kItemCost + nt) * G - 1) / U) - p.block0 + 1;
+                p.parts = (int)(((i0 + kItemCost + (nt - 1) * c + 1) * G - 1) / U) - p.block0 + 1;
             }
             u = i0 + stop;
             off = 0;
@@ -1096,9 +1105,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_paged_attn(const __grid_co
     }
     pre += before - own;   // units before this thread's requests
     const unsigned tmem = sh.tmem;
-    // blocks with work: at least two tiles each, one for each softmax group (a
-    // part costs a join, the second tile runs beside the first)
-    const int G = (int)min((long long)gridDim.x, (U + 1) / 2);
+    // blocks with work: about two tiles each at least, one for each softmax group
+    // (a part costs a join, the second tile runs beside the first)
+    const int G = (int)min((long long)gridDim.x, (U + kMinUnits - 1) / kMinUnits);
     const int blk = blockIdx.x;
     const long long u0 = G > 0 ? U * blk / G : 0, u1 = G > 0 ? U * (blk + 1) / G : 0;
     const bool work = blk < G;
@@ -1128,7 +1137,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_paged_attn(const __grid_co
             } else {
                 int toks, lo, hi;
                 for (;; ++i0) {
-                    const int cost = kItemCost + item_tiles(a, r, i0 * d, &toks, &lo, &hi);
+                    const int nt = item_tiles(a, r, i0 * d, &toks, &lo, &hi);
+                    const int cost = kItemCost + nt * tile_cost(a, toks);
                     if (left < cost) break;
                     left -= cost;
                 }
