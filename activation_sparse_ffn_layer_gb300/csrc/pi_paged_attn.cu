@@ -296,22 +296,45 @@ __device__ __noinline__ void careful_row(const PagedArgs& a, int b, int g, long 
         q[e] = to_f(qp[e]);
         o[e] = 0.f;
     }
-    for (int x = lo; x < hi; ++x) {
-        const int page = a.table[(size_t)b * a.max_pages + x / a.page_size];
-        const bool ok = page >= 0 && page < a.num_pages;
-        const long long at = (ok ? page : 0) * a.page_stride + g * a.head_stride +
-                             (x % a.page_size) * a.token_stride + lane * E;
-        const T *kp = static_cast<const T*>(a.k) + at, *vp = static_cast<const T*>(a.v) + at;
-        float s = 0.f;
+    constexpr int N = 4;   // keys at a time, their loads in flight together
+    for (int x0 = lo; x0 < hi; x0 += N) {
+        float k[N][E], v[N][E], s[N];
 #pragma unroll
-        for (int e = 0; e < E; ++e) s = fmaf(q[e], ok ? to_f(kp[e]) : 0.f, s);
-        s = warp_sum(s) * c;
-        const float mn = fmaxf(m, s), use = mn == -INFINITY ? 0.f : mn;
-        const float f = exp2f(m - use), w = exp2f(s - use + kLift);
-        l = l * f + w;
+        for (int i = 0; i < N; ++i) {
+            const int x = min(x0 + i, hi - 1);
+            const int page = a.table[(size_t)b * a.max_pages + x / a.page_size];
+            const bool ok = page >= 0 && page < a.num_pages;   // else the copies read zeros
+            const long long at = (ok ? page : 0) * a.page_stride + g * a.head_stride +
+                                 (x % a.page_size) * a.token_stride + lane * E;
+            const T *kp = static_cast<const T*>(a.k) + at, *vp = static_cast<const T*>(a.v) + at;
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], f, w * (ok ? to_f(vp[e]) : 0.f));
-        m = mn;
+            for (int e = 0; e < E; ++e) {
+                k[i][e] = ok ? to_f(kp[e]) : 0.f;
+                v[i][e] = ok ? to_f(vp[e]) : 0.f;
+            }
+        }
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            s[i] = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) s[i] = fmaf(q[e], k[i][e], s[i]);
+            s[i] = warp_sum(s[i]) * c;
+            top = fmaxf(top, s[i]);
+        }
+        const float use = top == -INFINITY ? 0.f : top, f = exp2f(m - use);
+        l *= f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] *= f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (x0 + i >= hi) break;
+            const float w = exp2f(s[i] - use + kLift);
+            l += w;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = fmaf(w, v[i][e], o[e]);
+        }
+        m = top;
     }
     m_out = m;
     l_out = l;
@@ -908,7 +931,7 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
                 l = mine_k == 0 ? fmaf(x.y, f_there, l * f_here) : fmaf(l, f_here, x.y * f_there);
                 m = M;
             }
-            bool odd = false;
+            bool odd = !(fabsf(l) < INFINITY);   // weights that outgrew fp32 before m could follow, or a NaN
             for (;;) {
                 const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
                 const float4* pt = reinterpret_cast<const float4*>(a.part_o + (size_t)there * DH * a.part_rows) + (live ? r : 0);

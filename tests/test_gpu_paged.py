@@ -280,6 +280,23 @@ def test_sharp_and_flat_scores(P, gain, scale, dt):
     compare(P, (q, kc, vc, table, cu, kv), scale=scale)
 
 
+@pytest.mark.parametrize("dt", [F16, BF16])
+@pytest.mark.parametrize("jump", [10.0, 60.0, 85.0, 200.0, 2000.0])
+@pytest.mark.parametrize("lens,H,G", [([(1, 700)], 4, 2), ([(200, 900)], 2, 2), ([(1, 3000), (40, 1000)], 4, 1)])
+def test_scores_that_jump(P, lens, H, G, dt, jump):
+    """Keys whose scores lie `jump` above all before them, in the midst of a tile and at its start, and small
+    values: weights relative to what was the maximum leave fp16's range, then fp32's."""
+    q, kc, vc, table, cu, kv = paged_case(lens, H, G, 64, dt, 16, seed=6)
+    q[..., 0] = 16.0
+    kc *= 0.1
+    vc *= 2.0 ** -6
+    for b, n in enumerate(kv):
+        for i, t in enumerate((256, 330, 512, 650)):
+            if t < n:
+                kc[table[b, t // 16].long(), :, t % 16, 0] = jump * (i + 1) / 2.0    # q . k / 8 = jump (i + 1)
+    compare(P, (q, kc, vc, table, cu, kv))
+
+
 def test_small_weights_keep_their_mass(P):
     """One key of weight 1 and 20000 of weight 2^-22 each: together 0.5 %."""
     n = 20001
