@@ -2,7 +2,8 @@
 
 The compute lives in ``libpi.so`` (hand-written CUDA for sm_103a behind the C
 ABI of ``include/pi.h``); :mod:`.binding` marshals torch CUDA tensors into it,
-and :mod:`.runtime` holds layers and workspaces for whole decode steps.
+:mod:`.runtime` holds layers and workspaces for whole decode steps, and
+:mod:`.paged` block tables and caches for serving over a paged cache.
 """
 from .binding import (PiError, desc_of, layer_desc, lib, library_path, pi_compact,  # noqa: F401
                       pi_debug_set_wait_timeout, pi_debug_wait_timeout, pi_ffn_layer, pi_ffn_stack, pi_last_device_status,

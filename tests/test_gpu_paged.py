@@ -479,3 +479,61 @@ def test_tables_store_and_attention_together(P):
             at += new[b]
     assert P.pi_last_device_status() == 0
     assert kv.tolist() == [52, 49] and count.item() == pages - 4 - 4
+
+
+def test_paged_cache_serves_chunks_and_decodes(P):
+    """Two layers behind one set of tables: prompts in chunks, then single tokens, a request that ends and one that
+    takes its row, a pool that runs dry; every step's rows match the dense reference over the same history."""
+    from activation_sparse_ffn_layer_gb300.paged import PagedCache
+    torch.manual_seed(11)
+    n, H, G, dh = 3, 6, 2, 64
+    cache = PagedCache(H, G, dh, n, 100, 40, 80, layers=2, page_size=16, num_pages=9, dtype=BF16, rope=P.rope_plan(dh, 16))
+    f = R.frequencies(16, 10000.0)
+    hist = [[([], []) for _ in range(2)] for _ in range(n)]
+    have = [0] * n
+    for step, (new, keep) in enumerate([([40, 7, 0], None), ([20, 30, 5], None), ([1, 1, 1], None), ([1, 0, 40], None),
+                                        ([1, 33, 1], [61 + 1, 0, 6]), ([1, 1, 40], None)]):
+        if keep is not None:
+            for b in range(n):
+                if keep[b] < have[b]:
+                    hist[b], have[b] = [([], []), ([], [])], 0
+        T = sum(new)
+        cache.begin(i32(new), T, max(new), None if keep is None else i32(keep))
+        served = [k > 0 or m == 0 for k, m in zip(cache.kv_len.tolist(), new)]
+        for layer in range(2):
+            q, k, v = torch.randn(T, H + 2 * G, dh, device="cuda").split([H, G, G], 1)
+            out = cache.attend(layer, q, k, v, torch.empty(T, H, dh, device="cuda").bfloat16())
+            at = 0
+            for b in range(n):
+                rows = slice(at, at + new[b])
+                at += new[b]
+                if new[b] == 0:
+                    continue
+                if not served[b]:
+                    assert bool((out[rows] == 0).all())
+                    continue
+                p = torch.arange(new[b], device="cuda") + have[b]
+                # the stored keys are read back, so that the reference attends to the same rounded values
+                slot = cache.slots[rows]
+                pg, off = slot // 16, slot % 16
+                kk, vv = cache.kcache[layer][pg, :, off], cache.vcache[layer][pg, :, off]
+                want, slack = R.rotate(k[rows], p, f, False)
+                u = R.half_step(BF16)
+                R.check(kk, want, u * want.abs() + (1 + u) * 1.4 * slack + 2.0 ** -25, "stored keys")
+                hist[b][layer][0].append(kk)
+                hist[b][layer][1].append(vv)
+                ks, vs = torch.cat(hist[b][layer][0]), torch.cat(hist[b][layer][1])
+                want, _, tol, _ = R.attention(cache.q[rows], ks.transpose(0, 1)[None], vs.transpose(0, 1)[None],
+                                              torch.zeros(1, 1, dtype=torch.int32, device="cuda"), [0, new[b]], [ks.shape[0]])
+                R.check(out[rows], want, tol, f"step {step} layer {layer} request {b}")
+        have = [h + m if s else h for h, m, s in zip(have, new, served)]
+        assert cache.cached.tolist() == have
+        # pages held and pages free make up the pool
+        assert int(cache.held.sum()) + cache.free_count.item() == 9
+    assert P.pi_last_device_status() == 0
+
+
+def test_paged_example_runs(P, capsys):
+    from activation_sparse_ffn_layer_gb300 import paged
+    paged.main(["--config", "c1", "--requests", "3", "--prompt", "70", "--chunk", "32", "--tokens", "3", "--layers", "2"])
+    assert "3 requests" in capsys.readouterr().out
