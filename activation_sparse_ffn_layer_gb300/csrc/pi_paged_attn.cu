@@ -271,6 +271,11 @@ PI_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
+PI_DEV uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 PI_DEV uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -677,10 +682,10 @@ PI_DEV int peek_gpu(const int* p) {
 // Adds the parts of rows r0 .. r0 + rows - 1 (at most 32) of an item's tile,
 // whose first token is tok0, columns c0 .. c0 + cols - 1, in block order and
 // writes the outputs: one warp, once all parts have arrived.  A lane keeps one row and every (32 / rows)-th group of 4 columns,
-// so that a few rows still use the whole warp, and asks for four column groups
-// of four parts, sixteen 16-byte values, at a time (the L2 latency is what a
-// join costs).
-template <typename T, int DH>
+// so that a few rows still use the whole warp, and asks for CS column groups of
+// KS parts at a time (what other blocks have just written takes 1500 cycles to
+// come).
+template <typename T, int DH, int CS, int KS>
 __device__ __noinline__ void join_parts(const PagedArgs& a, const Piece& p, bool pair, int w, int r0, int rows, int tok0, int c0, int cols) {
     const int lane = threadIdx.x & 31;
     const int span = rows > 16 ? 32 : rows > 8 ? 16 : rows > 4 ? 8 : rows > 2 ? 4 : rows;   // power of two
@@ -718,7 +723,6 @@ __device__ __noinline__ void join_parts(const PagedArgs& a, const Piece& p, bool
     const long long orow = p.cu + tok0 + tok;
     T* dst = static_cast<T*>(a.out) + orow * a.o_stride + (long long)head * DH;
     const int end = (c0 + cols) / 4;
-    constexpr int CS = 4, KS = 4;
     for (int c = c0 / 4 + cg; c < end; c += CS * step) {
         float4 v[CS];
 #pragma unroll
@@ -795,7 +799,8 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
         const int lo_most = __reduce_max_sync(FULL, lo), hi_least = __reduce_min_sync(FULL, hi);
         float m = -INFINITY, l = 0.f;
         bool fresh = true;    // some row of the warp has seen nothing yet
-        float over = 0.f;     // bf16: the last tile's weights, if they add up to too much
+        float over = 0.f;     // bf16: the last tile's weights, and whether some row's add up to too much
+        bool outgrown = false;
         int mine = 0;         // tiles of this piece that this group has done
         for (int t = pair ? 0 : w; t < nt; t += pair ? 1 : 2) {
             if (!warp_wait(&sh.sfull[w], ns & 1, ctl)) return;
@@ -826,7 +831,7 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
                     to = fmaxf(m, largest<kKeys>(s) * c);
                     if (!fresh) move = __any_sync(FULL, live && to > m + kGrow);
                 }
-                if (!kHalfType && __any_sync(FULL, over > kSum)) {
+                if (!kHalfType && outgrown) {
                     if (over > kSum) to = fmaxf(to, m + log2f(over) - kLift);
                     move = true;
                 }
@@ -862,7 +867,10 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
                 tc_before();
                 warp_arrive(&sh.pready[w][1]);
                 l += u + v;
-                if (!kHalfType) over = live ? u + v : 0.f;
+                if (!kHalfType) {
+                    over = live ? u + v : 0.f;
+                    outgrown = __any_sync(FULL, over > kSum);
+                }
             } else {
                 tc_before();
                 warp_arrive(&sh.pready[w][0]);
@@ -909,11 +917,11 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
             const int blk = (int)blockIdx.x * 2 + p.own;
             float* po = a.part_o + (size_t)blk * DH * a.part_rows;
             int* const arrivals = a.counters + p.block0 * 8 + warp;
-            // With two parts, and the other there already, nothing is written for
-            // others to read: the two are added on the spot (in block order, as
-            // join_parts does).
-            bool last = false;
-            if (p.parts == 2) {
+            // Of two parts, the one that finds the other there adds the two on the
+            // spot (in block order, as join_parts does); where both finish together,
+            // the last to arrive does so with its sums still in tensor memory.
+            bool spot = p.parts == 2, last = false;
+            if (spot) {
                 int seen = 0;
                 if (lane == 0) seen = peek_gpu(arrivals);
                 last = __shfl_sync(FULL, seen, 0) == 1;
@@ -922,63 +930,69 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
             const int there = (p.block0 + 1 - mine_k) * 2 + mine_k;   // the other's partial: its second slot is of part 0
             const float m_own = m, l_own = l;
             float f_here = 1.f, f_there = 0.f;
-            if (last) {
-                const float2 x = __ldcg(reinterpret_cast<const float2*>(
-                    a.part_ml + ((size_t)(there * 2 + (pair ? 0 : w)) * a.part_rows + (live ? r : 0)) * 2));
-                const float M = fmaxf(m, x.x), use = M == -INFINITY ? 0.f : M;
-                f_here = ex2(m - use);
-                f_there = ex2(x.x - use);
-                l = mine_k == 0 ? fmaf(x.y, f_there, l * f_here) : fmaf(l, f_here, x.y * f_there);
-                m = M;
-            }
-            bool odd = !(fabsf(l) < INFINITY);   // weights that outgrew fp32 before m could follow, or a NaN
             for (;;) {
+                m = m_own;
+                l = l_own;
+                if (last) {
+                    const float2 x = __ldcg(reinterpret_cast<const float2*>(
+                        a.part_ml + ((size_t)(there * 2 + (pair ? 0 : w)) * a.part_rows + (live ? r : 0)) * 2));
+                    const float M = fmaxf(m, x.x), use = M == -INFINITY ? 0.f : M;
+                    f_here = ex2(m - use);
+                    f_there = ex2(x.x - use);
+                    l = mine_k == 0 ? fmaf(x.y, f_there, l * f_here) : fmaf(l, f_here, x.y * f_there);
+                    m = M;
+                }
+                bool odd = !(fabsf(l) < INFINITY);   // weights that outgrew fp32 before m could follow, or a NaN
                 const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
                 const float4* pt = reinterpret_cast<const float4*>(a.part_o + (size_t)there * DH * a.part_rows) + (live ? r : 0);
+                // a whole item's 1 / l goes into what the groups' O count for
+                const bool both = own_any && other_any;
+                const unsigned from = own_any ? o_at : o_other;
+                const float g1 = (own_any ? f_own : f_other) * (whole ? inv : 1.f), g2 = f_other * (whole ? inv : 1.f);
+                const uint64_t gg1 = pair2(g1, g1), gg2 = pair2(g2, g2);
 #pragma unroll 1
                 for (int i = c0; i < c0 + cols; i += 32) {
                     float v[32];
-                    float4 y[8];
-                    uint32_t o[32];
+                    uint32_t o[32], q[32];
+                    tmem_ld32(from + (unsigned)i, o);
+                    if (both) tmem_ld32(o_other + (unsigned)i, q);
+                    tmem_wait_ld();
+                    tmem_loaded<32>(o);
+                    uint64_t check[2] = {0, 0};
+                    if (both) {
+                        tmem_loaded<32>(q);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2)
+                            split2(fma2(pair2(__uint_as_float(q[e]), __uint_as_float(q[e + 1])), gg2,
+                                        mul2(pair2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), gg1)), v[e], v[e + 1]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2)
+                            split2(mul2(pair2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), gg1), v[e], v[e + 1]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) check[(e >> 1) & 1] = fma2(pair2(v[e], v[e + 1]), 0, check[(e >> 1) & 1]);
+                    float z0, z1;
+                    split2(add2(check[0], check[1]), z0, z1);
+                    odd |= z0 + z1 != 0.f;   // NaN: some value is not finite
                     if (last) {
+                        float4 y[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) y[e] = __ldcg(pt + (size_t)(i / 4 + e) * a.part_rows);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = 0.f;
-                    if (own_any) {
-                        tmem_ld32(o_at + (unsigned)i, o);
-                        tmem_wait_ld();
-                        tmem_loaded<32>(o);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * f_own;
-                    }
-                    if (other_any) {
-                        tmem_ld32(o_other + (unsigned)i, o);
-                        tmem_wait_ld();
-                        tmem_loaded<32>(o);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = fmaf(__uint_as_float(o[e]), f_other, v[e]);
-                    }
-                    float check[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) check[e & 3] = fmaf(v[e], 0.f, check[e & 3]);
-                    odd |= (check[0] + check[1]) + (check[2] + check[3]) != 0.f;   // NaN: some value is not finite
-                    if (last) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
                             const float z = e % 4 == 0 ? y[e / 4].x : e % 4 == 1 ? y[e / 4].y : e % 4 == 2 ? y[e / 4].z : y[e / 4].w;
-                            v[e] = mine_k == 0 ? fmaf(z, f_there, fmaf(v[e], f_here, 0.f))
-                                               : fmaf(v[e], f_here, fmaf(z, f_there, 0.f));
+                            v[e] = (mine_k == 0 ? fmaf(z, f_there, fmaf(v[e], f_here, 0.f))
+                                                : fmaf(v[e], f_here, fmaf(z, f_there, 0.f))) * inv;
                         }
                     }
                     if (live && (whole || last)) {
                         T* dst = static_cast<T*>(a.out) + orow * a.o_stride + (long long)head * DH + i;
 #pragma unroll
                         for (int e = 0; e < 32; e += 8)
-                            *reinterpret_cast<uint4*>(dst + e) = make_uint4(
-                                pack2(v[e] * inv, v[e + 1] * inv, T()), pack2(v[e + 2] * inv, v[e + 3] * inv, T()),
-                                pack2(v[e + 4] * inv, v[e + 5] * inv, T()), pack2(v[e + 6] * inv, v[e + 7] * inv, T()));
+                            *reinterpret_cast<uint4*>(dst + e) =
+                                make_uint4(pack2(v[e], v[e + 1], T()), pack2(v[e + 2], v[e + 3], T()),
+                                           pack2(v[e + 4], v[e + 5], T()), pack2(v[e + 6], v[e + 7], T()));
                     } else if (live) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
@@ -986,43 +1000,45 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
                                 make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
                     }
                 }
-                if (!last || !__any_sync(FULL, live && odd)) break;
-                // a sum to be looked at row by row: the way over the workspace
-                last = false;
-                m = m_own;
-                l = l_own;
-            }
-            // rows whose sums are not finite, once more without the keys they do not see
-            const unsigned redo = __ballot_sync(FULL, live && odd);
-            __syncwarp();
-            for (unsigned left = redo; left; left &= left - 1) {
-                const int src = __ffs(left) - 1;
-                const int rlo = max(__shfl_sync(FULL, lo, src), p.j0 * kKeys);
-                const int rhi = min(__shfl_sync(FULL, hi, src), (p.j0 + p.nt) * kKeys);
-                const int rt = __shfl_sync(FULL, tok, src), rh = __shfl_sync(FULL, h, src), rr = __shfl_sync(FULL, r, src);
-                float rm, rl, ro[DH / 32];
-                careful_row<T, DH>(a, p.b, p.g, (long long)(p.cu + rt) * a.q_stride + (long long)(p.g * a.group + rh) * DH,
-                                   rlo, rhi, rm, rl, ro);
-                if (lane == src) {
-                    m = rm;
-                    l = rl;
+                // rows whose sums are not finite, once more without the keys they do not
+                // see (and by way of the workspace, where there is another part)
+                const unsigned redo = __ballot_sync(FULL, live && odd);
+                if (last && redo != 0) {
+                    spot = last = false;
+                    continue;
                 }
+                __syncwarp();
+                for (unsigned left = redo; left; left &= left - 1) {
+                    const int src = __ffs(left) - 1;
+                    const int rlo = max(__shfl_sync(FULL, lo, src), p.j0 * kKeys);
+                    const int rhi = min(__shfl_sync(FULL, hi, src), (p.j0 + p.nt) * kKeys);
+                    const int rt = __shfl_sync(FULL, tok, src), rh = __shfl_sync(FULL, h, src), rr = __shfl_sync(FULL, r, src);
+                    float rm, rl, ro[DH / 32];
+                    careful_row<T, DH>(a, p.b, p.g,
+                                       (long long)(p.cu + rt) * a.q_stride + (long long)(p.g * a.group + rh) * DH, rlo, rhi, rm,
+                                       rl, ro);
+                    if (lane == src) {
+                        m = rm;
+                        l = rl;
+                    }
 #pragma unroll
-                for (int e = 0; e < DH / 32; ++e) {
-                    const int col = lane * (DH / 32) + e;
-                    if (col < c0 || col >= c0 + cols) continue;
-                    if (whole)
-                        static_cast<T*>(a.out)[(long long)(p.cu + rt) * a.o_stride + (long long)(p.g * a.group + rh) * DH +
-                                               col] = T(rl > 0.f || rl != rl ? ro[e] / rl : 0.f);
-                    else
-                        po[((size_t)(col / 4) * a.part_rows + rr) * 4 + col % 4] = ro[e];
+                    for (int e = 0; e < DH / 32; ++e) {
+                        const int col = lane * (DH / 32) + e;
+                        if (col < c0 || col >= c0 + cols) continue;
+                        if (whole)
+                            static_cast<T*>(a.out)[(long long)(p.cu + rt) * a.o_stride +
+                                                   (long long)(p.g * a.group + rh) * DH + col] =
+                                T(rl > 0.f || rl != rl ? ro[e] / rl : 0.f);
+                        else
+                            po[((size_t)(col / 4) * a.part_rows + rr) * 4 + col % 4] = ro[e];
+                    }
                 }
-            }
-            float out_lse = l == 0.f ? -INFINITY : (m - kLift + log2f(l)) * kLn2;
-            if (whole || last) {
-                if (live && a.lse != nullptr && c0 == 0) a.lse[orow * a.heads + head] = out_lse;
-                if (last && lane == 0) *arrivals = 0;
-            } else {
+                if (whole || last) {
+                    if (live && a.lse != nullptr && c0 == 0)
+                        a.lse[orow * a.heads + head] = l == 0.f ? -INFINITY : (m - kLift + log2f(l)) * kLn2;
+                    if (last && lane == 0) *arrivals = 0;
+                    break;
+                }
                 float* ml = a.part_ml + ((size_t)(blk * 2 + (pair ? 0 : w)) * a.part_rows + r) * 2;
                 if (live) *reinterpret_cast<float2*>(ml) = make_float2(m, l);
                 // the lanes' stores happen before lane 0's arrival (__syncwarp, then
@@ -1030,12 +1046,18 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
                 __syncwarp();
                 int seen = 0;
                 if (lane == 0) seen = arrive_gpu(arrivals);
-                seen = __shfl_sync(FULL, seen, 0);
-                if (seen == p.parts - 1) {
-                    if (lane == 0) *arrivals = 0;
-                    const int rows = min(32, tile_rows - 32 * quad);
-                    join_parts<T, DH>(a, p, pair, w, 32 * quad, rows, tok0, c0, cols);
+                if (__shfl_sync(FULL, seen, 0) != p.parts - 1) break;
+                if (spot && redo == 0) {
+                    last = true;
+                    continue;
                 }
+                if (lane == 0) *arrivals = 0;
+                const int rows = min(32, tile_rows - 32 * quad);
+                if (p.parts <= 3)
+                    join_parts<T, DH, 8, 3>(a, p, pair, w, 32 * quad, rows, tok0, c0, cols);
+                else
+                    join_parts<T, DH, 4, 4>(a, p, pair, w, 32 * quad, rows, tok0, c0, cols);
+                break;
             }
         }
         if (!pair) {
