@@ -55,7 +55,7 @@ constexpr int kWalk = 16;              // items of a request that are counted on
 // What the work split counts, in units of half a microsecond or so: a key tile
 // for one tile of rows (memory), for two (products), an item besides its tiles.
 constexpr int kTileCost = 2, kPairCost = 3, kItemCost = 6;
-constexpr int kMinUnits = 5;           // of a block
+constexpr int kMinUnits = 5;          // of a block
 constexpr float kLift = 7.f;           // log2 of the factor that P, l and O share
 constexpr float kGrow = 8.f;           // fp16: growth (log2) of a maximum before m follows
 constexpr float kSum = 1073741824.f;   // bf16: sum of a tile's weights from which m follows
@@ -345,6 +345,12 @@ __device__ __noinline__ void careful_row(const PagedArgs& a, int b, int g, long 
     l_out = l;
 }
 
+// a / b for positive numbers, in 32 bits where they fit (a 64-bit division is a call)
+PI_DEV long long quotient(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return (unsigned)a / (unsigned)b;
+    return a / b;
+}
+
 // ------------------------------------------------------------ work list (warp 11)
 //
 // Units u of the block's range run through the items: kItemCost, then its
@@ -385,8 +391,8 @@ PI_DEV void list_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* qs
             p.parts = 1;
             p.own = from == 0;
             if (p.nt != nt) {   // blocks that own its first and its last tile
-                p.block0 = (int)(((i0 + kItemCost + 1) * G - 1) / U);
-                p.parts = (int)(((i0 + kItemCost + (nt - 1) * c + 1) * G - 1) / U) - p.block0 + 1;
+                p.block0 = (int)quotient((i0 + kItemCost + 1) * G - 1, U);
+                p.parts = (int)quotient((i0 + kItemCost + (nt - 1) * c + 1) * G - 1, U) - p.block0 + 1;
             }
             u = i0 + stop;
             off = 0;
@@ -1154,7 +1160,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_paged_attn(const __grid_co
     // (a part costs a join, the second tile runs beside the first)
     const int G = (int)min((long long)gridDim.x, (U + kMinUnits - 1) / kMinUnits);
     const int blk = blockIdx.x;
-    const long long u0 = G > 0 ? U * blk / G : 0, u1 = G > 0 ? U * (blk + 1) / G : 0;
+    const long long u0 = G > 0 ? quotient(U * blk, G) : 0, u1 = G > 0 ? quotient(U * (blk + 1), G) : 0;
     const bool work = blk < G;
     if (work && pre <= u0 && u0 < pre + own) {
         // this block's range starts in this thread's requests
@@ -1167,7 +1173,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_paged_attn(const __grid_co
                 left -= a.kv_heads * u;
                 continue;
             }
-            const int g = (int)(left / u);
+            const int g = (int)quotient(left, u);
             left -= g * u;
             // the item: the last one that starts at or before `left`
             const int d = 2 * a.tile_tokens;
