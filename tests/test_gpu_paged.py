@@ -537,3 +537,39 @@ def test_paged_example_runs(P, capsys):
     from activation_sparse_ffn_layer_gb300 import paged
     paged.main(["--config", "c1", "--requests", "3", "--prompt", "70", "--chunk", "32", "--tokens", "3", "--layers", "2"])
     assert "3 requests" in capsys.readouterr().out
+
+
+def test_a_captured_decode_step_goes_on(P):
+    """A decode step (tables, store, attention, state in place) replayed as a graph: every replay's outputs are the
+    eager cache's bits, over page borders and past the end of the pool."""
+    from activation_sparse_ffn_layer_gb300.paged import PagedCache
+    n, H, G, dh, T = 3, 8, 2, 64, 20
+    make = lambda: PagedCache(H, G, dh, n, 64, T, 2 * T, page_size=16, num_pages=8, rope=P.rope_plan(dh))  # noqa: E731
+    a, b = make(), make()
+    torch.manual_seed(3)
+    first = torch.randn(T + 10 + 3, H + 2 * G, dh, device="cuda").half()
+    x = torch.randn(n, H + 2 * G, dh, device="cuda").half()
+    outs = []
+    for c in (a, b):
+        c.begin(i32([T, 10, 3]), T + 13, T)
+        q, k, v = first.split([H, G, G], 1)
+        c.attend(0, q, k, v, torch.empty(T + 13, H, dh, device="cuda").half())
+    out = torch.empty(n, H, dh, device="cuda").half()
+    ones = i32([1] * n)
+
+    def step(c, o):
+        c.begin(ones, n, 1)
+        c.attend(0, *x.split([H, G, G], 1), o)
+
+    step(b, out.clone())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(b, out)
+    eager = torch.empty_like(out)
+    step(a, eager)
+    for i in range(40):
+        x.copy_(torch.randn(x.shape, generator=torch.Generator().manual_seed(i)))
+        graph.replay()
+        step(a, eager)
+        assert torch.equal(out, eager) and torch.equal(a.cached, b.cached) and torch.equal(a.slots[:n], b.slots[:n]), i
+    assert int((a.kv_len == 0).sum()) > 0 and P.pi_last_device_status() == 0
