@@ -3,7 +3,8 @@
 // The query heads that share a KV head go through its keys together: a tile of
 // rows is as many whole tokens as fit 128 rows (row = token * group + head in
 // the group), so one pass over the keys serves the whole group.  An item is up
-// to two such tiles of one request and KV head; its keys come in tiles of 128.  For a tile, on the tcgen05 tensor cores,
+// to two such tiles of one request and KV head; its keys come in tiles of 128.
+// For a tile, on the tcgen05 tensor cores,
 //     S = Q K^T         (fp16/bf16 products, fp32 sums in tensor memory)
 //     P = 2^(c S - m)   (a thread per row; running m and l = sum P)
 //     O += P V          (P as the A operand in tensor memory)
@@ -16,11 +17,10 @@
 // survive the rounding.
 //
 // Warps: 0-3 and 4-7 softmax (a thread per row), 8 key copies, 9 MMA issue, 10
-// value copies, 11 the work list and the query copies.  Items of two
-// tiles of rows give each softmax group one (both use every key tile: "pair");
-// smaller items, decode steps among them, give the two groups alternate key
-// tiles and merge at the end: one group's exponentials run beside the other's
-// products.
+// value copies, 11 the work list and the query copies.  Items of two tiles of
+// rows give each softmax group one (both use every key tile: "pair"); smaller
+// items, decode steps among them, give the two groups alternate key tiles and
+// merge at the end: one group's exponentials run beside the other's products.
 //
 // Work split: the (item x key tile) space is cut into equal contiguous ranges
 // per block, whatever the lengths; an item cut by a border leaves unnormalised
@@ -948,7 +948,9 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
                     l = mine_k == 0 ? fmaf(x.y, f_there, l * f_here) : fmaf(l, f_here, x.y * f_there);
                     m = M;
                 }
-                bool odd = !(fabsf(l) < INFINITY);   // weights that outgrew fp32 before m could follow, or a NaN
+                // weights that outgrew fp32 before m could follow, or a NaN, in this part
+                // (the other has been looked at by its block)
+                bool odd = !(fabsf(l_own) < INFINITY);
                 const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
                 const float4* pt = reinterpret_cast<const float4*>(a.part_o + (size_t)there * DH * a.part_rows) + (live ? r : 0);
                 // a whole item's 1 / l goes into what the groups' O count for

@@ -573,3 +573,29 @@ def test_a_captured_decode_step_goes_on(P):
         step(a, eager)
         assert torch.equal(out, eager) and torch.equal(a.cached, b.cached) and torch.equal(a.slots[:n], b.slots[:n]), i
     assert int((a.kv_len == 0).sum()) > 0 and P.pi_last_device_status() == 0
+
+
+@pytest.mark.parametrize("H,G,lens", [(4, 4, [(1, 3000), (1, 2900)]), (2, 2, [(300, 2000)]), (8, 1, [(1, 20000)])])
+@pytest.mark.parametrize("which", [1, 2])
+def test_cut_items_with_bad_values(P, H, G, lens, which):
+    """A non-finite key or value in one part of items that many blocks share: those rows are not finite, the others
+    right, call after call on one workspace, and so is a good call after them."""
+    good = paged_case(lens, H, G, 64, F16, 16, seed=12)
+    q, kc, vc, table, cu, kv = good
+    d, pg = P.paged_desc(H, len(kv), q.shape[0], max(n for n, _ in lens), table.shape[1]), P.page_desc(kc, vc)
+    ws = torch.zeros(P.pi_paged_workspace_bytes(d, pg), dtype=torch.uint8, device="cuda")
+    want = run_attn(P, *good, ws=ws)
+    for at in (3, 700, kv[0] - lens[0][0] - 1):
+        bad = [x.clone() if torch.is_tensor(x) else x for x in good]
+        bad[which][table[0, at // 16].long(), 0, at % 16, 5] = math.nan
+        for _ in range(6):
+            out, lse = run_attn(P, *bad, ws=ws)
+            see = torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda")
+            see[:lens[0][0], :H // G] = True
+            hit = out[see][:, 5] if which == 2 else out[see]
+            assert bool(torch.isnan(hit).all())
+            # rows without it: the same keys in the same parts, so the same bits
+            assert torch.equal(out[~see], want[0][~see]) and torch.equal(lse[~see], want[1][~see])
+        again = run_attn(P, *good, ws=ws)
+        assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+    assert P.pi_last_device_status() == 0
