@@ -599,3 +599,29 @@ def test_cut_items_with_bad_values(P, H, G, lens, which):
         again = run_attn(P, *good, ws=ws)
         assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
     assert P.pi_last_device_status() == 0
+
+
+@pytest.mark.parametrize("lens,H,G", [([(1, 5000), (1, 300)], 8, 2), ([(300, 4000)], 4, 2)])
+def test_waits_that_run_out(P, lens, H, G):
+    """With a wait limit of 1 ns the first wait that is not satisfied at once gives up: the blocks wait for their own
+    copies and products, free their tensor memory and return, and the status is PI_ERR_TIMEOUT.  After a zero fill of
+    the workspace the same call gives the bits of a clean run."""
+    case = paged_case(lens, H, G, 128, F16, 16, seed=13)
+    q, kc, vc, table, cu, kv = case
+    d, pg = P.paged_desc(H, len(kv), q.shape[0], max(n for n, _ in lens), table.shape[1]), P.page_desc(kc, vc)
+    ws = torch.zeros(P.pi_paged_workspace_bytes(d, pg), dtype=torch.uint8, device="cuda")
+    want = run_attn(P, *case, ws=ws)
+    assert P.pi_last_device_status() == 0
+    for limit in (1, 3000):
+        P.pi_debug_set_wait_timeout(limit)
+        try:
+            run_attn(P, *case, ws=ws)
+            torch.cuda.synchronize()
+        finally:
+            P.pi_debug_set_wait_timeout(0)
+        assert P.pi_last_device_status() in ((4,) if limit == 1 else (0, 4))
+        ws.zero_()
+        for _ in range(3):
+            got = run_attn(P, *case, ws=ws)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert P.pi_last_device_status() == 0
