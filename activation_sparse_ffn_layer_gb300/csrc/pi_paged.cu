@@ -26,7 +26,9 @@ namespace {
 // page x - count, still in its row's table entry (releasing rows' entries are
 // not overwritten, free-list entries below the old count are not written).
 //
-// Bound by latency (a few KB to a MB of traffic).  Every block scans all rows
+// Bound by latency, the chain from lengths over prefixes to table entries and
+// slots: 4.7 us for 8 decoding rows, 10.4 us for 2048 rows with 60 thousand
+// tokens (1.6 MB, 0.24 us of HBM).  Every block scans all rows
 // (three block prefixes) and takes its share of the writes.  Small steps are
 // one block.  Large ones are two grids: kTabMoves, as wide as the writes need,
 // writes pages, slots and positions; kTabState, one block, writes held_out and
@@ -250,8 +252,10 @@ __global__ void __launch_bounds__(kTabThreads) k_block_tables(const TablesArgs a
 // 16-byte stores, so the kernel is bound by HBM; a block takes one token (a
 // share of its units where there are many), asks for all its loads first,
 // and computes the token's cos and sin once for all heads while they are on
-// their way.
-constexpr int kRopeUnits = 2;   // units per thread (4: 28.6 against 26.2 us for 1999 tokens, the last wave's; the same for 16384)
+// their way.  16384 bf16 tokens (64 + 2 x 8 heads of 128): 103 us, 6.5 TB/s;
+// 1999 fp32 tokens (32 + 2 x 32 heads) into fp16: 26.2 us, 5.6 TB/s; 32
+// decoding tokens: 2.5 us, a launch.
+constexpr int kRopeUnits = 2;   // units per thread (1: 134 us for the 16384 tokens, 4: 104, and 28.6 for the 1999: the last wave)
 constexpr int kRopeMaxPairs = 64;
 
 struct RopeArgs {
@@ -491,10 +495,15 @@ pi_status pi_block_tables(const pi_tables_desc* desc, const int32_t* cached_len,
                  desc->num_pages, desc->max_pages, desc->max_tokens, status_word()};
     if (a.status == nullptr) return PI_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // writes to expect: a token each, and some tens of moved pages a row
-    const long long writes = desc->max_tokens + 32ll * desc->batch;
+    // writes to expect: a token each, and a few moved pages a row (a decoding
+    // row moves one in page_size steps, a row that ends gives all back).  One
+    // block takes 4.3 us and 1.2 more per 1024 tokens, two grids 6.8 us: 5.9
+    // against 6.7 at 2048 tokens of 64 rows, 4.9 against 7.0 at 512 decoding
+    // rows (6.6 against 7.1 if each gives back 4 pages), 10 against 6.9 at 8192
+    // tokens, 187 against 10.4 at 2048 rows with 60 thousand tokens.
+    const long long writes = desc->max_tokens + 4ll * desc->batch;
     cudaError_t e;
-    if (writes <= 4 * kTabThreads) {
+    if (writes <= 5 * kTabThreads / 2) {
         e = launch_tables<kTabAll>(a, 1, s);
     } else {
         e = launch_tables<kTabMoves>(a, (int)std::min<long long>(128, (writes + kTabThreads - 1) / kTabThreads), s);

@@ -26,6 +26,22 @@
 // per block, whatever the lengths; an item cut by a border leaves unnormalised
 // partials (m, l, O) in the workspace, and the block that arrives last adds
 // them in block order (the order is fixed, who does it is not: same bits).
+//
+// Bounds and figures (GB300, 64 query and 8 KV heads of 128 unless said):
+//  - few rows per key (decoding): HBM.  Four sequences with 120-131 thousand
+//    keys, bf16: 300 us, 6.9 TB/s.  32 sequences with 500-8000 keys, fp16: 82
+//    us, 5.6 TB/s; DRAM reads are 1.006 of the keys and values, the start and
+//    the joins of cut items are the rest.  One sequence with 1001 keys: 13.8
+//    us of latency, two key tiles per block and a join.
+//  - many rows (a chunk of 4096 tokens behind 12288, bf16): the tensor cores.
+//    1.11-1.19 ms, 1.62-1.73 PFLOP/s.  Two tiles of rows keep them busy for
+//    2048 cycles per key tile; the softmax of both takes 1350 beside that
+//    (1170 of them for 2 x 128 x 128 exponentials), the copies of a tile's
+//    eight pages 600 on each of two warps.
+//  - prompts of some thousand tokens and mixed steps: 28 us for a prompt of
+//    1999 tokens (12 heads of 64), 117 us for 16 sequences that decode or take
+//    100-700 tokens (32 heads, window of 2000).  A block has its SM to itself,
+//    so nothing hides its start, its items' outputs and the joins.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -51,11 +67,15 @@ constexpr int kTileRows = 128;         // rows of a tile at most
 constexpr int kPagedThreads = 384;
 constexpr int kListDepth = 4;          // pieces the work list runs ahead
 constexpr int kConsumers = 11;         // warps that read the work list: all but the one that writes it
-constexpr int kWalk = 16;              // items of a request that are counted one by one, not by formula
+constexpr int kWalk = 16;              // items of a request that are counted one by one, not by formula (a prompt of
+                                       // 1999 tokens: 28.4 us so, 31.3 by formula; the walk grows with the prompt)
 // What the work split counts, in units of half a microsecond or so: a key tile
 // for one tile of rows (memory), for two (products), an item besides its tiles.
+// Without these weights a mixed step of 16 sequences that decode or take
+// 100-700 tokens took 131 us instead of 117; item costs of 4 to 12 and pair costs of 3 to 5 lie
+// within the noise of each other.
 constexpr int kTileCost = 2, kPairCost = 3, kItemCost = 6;
-constexpr int kMinUnits = 5;          // of a block
+constexpr int kMinUnits = 5;          // of a block: two key tiles (one sequence with 1001 keys 13.8 us; 8 units 14.3, 12 units 16.9)
 constexpr float kLift = 7.f;           // log2 of the factor that P, l and O share
 constexpr float kGrow = 8.f;           // fp16: growth (log2) of a maximum before m follows
 constexpr float kSum = 1073741824.f;   // bf16: sum of a tile's weights from which m follows
