@@ -70,12 +70,16 @@ constexpr int kConsumers = 11;         // warps that read the work list: all but
 constexpr int kWalk = 16;              // items of a request that are counted one by one, not by formula (a prompt of
                                        // 1999 tokens: 28.4 us so, 31.3 by formula; the walk grows with the prompt)
 // What the work split counts, in units of half a microsecond or so: a key tile
-// for one tile of rows (memory), for two (products), an item besides its tiles.
-// Without these weights a mixed step of 16 sequences that decode or take
-// 100-700 tokens took 131 us instead of 117; item costs of 4 to 12 and pair costs of 3 to 5 lie
-// within the noise of each other.
-constexpr int kTileCost = 2, kPairCost = 3, kItemCost = 6;
-constexpr int kMinUnits = 5;          // of a block: two key tiles (one sequence with 1001 keys 13.8 us; 8 units 14.3, 12 units 16.9)
+// for one tile of rows (memory), for two (products), an item besides its tiles
+// (kLead before them, the rest after: a border that falls there does not cut the
+// item).  Without these weights a mixed step of 16 sequences that decode or take
+// 100-700 tokens took 131 us instead of 117.  Over 18 cases of all kinds the
+// geometric mean is 31.1 us so, 31.7 with 6 units all before the tiles, 31.3
+// with 3 + 3 or 5 + 5, 30.9 with 6 + 6 (one sequence with 1001 keys the same,
+// 32 decoding ones 83 instead of 80.5); pair costs of 3.5 and 4 add 1 or 2 %.
+constexpr int kTileCost = 2, kPairCost = 3, kItemCost = 8, kLead = 4;
+constexpr int kMinUnits = 5;           // of a block: two key tiles (one sequence with 1001 keys 13.8 us; 8 units 14.3, 12
+                                       // units 16.9)
 constexpr float kLift = 7.f;           // log2 of the factor that P, l and O share
 constexpr float kGrow = 8.f;           // fp16: growth (log2) of a maximum before m follows
 constexpr float kSum = 1073741824.f;   // bf16: sum of a tile's weights from which m follows
@@ -373,8 +377,8 @@ PI_DEV long long quotient(long long a, long long b) {
 
 // ------------------------------------------------------------ work list (warp 11)
 //
-// Units u of the block's range run through the items: kItemCost, then its
-// tiles' costs.  A block does the tiles that begin in its range (a range is
+// Units u of the block's range run through the items: kLead, the tiles' costs,
+// the rest of kItemCost.  A block does the tiles that begin in its range (a range is
 // longer than a tile's cost, so every block between an item's first and last
 // has one).  With a piece go its
 // query tiles, once the scores of the piece before are done; tokens past the
@@ -397,7 +401,7 @@ PI_DEV void list_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* qs
             const int c = tile_cost(a, toks);
             const long long i0 = u - off;   // the item's first unit
             const int stop = (int)min((long long)(kItemCost + nt * c), u1 - i0);
-            const int from = (max(off - kItemCost, 0) + c - 1) / c, to = (max(stop - kItemCost, 0) + c - 1) / c;
+            const int from = min((max(off - kLead, 0) + c - 1) / c, nt), to = min((max(stop - kLead, 0) + c - 1) / c, nt);
             p.nt = to - from;
             p.j0 = lo / kKeys + from;
             p.lo = lo;
@@ -411,8 +415,8 @@ PI_DEV void list_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* qs
             p.parts = 1;
             p.own = from == 0;
             if (p.nt != nt) {   // blocks that own its first and its last tile
-                p.block0 = (int)quotient((i0 + kItemCost + 1) * G - 1, U);
-                p.parts = (int)quotient((i0 + kItemCost + (nt - 1) * c + 1) * G - 1, U) - p.block0 + 1;
+                p.block0 = (int)quotient((i0 + kLead + 1) * G - 1, U);
+                p.parts = (int)quotient((i0 + kLead + (nt - 1) * c + 1) * G - 1, U) - p.block0 + 1;
             }
             u = i0 + stop;
             off = 0;
@@ -1180,7 +1184,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_paged_attn(const __grid_co
     const unsigned tmem = sh.tmem;
     // blocks with work: about two tiles each at least, one for each softmax group
     // (a part costs a join, the second tile runs beside the first)
-    const int G = (int)min((long long)gridDim.x, (U + kMinUnits - 1) / kMinUnits);
+    const int G = (int)min((long long)gridDim.x, max(U / kMinUnits, U > 0 ? 1ll : 0ll));
     const int blk = blockIdx.x;
     const long long u0 = G > 0 ? quotient(U * blk, G) : 0, u1 = G > 0 ? quotient(U * (blk + 1), G) : 0;
     const bool work = blk < G;
