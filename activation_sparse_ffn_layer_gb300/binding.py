@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
-from typing import Optional
+from typing import Optional, Tuple
 
 import torch
 
@@ -169,12 +169,13 @@ def _ptr(t: Optional[torch.Tensor]):
 # handle of a device's current stream without a torch.cuda.Stream object around
 # it (3 us a call on a Grace core); the public way where torch has no such call
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)   # torch.cuda.current_device without its check for a first use
 
 
 def _stream():
-    if _raw_stream is None:
+    if _raw_stream is None or _raw_device is None:
         return torch.cuda.current_stream().cuda_stream
-    return _raw_stream(torch.cuda.current_device())
+    return _raw_stream(_raw_device())
 
 
 def _check(fn: str, st: int):
@@ -400,14 +401,15 @@ def _flat(t: torch.Tensor, dtype: torch.dtype, least: int, name: str) -> int:
     return t.data_ptr()
 
 
-def _rows(t: torch.Tensor, heads: int, head_dim: int, name: str) -> int:
+def _rows(t: torch.Tensor, heads: int, head_dim: int, name: str) -> Tuple[int, int]:
     """Checks a [tokens, heads, head_dim] CUDA tensor whose tokens may be apart;
-    returns the elements between tokens."""
+    returns its tokens and the elements between them."""
     shape, stride = t.shape, t.stride()
     if not t.is_cuda or len(shape) != 3 or shape[1] != heads or shape[2] != head_dim or stride[2] != 1 or \
             (stride[1] != head_dim and heads > 1):
         raise ValueError(f"{name}: expected a CUDA tensor [tokens, {heads}, {head_dim}] with its heads one after another")
-    return stride[0] if shape[0] > 1 else heads * head_dim
+    n = shape[0]
+    return n, (stride[0] if n > 1 else heads * head_dim)
 
 
 def tables_desc(batch: int, page_size: int, num_pages: int, max_pages: int, max_tokens: int) -> pi_tables_desc:
@@ -483,22 +485,24 @@ def pi_rope_store(plan, cache, q, k, v, positions, slots, q_out, kcache, vcache)
     x = q if q is not None else k
     if x is None:
         raise ValueError("expected q or k")
-    T, dh, kind, heads = x.shape[0], cache.head_dim, _DTYPES.get(x.dtype, -1), 1
+    dh, dtype, heads = cache.head_dim, x.dtype, 1
     qs = ks = vs = os_ = 0
     qp = op = kp = vp = sp = kc = vc = None
     if q is not None:
         heads = q.shape[1]
-        qs, os_ = _rows(q, heads, dh, "q"), _rows(q_out, heads, dh, "q_out")
-        if q_out.shape[0] < T or _DTYPES.get(q_out.dtype) != cache.dtype:
+        (T, qs), (n, os_) = _rows(q, heads, dh, "q"), _rows(q_out, heads, dh, "q_out")
+        if n < T or _DTYPES.get(q_out.dtype) != cache.dtype:
             raise ValueError("q_out: expected the shape of q and the type of the cache")
         qp, op = q.data_ptr(), q_out.data_ptr()
     if k is not None:
-        ks, vs = _rows(k, cache.kv_heads, dh, "k"), _rows(v, cache.kv_heads, dh, "v")
-        if k.shape[0] != T or v.shape[0] != T or k.dtype is not x.dtype or v.dtype is not x.dtype:
+        (n, ks), (m, vs) = _rows(k, cache.kv_heads, dh, "k"), _rows(v, cache.kv_heads, dh, "v")
+        if q is None:
+            T = n
+        if n != T or m != T or k.dtype is not dtype or v.dtype is not dtype:
             raise ValueError("k, v: expected the tokens and the type of q")
         kp, vp, sp = k.data_ptr(), v.data_ptr(), _flat(slots, torch.int64, T, "slots")
         kc, vc = _cache(cache, kcache, "kcache"), _cache(cache, vcache, "vcache")
-    d = pi_qkv_desc(T, heads, kind, qs, ks, vs, os_)
+    d = pi_qkv_desc(T, heads, _DTYPES.get(dtype, -1), qs, ks, vs, os_)
     _check("pi_rope_store", lib().pi_rope_store(C.byref(plan), C.byref(cache), C.byref(d), qp, kp, vp,
                                                 _flat(positions, torch.int32, T, "positions"), sp, op, kc, vc,
                                                 _stream()))
@@ -519,8 +523,8 @@ def pi_paged_attn(desc, cache, q, kcache, vcache, block_table, cu_new, kv_len, o
     the paged cache into out (same shape and type); lse [max_tokens, heads]
     fp32 or None; workspace uint8, zero-filled before its first use."""
     T, H, B, i32 = desc.max_tokens, desc.heads, desc.batch, torch.int32
-    qs, os_ = _rows(q, H, cache.head_dim, "q"), _rows(out, H, cache.head_dim, "out")
-    if q.shape[0] < T or out.shape[0] < T or _DTYPES.get(q.dtype) != cache.dtype or out.dtype is not q.dtype:
+    (n, qs), (m, os_) = _rows(q, H, cache.head_dim, "q"), _rows(out, H, cache.head_dim, "out")
+    if n < T or m < T or _DTYPES.get(q.dtype) != cache.dtype or out.dtype is not q.dtype:
         raise ValueError("q, out: expected max_tokens rows of the cache's type")
     _check("pi_paged_attn", lib().pi_paged_attn(
         C.byref(desc), C.byref(cache), q.data_ptr(), qs, _cache(cache, kcache, "kcache"),
