@@ -506,7 +506,9 @@ pi_status pi_block_tables(const pi_tables_desc* desc, const int32_t* cached_len,
     if (writes <= 5 * kTabThreads / 2) {
         e = launch_tables<kTabAll>(a, 1, s);
     } else {
-        e = launch_tables<kTabMoves>(a, (int)std::min<long long>(128, (writes + kTabThreads - 1) / kTabThreads), s);
+        // wide enough for tens of moved pages a row (2048 rows: 10.4 us so, 11.4 with blocks for 4 a row)
+        const long long most = desc->max_tokens + 32ll * desc->batch;
+        e = launch_tables<kTabMoves>(a, (int)std::min<long long>(128, (most + kTabThreads - 1) / kTabThreads), s);
         if (e == cudaSuccess) e = launch_tables<kTabState>(a, 1, s);
     }
     return e == cudaSuccess ? PI_OK : PI_ERR_CUDA;
