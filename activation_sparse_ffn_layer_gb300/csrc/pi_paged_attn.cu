@@ -711,12 +711,16 @@ PI_DEV int peek_gpu(const int* p) {
 
 // Adds the parts of rows r0 .. r0 + rows - 1 (at most 32) of an item's tile,
 // whose first token is tok0, columns c0 .. c0 + cols - 1, in block order and
-// writes the outputs: one warp, once all parts have arrived.  A lane keeps one row and every (32 / rows)-th group of 4 columns,
-// so that a few rows still use the whole warp, and asks for CS column groups of
-// KS parts at a time (what other blocks have just written takes 1500 cycles to
-// come).
-template <typename T, int DH, int CS, int KS>
-__device__ __noinline__ void join_parts(const PagedArgs& a, const Piece& p, bool pair, int w, int r0, int rows, int tok0, int c0, int cols) {
+// writes the outputs: one warp, once all parts have arrived.  A lane keeps one
+// row and every (32 / rows)-th group of 4 columns, so that a few rows still use
+// the whole warp, and asks for CS column groups of KS parts and for their m and
+// l at a time (what other blocks have just written takes 1500 cycles to come;
+// one sequence with 1001 keys: 13.3 us so, 14.0 with m and l fetched first; 24
+// loads at a time spill, here or in the caller).
+template <typename T, int DH>
+__device__ __noinline__ void join_parts(const PagedArgs& a, const Piece& p, bool pair, int w, int r0, int rows, int tok0,
+                                        int c0, int cols) {
+    constexpr int CS = 4, KS = 4;
     const int lane = threadIdx.x & 31;
     const int span = rows > 16 ? 32 : rows > 8 ? 16 : rows > 4 ? 8 : rows > 2 ? 4 : rows;   // power of two
     const int tr = r0 + (lane & (span - 1));   // row of the tile
@@ -729,30 +733,12 @@ __device__ __noinline__ void join_parts(const PagedArgs& a, const Piece& p, bool
                        (size_t)(pair ? 0 : w) * a.part_rows + r;
     const float4* po = reinterpret_cast<const float4*>(a.part_o) + (size_t)p.block0 * o_step + r;
     const size_t ml_first = (size_t)2 * a.part_rows, o_first = (size_t)DH / 4 * a.part_rows;
-    float M = -INFINITY, L = 0.f;
-    for (int k0 = 0; k0 < p.parts; k0 += 8) {
-        float2 x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int k = min(k0 + i, p.parts - 1);
-            x[i] = __ldcg(ml + k * ml_step + (k == 0 ? ml_first : 0));
-            if (k0 + i >= p.parts) x[i] = make_float2(-INFINITY, 0.f);
-        }
-        float top = M;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, x[i].x);
-        const float use = top == -INFINITY ? 0.f : top;
-        L *= ex2(M - use);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) L = fmaf(x[i].y, ex2(x[i].x - use), L);
-        M = top;
-    }
-    const float use = M == -INFINITY ? 0.f : M;
-    const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
     const int tok = tr / a.group, head = p.g * a.group + tr - tok * a.group;
     const long long orow = p.cu + tok0 + tok;
     T* dst = static_cast<T*>(a.out) + orow * a.o_stride + (long long)head * DH;
     const int end = (c0 + cols) / 4;
+    float M = -INFINITY, L = 0.f, use = 0.f, inv = 0.f;
+    bool first = true;
     for (int c = c0 / 4 + cg; c < end; c += CS * step) {
         float4 v[CS];
 #pragma unroll
@@ -760,20 +746,35 @@ __device__ __noinline__ void join_parts(const PagedArgs& a, const Piece& p, bool
         for (int k0 = 0; k0 < p.parts; k0 += KS) {
             // loads without conditions, so that all of them are in flight at once
             // (past the end: once more the last one, left out below)
-            float f[KS];
+            float2 s[KS];
             float4 x[KS][CS];
 #pragma unroll
             for (int i = 0; i < KS; ++i) {
                 const int k = min(k0 + i, p.parts - 1);
-                f[i] = __ldcg(ml + k * ml_step + (k == 0 ? ml_first : 0)).x;
+                s[i] = __ldcg(ml + k * ml_step + (k == 0 ? ml_first : 0));
                 const float4* src = po + k * o_step + (k == 0 ? o_first : 0);
 #pragma unroll
                 for (int j = 0; j < CS; ++j) x[i][j] = __ldcg(src + (size_t)min(c + j * step, end - 1) * a.part_rows);
             }
+            if (first) {   // m and l of all parts, while those are on their way
+                first = false;
+                auto add = [&](float2 y) {
+                    const float top = fmaxf(M, y.x);
+                    use = top == -INFINITY ? 0.f : top;
+                    L = fmaf(y.y, ex2(y.x - use), L * ex2(M - use));
+                    M = top;
+                };
+#pragma unroll
+                for (int i = 0; i < KS; ++i)
+                    if (i < p.parts) add(s[i]);
+#pragma unroll 1
+                for (int k = KS; k < p.parts; ++k) add(__ldcg(ml + k * ml_step));
+                inv = L > 0.f || L != L ? 1.f / L : 0.f;
+            }
 #pragma unroll
             for (int i = 0; i < KS; ++i) {
                 if (k0 + i >= p.parts) break;
-                const float g = ex2(f[i] - use);
+                const float g = ex2(s[i].x - use);
 #pragma unroll
                 for (int j = 0; j < CS; ++j) {
                     v[j].x = fmaf(x[i][j].x, g, v[j].x);
@@ -1085,10 +1086,7 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
                 }
                 if (lane == 0) *arrivals = 0;
                 const int rows = min(32, tile_rows - 32 * quad);
-                if (p.parts <= 3)
-                    join_parts<T, DH, 8, 3>(a, p, pair, w, 32 * quad, rows, tok0, c0, cols);
-                else
-                    join_parts<T, DH, 4, 4>(a, p, pair, w, 32 * quad, rows, tok0, c0, cols);
+                join_parts<T, DH>(a, p, pair, w, 32 * quad, rows, tok0, c0, cols);
                 break;
             }
         }
