@@ -29,17 +29,19 @@
 //
 // Bounds and figures (GB300, 64 query and 8 KV heads of 128 unless said):
 //  - few rows per key (decoding): HBM.  Four sequences with 120-131 thousand
-//    keys, bf16: 300 us, 6.9 TB/s.  32 sequences with 500-8000 keys, fp16: 82
-//    us, 5.6 TB/s; DRAM reads are 1.006 of the keys and values, the start and
-//    the joins of cut items are the rest.  One sequence with 1001 keys: 13.8
+//    keys, bf16: 300 us, 6.9 TB/s.  32 sequences with 500-8000 keys, fp16: 80
+//    us, 5.7 TB/s; DRAM reads are 1.006 of the keys and values, the start and
+//    the joins of cut items are the rest.  One sequence with 1001 keys: 13.3
 //    us of latency, two key tiles per block and a join.
 //  - many rows (a chunk of 4096 tokens behind 12288, bf16): the tensor cores.
-//    1.11-1.19 ms, 1.62-1.73 PFLOP/s.  Two tiles of rows keep them busy for
-//    2048 cycles per key tile; the softmax of both takes 1350 beside that
-//    (1170 of them for 2 x 128 x 128 exponentials), the copies of a tile's
-//    eight pages 600 on each of two warps.
+//    1.11-1.20 ms, 1.60-1.73 PFLOP/s.  Two tiles of rows keep them busy for
+//    2048 cycles per key tile, which takes 2900: each group's chain of S, the
+//    softmax (1350 for both, 1170 of them for 2 x 128 x 128 exponentials) and
+//    P V is longer than the other's products beside it, and tensor memory has
+//    no room for a second S.  The copies of a tile's eight pages take 600 on
+//    each of two warps.
 //  - prompts of some thousand tokens and mixed steps: 28 us for a prompt of
-//    1999 tokens (12 heads of 64), 117 us for 16 sequences that decode or take
+//    1999 tokens (12 heads of 64), 119 us for 16 sequences that decode or take
 //    100-700 tokens (32 heads, window of 2000).  A block has its SM to itself,
 //    so nothing hides its start, its items' outputs and the joins.
 #include <cuda.h>
@@ -73,13 +75,15 @@ constexpr int kWalk = 16;              // items of a request that are counted on
 // for one tile of rows (memory), for two (products), an item besides its tiles
 // (kLead before them, the rest after: a border that falls there does not cut the
 // item).  Without these weights a mixed step of 16 sequences that decode or take
-// 100-700 tokens took 131 us instead of 117.  Over 18 cases of all kinds the
-// geometric mean is 31.1 us so, 31.7 with 6 units all before the tiles, 31.3
-// with 3 + 3 or 5 + 5, 30.9 with 6 + 6 (one sequence with 1001 keys the same,
-// 32 decoding ones 83 instead of 80.5); pair costs of 3.5 and 4 add 1 or 2 %.
+// 100-700 tokens took 131 us instead of 119.  Over 18 cases of all kinds the
+// geometric mean is 2 % below that of 6 units all before the tiles, 0.6 % below
+// 3 + 3 and 5 + 5, 0.7 % above 6 + 6 (32 decoding sequences 83 us instead of
+// 80); pair costs of 3.5 and 4 add 1 or 2 %.
 constexpr int kTileCost = 2, kPairCost = 3, kItemCost = 8, kLead = 4;
-constexpr int kMinUnits = 5;           // of a block: two key tiles (one sequence with 1001 keys 13.8 us; 8 units 14.3, 12
-                                       // units 16.9)
+// Units of a block at least (a tile's cost or more): 18 cases' mean 30.5 us, one
+// sequence with 1001 keys 13.4 us; with 3 units 31.1 and 13.8, 4 30.8 and 12.7,
+// 6 30.5 and 13.5, 9 30.7 and 14.5.
+constexpr int kMinUnits = 5;
 constexpr float kLift = 7.f;           // log2 of the factor that P, l and O share
 constexpr float kGrow = 8.f;           // fp16: growth (log2) of a maximum before m follows
 constexpr float kSum = 1073741824.f;   // bf16: sum of a tile's weights from which m follows
@@ -471,11 +475,12 @@ PI_DEV Piece next_piece(PagedShared<DH>& sh, int n, const Ctl& ctl) {
 
 // ------------------------------------------------------------ key tiles (warp 8), value tiles (warp 10)
 //
-// A lane per page of a tile, one copy each (70 cycles to issue, so a warp for
-// each ring: 8 pages of 16 positions and their table entries take most of the
-// time that a tile's products do).  Pages outside the keys the item sees are not
-// read (their rows of the slot are stale: scores there are masked, value rows
-// are cleared by the MMA warp).
+// A lane per page of a tile, one copy each.  A copy takes 70 cycles to issue:
+// keys and values from one warp, 16 pages of 16 positions and their table
+// entries, would take most of the 2048 cycles of a step's products, so a warp
+// for each ring.  Pages outside the keys the item sees are not read (their rows
+// of the slot are stale: scores there are masked, value rows are cleared by the
+// MMA warp).
 template <int DH, bool VALUES>
 PI_DEV void tile_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* ring, const Ctl& ctl) {
     using C = PagedCfg<DH>;
@@ -1181,7 +1186,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_paged_attn(const __grid_co
     pre += before - own;   // units before this thread's requests
     const unsigned tmem = sh.tmem;
     // blocks with work: about two tiles each at least, one for each softmax group
-    // (a part costs a join, the second tile runs beside the first)
+    // (a part costs a join, the second tile runs beside the first); U / G is
+    // kMinUnits or more, or all
     const int G = (int)min((long long)gridDim.x, max(U / kMinUnits, U > 0 ? 1ll : 0ll));
     const int blk = blockIdx.x;
     const long long u0 = G > 0 ? quotient(U * blk, G) : 0, u1 = G > 0 ? quotient(U * (blk + 1), G) : 0;
