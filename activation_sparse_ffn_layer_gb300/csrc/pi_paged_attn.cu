@@ -98,7 +98,7 @@ struct PagedCfg {
     static constexpr int SK = DH == 128 ? 3 : 6;         // ring slots for keys: one more than for values, since
     static constexpr int SV = DH == 128 ? 2 : 6;         // a key tile is used a step before its values
     static constexpr int GROUP = HALVES * 1024;          // bytes of 8 keys or values: a 64-element block after the other
-    static constexpr int MISC = 3072;
+    static constexpr int MISC = 3 * 1024;
     static constexpr int SMEM = Q + (SK + SV) * TILE + MISC;
     static constexpr unsigned O_COL = 2 * kKeys;         // tensor memory: S0 S1 | O0 O1
     static_assert(SMEM <= 232448, "shared memory of a block");
