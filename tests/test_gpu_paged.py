@@ -625,3 +625,21 @@ def test_waits_that_run_out(P, lens, H, G):
             got = run_attn(P, *case, ws=ws)
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
         assert P.pi_last_device_status() == 0
+
+
+@pytest.mark.parametrize("seed", range(8))
+def test_steps_of_many_sizes_on_one_workspace(P, seed):
+    """Decodes, chunks and empty rows whose items the blocks' borders cut anywhere, one step after the other on one
+    workspace that is filled with zeros only once."""
+    r = random.Random(seed)
+    ws = torch.zeros(1 << 27, dtype=torch.uint8, device="cuda")
+    for _ in range(4):
+        H, G = r.choice([(4, 4), (8, 2), (16, 1), (64, 8)])
+        dh, dt, page, window = r.choice([64, 128]), r.choice([F16, BF16]), r.choice([16, 32, 128]), r.choice([0, 0, 1, 300])
+        lens = []
+        for _ in range(r.choice([1, 2, 5, 40])):
+            n = r.choice([0, 1, 1, 1, r.randint(2, 30), r.randint(30, 400)])
+            lens.append((n, n + r.choice([0, r.randint(0, 100), r.randint(100, 1500)])))
+        if not any(n for n, _ in lens):
+            lens.append((1, 700))
+        compare(P, paged_case(lens, H, G, dh, dt, page, seed=r.randrange(1000), junk=math.nan, window=window), window=window, ws=ws)
