@@ -103,7 +103,10 @@ __global__ void __launch_bounds__(kTabThreads) k_block_tables(const TablesArgs a
     int* sneed = sheld + B;        // pages needed, -1: not served
     const int per = (B + kTabThreads - 1) / kTabThreads;
     int c[kTabPer], n[kTabPer], h[kTabPer];
-    bool bad[kTabPer];
+    bool bad[kTabPer], over[kTabPer];
+    // this thread's tokens (at most 2^42 over all rows), and from bit 44 on its
+    // rows that ask for more positions than their table row has
+    constexpr long long kOver = 1ll << 44;
     long long tok = 0;
     bool any_bad = false;
     const int page = 1 << a.page_shift;
@@ -112,20 +115,38 @@ __global__ void __launch_bounds__(kTabThreads) k_block_tables(const TablesArgs a
     for (int i = 0; i < kTabPer; ++i) {
         const int b = threadIdx.x * per + i;
         c[i] = n[i] = h[i] = 0;
-        bad[i] = false;
+        bad[i] = over[i] = false;
         if (i < per && b < B) {
             c[i] = a.cached[b];
             n[i] = a.fresh[b];
             h[i] = a.held[b];
-            bad[i] = c[i] < 0 || n[i] < 0 || h[i] < 0 || h[i] > a.max_pages || (long long)c[i] + n[i] > capacity;
+            bad[i] = c[i] < 0 || n[i] < 0 || h[i] < 0 || h[i] > a.max_pages || n[i] > capacity;
             if (bad[i]) n[i] = 0;
-            tok += n[i];
+            over[i] = !bad[i] && (long long)c[i] + n[i] > capacity;
+            bad[i] |= over[i];
+            tok += n[i] + (over[i] ? kOver : 0);
         }
         any_bad |= bad[i];
     }
     if (threadIdx.x == 0) free_in = *a.free_count;
     long long total_tok;
     long long tp = block_prefix(tok, warp_sums, &total_tok);
+    // the packed rows hold the tokens of rows that ask for too much as well, so
+    // those are counted (the rows after them would be moved); where the tokens
+    // do not all fit, the packed rows cannot hold them, and the others' are
+    if (total_tok >= kOver) {
+        if ((total_tok & (kOver - 1)) > a.max_tokens) {
+            tok = 0;
+#pragma unroll
+            for (int i = 0; i < kTabPer; ++i) {
+                if (over[i]) n[i] = 0;
+                tok += n[i];
+            }
+            tp = block_prefix(tok, warp_sums, &total_tok);
+        }
+        total_tok &= kOver - 1;
+        tp &= kOver - 1;
+    }
     const int f = min(max(free_in, 0), a.num_pages);
     any_bad |= f != free_in;
     long long give = 0, want = 0;
@@ -230,7 +251,7 @@ __global__ void __launch_bounds__(kTabThreads) k_block_tables(const TablesArgs a
         int pos = 0;
         if (i < T) {
             const int b = row_of(tfirst, B, (int)i);
-            pos = scached[b] + (int)(i - tfirst[b]);
+            pos = (int)((unsigned)scached[b] + (unsigned)(i - tfirst[b]));   // (a row that is not served may pass int)
             if (sneed[b] >= 0) {
                 const int pi = pos >> a.page_shift, held = sheld[b];
                 const int id = pi < held ? a.table[(size_t)b * a.max_pages + pi]

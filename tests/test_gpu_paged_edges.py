@@ -1,0 +1,111 @@
+"""Paged serving at its edges: rows that reach the end of their table row, requests with fewer positions than
+tokens, infinities and large values in long caches, sums near the end of fp32, many small requests."""
+import random
+
+import pytest
+import torch
+
+from tests import paged_ref as R
+from tests.test_gpu_paged import P, i32, run_tables  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ rows past the end of their table row
+
+def test_a_row_past_its_table_row_leaves_the_others_in_place(P):
+    """Row 0 holds all its 4 pages of 16 and asks for one more token: it is not served and reported, and the
+    tokens of the rows after it are still those at rows 1 and 2 of the packed projections."""
+    table, stack = [[0, 1, 2, 3], [5, -1, -1, -1], [4, -1, -1, -1]], [6, -1, -1, -1, -1, -1, -1]
+    got = run_tables(P, 16, 3, [64, 3, 3], [1, 1, 1], [4, 1, 1], table, stack, 1)
+    assert got == dict(held=[4, 1, 1], table=table, stack=stack, count=1, cu=[0, 1, 2, 3], kv=[0, 4, 4],
+                       slots=[-1, 5 * 16 + 3, 4 * 16 + 3], pos=[64, 3, 3], status=True)
+
+
+@pytest.mark.parametrize("B", [3, 300, 2100, 4096])
+@pytest.mark.parametrize("fits", [True, False])
+def test_rows_past_their_table_rows_at_random(P, B, fits):
+    """Rows that ask for more than their table row holds among others, in one block and in two grids.  Where all
+    tokens fit the packed rows theirs are counted; where they do not, the others' alone are (as paged_ref has it)."""
+    r, page, M = random.Random(B), 16, 6
+    cached, new, held, long = [], [], [], []
+    for b in range(B):
+        c = r.randint(0, M * page)
+        over = b % 3 == 1
+        n = r.randint(M * page - c + 1, M * page) if over and c > 0 else min(r.choice((0, 1, 5)), M * page - c)
+        cached.append(c)
+        new.append(n)
+        held.append(-(-c // page))
+        long.append(c + n > M * page)
+    total = sum(held)
+    ids = list(range(total + 40))
+    r.shuffle(ids)
+    at, table = 0, []
+    for h in held:
+        table.append([ids[at + j] if j < h else -5 for j in range(M)])
+        at += h
+    stack = ids[total:] + [-3] * total
+    args = (cached, new, held, table, stack, 40)
+    T = sum(new) if fits else sum(n for n, x in zip(new, long) if not x)
+    got, want = run_tables(P, page, T, *args), R.tables(page, T, *args)
+    assert any(long) and want["status"] and sum(new) > sum(n for n, x in zip(new, long) if not x)
+    if fits:
+        cu = [0]
+        for n in new:
+            cu.append(cu[-1] + n)
+        slots, pos = [], []
+        for b in range(B):
+            for i in range(new[b]):
+                p = cached[b] + i
+                pos.append(p)
+                slots.append(want["table"][b][p // page] * page + p % page if want["kv"][b] > 0 else -1)
+        want.update(cu=cu, slots=slots, pos=pos)
+    assert not [x for x in want if got[x] != want[x]]
+
+
+def test_a_full_row_does_not_move_the_others(P):
+    """A captured decode loop in which row 0 reaches its last position: the other rows' keys, values and outputs
+    stay those of their own projections, replay after replay."""
+    from activation_sparse_ffn_layer_gb300.paged import PagedCache
+    n, H, G, dh, page = 3, 4, 2, 64, 16
+    cache = PagedCache(H, G, dh, n, 64, 60, 80, page_size=page, rope=P.rope_plan(dh, 0))
+    torch.manual_seed(7)
+    first = torch.randn(73, H + 2 * G, dh, device="cuda").half()
+    cache.begin(i32([60, 10, 3]), 73, 60)
+    cache.attend(0, *first.split([H, G, G], 1), torch.empty(73, H, dh, device="cuda").half())
+    hist = [[first[a:b, H:]] for a, b in ((0, 60), (60, 70), (70, 73))]
+    x = torch.randn(n, H + 2 * G, dh, device="cuda").half()
+    out, ones = torch.empty(n, H, dh, device="cuda").half(), i32([1] * n)
+    one = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+
+    def step():
+        cache.begin(ones, n, 1)
+        cache.attend(0, *x.split([H, G, G], 1), out)
+
+    step()
+    for b in range(n):
+        hist[b].append(x[b:b + 1, H:].clone())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    assert P.pi_last_device_status() == 0
+    for i in range(20):
+        x.copy_(torch.randn(x.shape, generator=torch.Generator().manual_seed(i)))
+        graph.replay()
+        assert cache.cu.tolist() == [0, 1, 2, 3]
+        full = i >= 3                              # 61 + 3 positions are 64
+        assert cache.cached.tolist() == [64 if full else 62 + i, 12 + i, 5 + i]
+        assert P.pi_last_device_status() == (1 if full else 0)
+        for b in range(n):
+            if b == 0 and full:
+                assert int(cache.slots[0]) == -1 and bool((out[0] == 0).all())
+                continue
+            hist[b].append(x[b:b + 1, H:].clone())
+            kv = torch.cat(hist[b])
+            t = torch.arange(kv.shape[0], device="cuda")
+            ids = cache.table[b][t // page].long()
+            assert torch.equal(cache.kcache[0][ids, :, t % page], kv[:, :G])
+            assert torch.equal(cache.vcache[0][ids, :, t % page], kv[:, G:])
+            want, _, tol, _ = R.attention(x[b:b + 1, :H], kv[:, :G].transpose(0, 1)[None], kv[:, G:].transpose(0, 1)[None],
+                                          one, [0, 1], [kv.shape[0]])
+            R.check(out[b:b + 1], want, tol, f"step {i} row {b}")
