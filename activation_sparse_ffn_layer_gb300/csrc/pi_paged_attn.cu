@@ -1387,7 +1387,9 @@ pi_status pi_paged_attn(const pi_paged_desc* desc, const pi_page_desc* cache, co
     a.max_tokens = desc->max_tokens;
     a.max_new = desc->max_new;
     a.max_pages = desc->max_pages;
-    a.window = desc->window;
+    // a window of all positions a row can hold, or more, is none; below that,
+    // sums with first positions (down to -2^24) stay far from the ends of int
+    a.window = (long long)desc->window >= (long long)desc->max_pages * cache->page_size ? 0 : desc->window;
     a.page_size = cache->page_size;
     a.num_pages = cache->num_pages;
     a.group = desc->heads / cache->kv_heads;

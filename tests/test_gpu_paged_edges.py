@@ -1,12 +1,13 @@
 """Paged serving at its edges: rows that reach the end of their table row, requests with fewer positions than
 tokens, infinities and large values in long caches, sums near the end of fp32, many small requests."""
+import math
 import random
 
 import pytest
 import torch
 
 from tests import paged_ref as R
-from tests.test_gpu_paged import P, i32, run_tables  # noqa: F401
+from tests.test_gpu_paged import F16, P, compare, i32, paged_case, run_tables  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -109,3 +110,20 @@ def test_a_full_row_does_not_move_the_others(P):
             want, _, tol, _ = R.attention(x[b:b + 1, :H], kv[:, :G].transpose(0, 1)[None], kv[:, G:].transpose(0, 1)[None],
                                           one, [0, 1], [kv.shape[0]])
             R.check(out[b:b + 1], want, tol, f"step {i} row {b}")
+
+
+# ------------------------------------------------------------------ windows and requests that see nothing
+
+@pytest.mark.parametrize("n,kv", [(200, 100), (700, 500), (900, 2)])
+@pytest.mark.parametrize("window", [0, 1, 90, 2 ** 30, 2 ** 31 - 1])
+def test_more_tokens_than_positions_under_any_window(P, n, kv, window):
+    """A window of the largest int is no window; up to 29 items of a request whose first ones see nothing."""
+    q, kc, vc, table, cu, _ = paged_case([(n, n), (1, 40)], 8, 1, 64, F16, 16, seed=21)
+    compare(P, (q, kc, vc, table, cu, [kv, 40]), window=window)
+
+
+@pytest.mark.parametrize("B", [385, 1500, 4096])
+def test_thousands_of_small_requests(P, B):
+    r = random.Random(B)
+    lens = [(n, n + r.randint(0, 30)) for n in (r.choice((0, 1, 1, 1, 2)) for _ in range(B))]
+    compare(P, paged_case(lens, 4, 2, 64, F16, 16, seed=B, junk=math.nan))
