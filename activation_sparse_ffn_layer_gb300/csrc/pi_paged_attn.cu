@@ -961,6 +961,7 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
                 int seen = 0;
                 if (lane == 0) seen = peek_gpu(arrivals);
                 last = __shfl_sync(FULL, seen, 0) == 1;
+                __syncwarp();   // the other part, which lane 0 has acquired, is there for every lane (a shuffle orders no memory)
             }
             const int mine_k = (int)blockIdx.x - p.block0;
             const int there = (p.block0 + 1 - mine_k) * 2 + mine_k;   // the other's partial: its second slot is of part 0
@@ -1080,11 +1081,14 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
                 float* ml = a.part_ml + ((size_t)(blk * 2 + (pair ? 0 : w)) * a.part_rows + r) * 2;
                 if (live) *reinterpret_cast<float2*>(ml) = make_float2(m, l);
                 // the lanes' stores happen before lane 0's arrival (__syncwarp, then
-                // release), the other blocks' before what follows it (acquire)
+                // release), the other blocks' before what any lane reads after it
+                // (acquire, then __syncwarp)
                 __syncwarp();
                 int seen = 0;
                 if (lane == 0) seen = arrive_gpu(arrivals);
-                if (__shfl_sync(FULL, seen, 0) != p.parts - 1) break;
+                seen = __shfl_sync(FULL, seen, 0);
+                __syncwarp();
+                if (seen != p.parts - 1) break;
                 if (spot && redo == 0) {
                     last = true;
                     continue;

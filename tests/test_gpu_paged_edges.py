@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from tests import paged_ref as R
-from tests.test_gpu_paged import F16, P, compare, i32, paged_case, run_tables  # noqa: F401
+from tests.test_gpu_paged import BF16, F16, P, compare, i32, paged_case, run_attn, run_tables  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -127,3 +127,20 @@ def test_thousands_of_small_requests(P, B):
     r = random.Random(B)
     lens = [(n, n + r.randint(0, 30)) for n in (r.choice((0, 1, 1, 1, 2)) for _ in range(B))]
     compare(P, paged_case(lens, 4, 2, 64, F16, 16, seed=B, junk=math.nan))
+
+
+# ------------------------------------------------------------------ parts of an item that meet
+
+@pytest.mark.parametrize("lens,H,G", [([(1, 3800)] * 12, 16, 16), ([(1, 2600 + 100 * i) for i in range(9)], 64, 8),
+                                      ([(150, 1900), (70, 600), (1, 4000)], 16, 4)])
+def test_parts_that_meet_give_the_same_bits(P, lens, H, G):
+    """Items that one border cuts, both parts done at nearly the same time: whichever block adds them, and whether it
+    finds the other part there or waits for it, every call gives one result, which is right."""
+    case = paged_case(lens, H, G, 64, BF16, 16, seed=31)
+    q, kc, vc, table, cu, kv = case
+    d, pg = P.paged_desc(H, len(kv), q.shape[0], max(n for n, _ in lens), table.shape[1]), P.page_desc(kc, vc)
+    ws = torch.zeros(P.pi_paged_workspace_bytes(d, pg), dtype=torch.uint8, device="cuda")
+    first = compare(P, case, ws=ws)
+    for _ in range(60):
+        again = run_attn(P, *case, ws=ws)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
