@@ -27,6 +27,9 @@
 // partials (m, l, O) in the workspace, and the block that arrives last adds
 // them in block order (the order is fixed, who does it is not: same bits).
 //
+// Rows whose outputs are not finite are taken again in fp32 over the keys they
+// see, by the block that wrote them, once it is done with everything else.
+//
 // Bounds and figures (GB300, 64 query and 8 KV heads of 128 unless said):
 //  - few rows per key (decoding): HBM.  Four sequences with 120-131 thousand
 //    keys, bf16: 300 us, 6.9 TB/s.  32 sequences with 500-8000 keys, fp16: 80
@@ -146,17 +149,27 @@ struct Request {
     int cu, n, first;   // first row of q, tokens, position of the first token
 };
 
+// Where a block's range of units starts, and how far its pieces have been walked.
+struct Walk {
+    Request r;
+    long long u, u1, U;   // unit reached, the range's end, units in all
+    int G, b, g, tok0, off;   // blocks with work; request, KV head, first token and unit within the item at u
+
+    PI_DEV Piece next(const PagedArgs& a);   // nt = 0: none is left
+};
+
 template <int DH>
 struct PagedShared {
     unsigned long long kfull[6], kempty[6], vfull[6], vempty[6], qfull, qempty, sfull[2], pready[2][2], odone[2], lfull[kListDepth],
         lempty[kListDepth], merge[2], merged, drain;
     Piece list[kListDepth];
     float ml[2][kKeys][2];
-    Request start_r;
-    long long start_u;   // this block's first unit, and where it is
-    int start_b, start_g, start_tok0, start_off;
+    Walk walk;   // from this block's first unit
     unsigned tmem;
     int abort_flag;
+    int redo;            // some row that this block has written is not finite
+    int joined[2];       // warps that have written the outputs of a cut item (by Piece::own), a bit each
+    int odd_rows;        // rows of a piece to be taken again
 };
 
 PI_DEV Request request(const PagedArgs& a, int b, bool* bad) {
@@ -310,69 +323,6 @@ PI_DEV uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// One row over keys lo .. hi - 1 by the whole warp, key by key, keeping only
-// what the row sees.  For rows whose tensor-core result is not finite: there
-// 0 x value has let a non-finite value of a key that this row does not see
-// into the sum (P is 0 there, but 0 x inf is NaN), or the row sees such a
-// value itself.  Same convention as the tiles: m in log2 units, l and o with
-// the factor 2^kLift.
-template <typename T, int DH>
-__device__ __noinline__ void careful_row(const PagedArgs& a, int b, int g, long long q_at, int lo, int hi, float& m_out,
-                                         float& l_out, float (&o)[DH / 32]) {
-    constexpr int E = DH / 32;
-    const int lane = threadIdx.x & 31;
-    const T* qp = static_cast<const T*>(a.q) + q_at + lane * E;
-    const float c = a.scale / kLn2;
-    float q[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        q[e] = to_f(qp[e]);
-        o[e] = 0.f;
-    }
-    constexpr int N = 4;   // keys at a time, their loads in flight together
-    for (int x0 = lo; x0 < hi; x0 += N) {
-        float k[N][E], v[N][E], s[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int x = min(x0 + i, hi - 1);
-            const int page = a.table[(size_t)b * a.max_pages + x / a.page_size];
-            const bool ok = page >= 0 && page < a.num_pages;   // else the copies read zeros
-            const long long at = (ok ? page : 0) * a.page_stride + g * a.head_stride +
-                                 (x % a.page_size) * a.token_stride + lane * E;
-            const T *kp = static_cast<const T*>(a.k) + at, *vp = static_cast<const T*>(a.v) + at;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                k[i][e] = ok ? to_f(kp[e]) : 0.f;
-                v[i][e] = ok ? to_f(vp[e]) : 0.f;
-            }
-        }
-        float top = m;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            s[i] = 0.f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) s[i] = fmaf(q[e], k[i][e], s[i]);
-            s[i] = warp_sum(s[i]) * c;
-            top = fmaxf(top, s[i]);
-        }
-        const float use = top == -INFINITY ? 0.f : top, f = exp2f(m - use);
-        l *= f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] *= f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if (x0 + i >= hi) break;
-            const float w = exp2f(s[i] - use + kLift);
-            l += w;
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = fmaf(w, v[i][e], o[e]);
-        }
-        m = top;
-    }
-    m_out = m;
-    l_out = l;
-}
-
 // a / b for positive numbers, in 32 bits where they fit (a 64-bit division is a call)
 PI_DEV long long quotient(long long a, long long b) {
     if (((a | b) >> 32) == 0) return (unsigned)a / (unsigned)b;
@@ -384,68 +334,70 @@ PI_DEV long long quotient(long long a, long long b) {
 // Units u of the block's range run through the items: kLead, the tiles' costs,
 // the rest of kItemCost.  A block does the tiles that begin in its range (a range is
 // longer than a tile's cost, so every block between an item's first and last
-// has one).  With a piece go its
-// query tiles, once the scores of the piece before are done; tokens past the
-// request's end or the last row come along or read as zeros: a row of S depends
-// on its own query alone.
+// has one).
+PI_DEV Piece Walk::next(const PagedArgs& a) {
+    Piece p{};
+    while (u < u1 && p.nt == 0) {   // again where only an item's cost falls into this block
+        int toks, lo, hi;
+        const int nt = item_tiles(a, r, tok0, &toks, &lo, &hi);
+        const int c = tile_cost(a, toks);
+        const long long i0 = u - off;   // the item's first unit
+        const int stop = (int)min((long long)(kItemCost + nt * c), u1 - i0);
+        const int from = min((max(off - kLead, 0) + c - 1) / c, nt), to = min((max(stop - kLead, 0) + c - 1) / c, nt);
+        p.nt = to - from;
+        p.j0 = lo / kKeys + from;
+        p.lo = lo;
+        p.hi = hi;
+        p.b = b;
+        p.g = g;
+        p.tok0 = tok0;
+        p.toks = toks;
+        p.first = r.first;
+        p.cu = r.cu;
+        p.parts = 1;
+        p.own = from == 0;
+        if (p.nt != nt) {   // blocks that own its first and its last tile
+            p.block0 = (int)quotient((i0 + kLead + 1) * G - 1, U);
+            p.parts = (int)quotient((i0 + kLead + (nt - 1) * c + 1) * G - 1, U) - p.block0 + 1;
+        }
+        u = i0 + stop;
+        off = 0;
+        tok0 += 2 * a.tile_tokens;
+        if (u < u1 && tok0 >= r.n) {
+            tok0 = 0;
+            if (++g == a.kv_heads) {
+                g = 0;
+                // u < u1 <= U: a later request has tokens
+                do {
+                    if (++b >= a.batch) {   // the lengths changed under the kernel: stop
+                        u = u1;
+                        break;
+                    }
+                    bool bad = false;
+                    r = request(a, b, &bad);
+                } while (r.n == 0);
+            }
+        }
+    }
+    return p;
+}
+
+// With a piece go its query tiles, once the scores of the piece before are
+// done; tokens past the request's end or the last row come along or read as
+// zeros: a row of S depends on its own query alone.  A function of its own: in
+// line, its registers cost the other roles theirs (4096-token chunk 1.15 ms so,
+// 1.25 in line).
 template <int DH>
-PI_DEV void list_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* qs, Request r, long long u1, long long U,
-                      int G, const Ctl& ctl) {
+__device__ __noinline__ void list_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* qs, Walk walk, const Ctl& ctl) {
     using C = PagedCfg<DH>;
-    int b = sh.start_b, g = sh.start_g, tok0 = sh.start_tok0, off = sh.start_off;
-    long long u = sh.start_u;
-    bool bad = false;
     int n = 0;
     for (;;) {
-        Piece p{};
-        bool end = u >= u1;
-        if (!end) {
-            int toks, lo, hi;
-            const int nt = item_tiles(a, r, tok0, &toks, &lo, &hi);
-            const int c = tile_cost(a, toks);
-            const long long i0 = u - off;   // the item's first unit
-            const int stop = (int)min((long long)(kItemCost + nt * c), u1 - i0);
-            const int from = min((max(off - kLead, 0) + c - 1) / c, nt), to = min((max(stop - kLead, 0) + c - 1) / c, nt);
-            p.nt = to - from;
-            p.j0 = lo / kKeys + from;
-            p.lo = lo;
-            p.hi = hi;
-            p.b = b;
-            p.g = g;
-            p.tok0 = tok0;
-            p.toks = toks;
-            p.first = r.first;
-            p.cu = r.cu;
-            p.parts = 1;
-            p.own = from == 0;
-            if (p.nt != nt) {   // blocks that own its first and its last tile
-                p.block0 = (int)quotient((i0 + kLead + 1) * G - 1, U);
-                p.parts = (int)quotient((i0 + kLead + (nt - 1) * c + 1) * G - 1, U) - p.block0 + 1;
-            }
-            u = i0 + stop;
-            off = 0;
-            tok0 += 2 * a.tile_tokens;
-            if (u < u1 && tok0 >= r.n) {
-                tok0 = 0;
-                if (++g == a.kv_heads) {
-                    g = 0;
-                    // u < u1 <= U: a later request has tokens
-                    do {
-                        if (++b >= a.batch) {   // the lengths changed under the kernel: stop
-                            u = u1;
-                            break;
-                        }
-                        r = request(a, b, &bad);
-                    } while (r.n == 0);
-                }
-            }
-            if (p.nt == 0) continue;   // only the item's cost falls into this block
-        }
+        const Piece p = walk.next(a);
         const int s = n % kListDepth;
         if (n >= kListDepth && !bar_wait(&sh.lempty[s], (n / kListDepth - 1) & 1, ctl)) break;
         sh.list[s] = p;
         bar_arrive(&sh.lfull[s]);
-        if (end) break;
+        if (p.nt == 0) break;
         if (n >= 1 && !bar_wait(&sh.qempty, (n - 1) & 1, ctl)) break;
         const int tiles = p.toks > a.tile_tokens ? 2 : 1;
         bar_arrive_expect_tx(&sh.qfull, (unsigned)(tiles * C::HALVES * a.tile_tokens * a.group) * 128u);
@@ -702,6 +654,9 @@ PI_DEV float take_weights(const uint32_t* s, unsigned at, uint64_t c2, uint64_t 
     return u + v;
 }
 
+// 1 / l, 0 for a row that sees nothing, NaN for a sum that is not finite (the row is taken again)
+PI_DEV float inverse(float l) { return l < INFINITY ? (l > 0.f ? 1.f / l : 0.f) : NAN; }
+
 PI_DEV int arrive_gpu(int* p) {
     int old;
     asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(old) : "l"(p) : "memory");
@@ -721,16 +676,16 @@ PI_DEV int peek_gpu(const int* p) {
 // the whole warp, and asks for CS column groups of KS parts and for their m and
 // l at a time (what other blocks have just written takes 1500 cycles to come;
 // one sequence with 1001 keys: 13.3 us so, 14.0 with m and l fetched first; 24
-// loads at a time spill, here or in the caller).
+// loads at a time spill, here or in the caller).  True: some output is not finite.
 template <typename T, int DH>
-__device__ __noinline__ void join_parts(const PagedArgs& a, const Piece& p, bool pair, int w, int r0, int rows, int tok0,
+__device__ __noinline__ bool join_parts(const PagedArgs& a, const Piece& p, bool pair, int w, int r0, int rows, int tok0,
                                         int c0, int cols) {
     constexpr int CS = 4, KS = 4;
     const int lane = threadIdx.x & 31;
     const int span = rows > 16 ? 32 : rows > 8 ? 16 : rows > 4 ? 8 : rows > 2 ? 4 : rows;   // power of two
     const int tr = r0 + (lane & (span - 1));   // row of the tile
     const int cg = lane / span, step = 32 / span;
-    if ((lane & (span - 1)) >= rows) return;
+    if ((lane & (span - 1)) >= rows) return false;
     const int r = (pair ? w * kTileRows : 0) + tr;
     const size_t ml_step = (size_t)2 * 2 * a.part_rows, o_step = (size_t)2 * DH / 4 * a.part_rows;
     // partial of block block0 + k: its second slot (k = 0, where the item starts) or its first
@@ -743,7 +698,7 @@ __device__ __noinline__ void join_parts(const PagedArgs& a, const Piece& p, bool
     T* dst = static_cast<T*>(a.out) + orow * a.o_stride + (long long)head * DH;
     const int end = (c0 + cols) / 4;
     float M = -INFINITY, L = 0.f, use = 0.f, inv = 0.f;
-    bool first = true;
+    bool first = true, odd = false;
     for (int c = c0 / 4 + cg; c < end; c += CS * step) {
         float4 v[CS];
 #pragma unroll
@@ -774,7 +729,7 @@ __device__ __noinline__ void join_parts(const PagedArgs& a, const Piece& p, bool
                     if (i < p.parts) add(s[i]);
 #pragma unroll 1
                 for (int k = KS; k < p.parts; ++k) add(__ldcg(ml + k * ml_step));
-                inv = L > 0.f || L != L ? 1.f / L : 0.f;
+                inv = inverse(L);
             }
 #pragma unroll
             for (int i = 0; i < KS; ++i) {
@@ -791,12 +746,15 @@ __device__ __noinline__ void join_parts(const PagedArgs& a, const Piece& p, bool
         }
 #pragma unroll
         for (int j = 0; j < CS; ++j)
-            if (c + j * step < end)
-                *reinterpret_cast<uint2*>(dst + 4 * (c + j * step)) =
-                    make_uint2(pack2(v[j].x * inv, v[j].y * inv, T()), pack2(v[j].z * inv, v[j].w * inv, T()));
+            if (c + j * step < end) {
+                v[j] = make_float4(v[j].x * inv, v[j].y * inv, v[j].z * inv, v[j].w * inv);
+                odd |= !(fabsf(v[j].x) + fabsf(v[j].y) + fabsf(v[j].z) + fabsf(v[j].w) < INFINITY);
+                *reinterpret_cast<uint2*>(dst + 4 * (c + j * step)) = make_uint2(pack2(v[j].x, v[j].y, T()), pack2(v[j].z, v[j].w, T()));
+            }
     }
     if (a.lse != nullptr && c0 == 0 && cg == 0)
         a.lse[orow * a.heads + head] = L == 0.f ? -INFINITY : (M - kLift + log2f(L)) * kLn2;
+    return odd;
 }
 
 // ------------------------------------------------------------ softmax (warps 0-7)
@@ -979,10 +937,8 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
                     l = mine_k == 0 ? fmaf(x.y, f_there, l * f_here) : fmaf(l, f_here, x.y * f_there);
                     m = M;
                 }
-                // weights that outgrew fp32 before m could follow, or a NaN, in this part
-                // (the other has been looked at by its block)
-                bool odd = !(fabsf(l_own) < INFINITY);
-                const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+                bool odd = false;   // some output is not finite
+                const float inv = inverse(l);
                 const float4* pt = reinterpret_cast<const float4*>(a.part_o + (size_t)there * DH * a.part_rows) + (live ? r : 0);
                 // a whole item's 1 / l goes into what the groups' O count for
                 const bool both = own_any && other_any;
@@ -997,7 +953,6 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
                     if (both) tmem_ld32(o_other + (unsigned)i, q);
                     tmem_wait_ld();
                     tmem_loaded<32>(o);
-                    uint64_t check[2] = {0, 0};
                     if (both) {
                         tmem_loaded<32>(q);
 #pragma unroll
@@ -1009,11 +964,6 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
                         for (int e = 0; e < 32; e += 2)
                             split2(mul2(pair2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), gg1), v[e], v[e + 1]);
                     }
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) check[(e >> 1) & 1] = fma2(pair2(v[e], v[e + 1]), 0, check[(e >> 1) & 1]);
-                    float z0, z1;
-                    split2(add2(check[0], check[1]), z0, z1);
-                    odd |= z0 + z1 != 0.f;   // NaN: some value is not finite
                     if (last) {
                         float4 y[8];
 #pragma unroll
@@ -1024,6 +974,14 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
                             v[e] = (mine_k == 0 ? fmaf(z, f_there, fmaf(v[e], f_here, 0.f))
                                                 : fmaf(v[e], f_here, fmaf(z, f_there, 0.f))) * inv;
                         }
+                    }
+                    if (whole || last) {
+                        uint64_t check[2] = {0, 0};
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) check[(e >> 1) & 1] = fma2(pair2(v[e], v[e + 1]), 0, check[(e >> 1) & 1]);
+                        float z0, z1;
+                        split2(add2(check[0], check[1]), z0, z1);
+                        odd |= z0 + z1 != 0.f;   // NaN: some value is not finite
                     }
                     if (live && (whole || last)) {
                         T* dst = static_cast<T*>(a.out) + orow * a.o_stride + (long long)head * DH + i;
@@ -1039,43 +997,15 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
                                 make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
                     }
                 }
-                // rows whose sums are not finite, once more without the keys they do not
-                // see (and by way of the workspace, where there is another part)
-                const unsigned redo = __ballot_sync(FULL, live && odd);
-                if (last && redo != 0) {
-                    spot = last = false;
-                    continue;
-                }
-                __syncwarp();
-                for (unsigned left = redo; left; left &= left - 1) {
-                    const int src = __ffs(left) - 1;
-                    const int rlo = max(__shfl_sync(FULL, lo, src), p.j0 * kKeys);
-                    const int rhi = min(__shfl_sync(FULL, hi, src), (p.j0 + p.nt) * kKeys);
-                    const int rt = __shfl_sync(FULL, tok, src), rh = __shfl_sync(FULL, h, src), rr = __shfl_sync(FULL, r, src);
-                    float rm, rl, ro[DH / 32];
-                    careful_row<T, DH>(a, p.b, p.g,
-                                       (long long)(p.cu + rt) * a.q_stride + (long long)(p.g * a.group + rh) * DH, rlo, rhi, rm,
-                                       rl, ro);
-                    if (lane == src) {
-                        m = rm;
-                        l = rl;
-                    }
-#pragma unroll
-                    for (int e = 0; e < DH / 32; ++e) {
-                        const int col = lane * (DH / 32) + e;
-                        if (col < c0 || col >= c0 + cols) continue;
-                        if (whole)
-                            static_cast<T*>(a.out)[(long long)(p.cu + rt) * a.o_stride +
-                                                   (long long)(p.g * a.group + rh) * DH + col] =
-                                T(rl > 0.f || rl != rl ? ro[e] / rl : 0.f);
-                        else
-                            po[((size_t)(col / 4) * a.part_rows + rr) * 4 + col % 4] = ro[e];
-                    }
-                }
                 if (whole || last) {
                     if (live && a.lse != nullptr && c0 == 0)
                         a.lse[orow * a.heads + head] = l == 0.f ? -INFINITY : (m - kLift + log2f(l)) * kLn2;
-                    if (last && lane == 0) *arrivals = 0;
+                    odd = __any_sync(FULL, live && odd);
+                    if (lane == 0 && odd) sh.redo = 1;
+                    if (lane == 0 && last) {
+                        *arrivals = 0;
+                        atomicOr(&sh.joined[p.own], 1 << warp);
+                    }
                     break;
                 }
                 float* ml = a.part_ml + ((size_t)(blk * 2 + (pair ? 0 : w)) * a.part_rows + r) * 2;
@@ -1089,13 +1019,18 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
                 seen = __shfl_sync(FULL, seen, 0);
                 __syncwarp();
                 if (seen != p.parts - 1) break;
-                if (spot && redo == 0) {
+                if (spot) {
                     last = true;
                     continue;
                 }
-                if (lane == 0) *arrivals = 0;
                 const int rows = min(32, tile_rows - 32 * quad);
-                join_parts<T, DH>(a, p, pair, w, 32 * quad, rows, tok0, c0, cols);
+                odd = join_parts<T, DH>(a, p, pair, w, 32 * quad, rows, tok0, c0, cols);
+                odd = __any_sync(FULL, odd);
+                if (lane == 0) {
+                    *arrivals = 0;
+                    atomicOr(&sh.joined[p.own], 1 << warp);
+                    if (odd) sh.redo = 1;
+                }
                 break;
             }
         }
@@ -1107,6 +1042,194 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
             tc_after();
         }
         warp_arrive(&sh.lempty[n % kListDepth]);
+    }
+}
+
+// ------------------------------------------------------------ rows taken again (warps 0-7, after the block's pieces)
+//
+// Rows whose outputs are not finite, once more over all keys they see and only
+// those, in fp32.  On the tensor cores 0 x value lets a non-finite value of a
+// key that a row does not see into its sum (P is 0 there, but 0 x inf is NaN);
+// weights, or the parts' sums together, may have outgrown fp32 before m
+// followed; or the row sees such a value and stays as it is.  A block looks
+// through what it has written itself: the halves of a cut item's rows may have
+// been joined by different blocks, and each takes its half again.  No role waits
+// on this, so a long cache cannot make a wait run out.
+//
+// A warp per row, eight rows at a time over tiles of 64 keys in shared memory, a
+// lane per key for the scores and per column for the sums.  A tile starts at a
+// multiple of 64 whatever rows share it: same bits every time.
+PI_DEV void sync_softmax() { asm volatile("bar.sync 1, 256;" ::: "memory"); }   // warps 0-7
+PI_DEV void widen2(uint32_t w, float& x, float& y, __half) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    x = f.x;
+    y = f.y;
+}
+PI_DEV void widen2(uint32_t w, float& x, float& y, __nv_bfloat16) {
+    x = __uint_as_float(w << 16);
+    y = __uint_as_float(w & 0xffff0000u);
+}
+// keys that the row of the t-th token of a piece sees (none: hi <= lo)
+PI_DEV void row_sees(const PagedArgs& a, const Piece& p, int t, int* lo, int* hi) {
+    const int pos = p.first + p.tok0 + t;
+    *hi = pos + 1;
+    *lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+}
+
+template <typename T, int DH>
+__device__ __noinline__ void redo_rows(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* smem, Walk walk) {
+    constexpr int KT = 64, CHUNKS = DH / 8, ROW = DH * 2 + 16, E = DH / 32, EACH = KT * CHUNKS / 256;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    float* const q = reinterpret_cast<float*>(smem) + warp * DH;   // this warp's query
+    unsigned char* const kt = smem + 8 * DH * 4;                    // keys, rows 16 bytes apart in banks
+    unsigned char* const vt = kt + KT * ROW;
+    int* const list = reinterpret_cast<int*>(vt + KT * DH * 2);     // 4 x row + halves (bits)
+    const float c = a.scale / kLn2;
+    for (;;) {
+        sync_softmax();
+        if (tid == 0) {
+            sh.list[0] = walk.next(a);
+            sh.odd_rows = 0;
+        }
+        sync_softmax();
+        const Piece p = sh.list[0];
+        if (p.nt == 0) return;
+        const bool pair = p.toks > a.tile_tokens;
+        const int bits = p.parts == 1 ? 0xff : sh.joined[p.own];   // warps whose outputs this block wrote
+        for (int x = warp; x < p.toks * a.group; x += 8) {
+            const int t = x / a.group, w = t >= a.tile_tokens, quad = (x - w * a.tile_tokens * a.group) >> 5;
+            const int own = pair ? 3 * ((bits >> (4 * w + quad)) & 1) : ((bits >> quad) & 1) | 2 * ((bits >> (4 + quad)) & 1);
+            if (own == 0) continue;
+            const T* o = static_cast<const T*>(a.out) + (long long)(p.cu + p.tok0 + t) * a.o_stride +
+                         (long long)(p.g * a.group + x % a.group) * DH + lane * E;
+            bool odd = false;
+#pragma unroll
+            for (int e = 0; e < E; ++e) odd |= !(fabsf(to_f(o[e])) < INFINITY);
+            const unsigned who = __ballot_sync(FULL, odd);
+            const int halves = own & ((who & 0xffffu ? 1 : 0) | (who >> 16 ? 2 : 0));
+            if (halves != 0 && lane == 0) list[atomicAdd(&sh.odd_rows, 1)] = 4 * x + halves;
+        }
+        sync_softmax();
+        const int n = sh.odd_rows;
+        const int32_t* pages = a.table + (size_t)p.b * a.max_pages;
+        for (int i0 = 0; i0 < n; i0 += 8) {
+            // the rows' keys together, and this warp's
+            int from = 0x7fffffff, to = 0, lo = 0, hi = 0;
+            for (int i = i0; i < min(i0 + 8, n); ++i) {
+                int l, h;
+                row_sees(a, p, (list[i] >> 2) / a.group, &l, &h);
+                if (l < h) {
+                    from = min(from, l);
+                    to = max(to, h);
+                }
+                if (i == i0 + warp) {
+                    lo = l;
+                    hi = h;
+                }
+            }
+            const bool mine = i0 + warp < n;
+            const int entry = mine ? list[i0 + warp] : 0, x = entry >> 2;
+            const long long row = p.cu + p.tok0 + x / a.group;
+            const int head = p.g * a.group + x % a.group;
+            if (mine) {
+                const T* src = static_cast<const T*>(a.q) + row * a.q_stride + (long long)head * DH + lane * E;
+#pragma unroll
+                for (int e = 0; e < E; ++e) q[lane * E + e] = to_f(src[e]);
+            }
+            __syncwarp();
+            float m = -INFINITY, l = 0.f, o[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = 0.f;
+            uint4 k[EACH], v[EACH];   // this thread's part of the next tile
+            auto fetch = [&](int base) {
+#pragma unroll
+                for (int i = 0; i < EACH; ++i) {
+                    const int at = tid + 256 * i, key = base + at / CHUNKS;
+                    k[i] = v[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (key < from || key >= to) continue;
+                    const int page = pages[key / a.page_size];
+                    if (page < 0 || page >= a.num_pages) continue;   // reads as zeros
+                    const long long e = page * a.page_stride + p.g * a.head_stride + (key % a.page_size) * a.token_stride +
+                                        at % CHUNKS * 8;
+                    k[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.k) + e);
+                    v[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v) + e);
+                }
+            };
+            int base = from / KT * KT;
+            if (from < to) fetch(base);
+            for (; base < to; base += KT) {
+                sync_softmax();   // the last tile has been read
+#pragma unroll
+                for (int i = 0; i < EACH; ++i) {
+                    const int at = tid + 256 * i;
+                    *reinterpret_cast<uint4*>(kt + at / CHUNKS * ROW + at % CHUNKS * 16) = k[i];
+                    *reinterpret_cast<uint4*>(vt + at * 16) = v[i];
+                }
+                sync_softmax();
+                if (base + KT < to) fetch(base + KT);
+                if (!mine || hi <= base || lo >= base + KT) continue;
+                float s[2] = {0.f, 0.f};
+#pragma unroll
+                for (int d = 0; d < CHUNKS; ++d) {
+                    const float4 q0 = *reinterpret_cast<const float4*>(q + 8 * d), q1 = *reinterpret_cast<const float4*>(q + 8 * d + 4);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint4 y = *reinterpret_cast<const uint4*>(kt + (lane + 32 * j) * ROW + d * 16);
+                        float f[8];
+                        widen2(y.x, f[0], f[1], T());
+                        widen2(y.y, f[2], f[3], T());
+                        widen2(y.z, f[4], f[5], T());
+                        widen2(y.w, f[6], f[7], T());
+                        s[j] = fmaf(q0.x, f[0], fmaf(q0.y, f[1], fmaf(q0.z, f[2], fmaf(q0.w, f[3], s[j]))));
+                        s[j] = fmaf(q1.x, f[4], fmaf(q1.y, f[5], fmaf(q1.z, f[6], fmaf(q1.w, f[7], s[j]))));
+                    }
+                }
+                float top = m;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int key = base + lane + 32 * j;
+                    s[j] = key >= lo && key < hi ? s[j] * c : -INFINITY;
+                    top = fmaxf(top, s[j]);
+                }
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, d));
+                const float use = top == -INFINITY ? 0.f : top, f = exp2f(m - use);
+                const float w[2] = {exp2f(s[0] - use), exp2f(s[1] - use)};
+                m = top;
+                l = l * f + (w[0] + w[1]);
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] *= f;
+                for (int x = max(lo - base, 0); x < min(hi - base, KT); ++x) {
+                    const float wx = __shfl_sync(FULL, x < 32 ? w[0] : w[1], x & 31);
+                    const uint32_t* src = reinterpret_cast<const uint32_t*>(vt + (x * DH + lane * E) * 2);
+                    float y[E];
+#pragma unroll
+                    for (int e = 0; e < E; e += 2) widen2(src[e / 2], y[e], y[e + 1], T());
+                    if (wx == 0.f) {
+                        // e^a is not 0 but for a = -inf, so infinities count although the weight's fp32 is 0
+                        const float sx = __shfl_sync(FULL, x < 32 ? s[0] : s[1], x & 31);
+#pragma unroll
+                        for (int e = 0; e < E; ++e)
+                            if (sx > -INFINITY && !(fabsf(y[e]) < INFINITY)) o[e] += y[e];
+                            else o[e] = fmaf(0.f, y[e], o[e]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < E; ++e) o[e] = fmaf(wx, y[e], o[e]);
+                    }
+                }
+            }
+            l = warp_sum(l);
+            if (mine) {
+                if ((entry >> (lane >> 4)) & 1) {
+                    T* dst = static_cast<T*>(a.out) + row * a.o_stride + (long long)head * DH + lane * E;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) dst[e] = T(l == 0.f ? 0.f : o[e] / l);
+                }
+                if (a.lse != nullptr && (entry & 1) && lane == 0)
+                    a.lse[row * a.heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            }
+            __syncwarp();
+        }
     }
 }
 
@@ -1155,8 +1278,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_paged_attn(const __grid_co
         tmem_alloc(&sh.tmem, 512);
     }
     if (tid == 0) {   // no work, unless a thread finds this block's start below
-        sh.start_u = 0x7fffffffffffffffll;
-        sh.start_b = sh.start_g = sh.start_tok0 = sh.start_off = 0;
+        sh.walk = Walk{};
+        sh.walk.u = 0x7fffffffffffffffll;
+        sh.redo = sh.joined[0] = sh.joined[1] = 0;
     }
     if (warp == 8 && lane == 0) {
         tma_prefetch_map(&a.kmap);
@@ -1196,6 +1320,11 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_paged_attn(const __grid_co
     const int blk = blockIdx.x;
     const long long u0 = G > 0 ? quotient(U * blk, G) : 0, u1 = G > 0 ? quotient(U * (blk + 1), G) : 0;
     const bool work = blk < G;
+    if (tid == 0) {
+        sh.walk.u1 = u1;
+        sh.walk.U = U;
+        sh.walk.G = G;
+    }
     if (work && pre <= u0 && u0 < pre + own) {
         // this block's range starts in this thread's requests
         long long left = u0 - pre;
@@ -1229,12 +1358,12 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_paged_attn(const __grid_co
                 }
             }
             const int tok0 = i0 * d;
-            sh.start_u = u0;
-            sh.start_b = b;
-            sh.start_g = g;
-            sh.start_tok0 = tok0;
-            sh.start_off = (int)left;
-            sh.start_r = r;
+            sh.walk.u = u0;
+            sh.walk.b = b;
+            sh.walk.g = g;
+            sh.walk.tok0 = tok0;
+            sh.walk.off = (int)left;
+            sh.walk.r = r;
             break;
         }
     }
@@ -1255,7 +1384,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_paged_attn(const __grid_co
             else if (warp == 10)
                 tile_role<DH, true>(a, sh, vring, ctl);
             else if (lane == 0)
-                list_role<DH>(a, sh, qs, sh.start_r, u1, U, G, ctl);
+                list_role<DH>(a, sh, qs, sh.walk, ctl);
         }
     }
     tc_before();
@@ -1264,6 +1393,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_paged_attn(const __grid_co
         tc_after();
         tmem_free(tmem, 512);
     }
+    // all copies and products are in, the tiles' shared memory is free
+    if (warp < 8 && sh.redo != 0 && sh.abort_flag == 0) redo_rows<T, DH>(a, sh, qs, sh.walk);
 }
 
 bool paged_ok(const pi_paged_desc& d, const pi_page_desc& c) {

@@ -129,6 +129,104 @@ def test_thousands_of_small_requests(P, B):
     compare(P, paged_case(lens, 4, 2, 64, F16, 16, seed=B, junk=math.nan))
 
 
+# ------------------------------------------------------------------ infinities, large values, sums near the end of fp32
+
+def test_an_infinity_in_a_long_cache_costs_the_others_nothing(P):
+    """400 requests over the same pages but for one, whose own page holds an infinity: its rows are exact (32 of a
+    warp meet the infinity), the others keep their bits, and no wait runs out under a limit of 50 ms."""
+    B, H, dh, page, keys = 400, 32, 64, 128, 40000
+    g = torch.Generator(device="cuda").manual_seed(5)
+    used = -(-keys // page)
+    kc, vc = (torch.randn(used + 1, 1, page, dh, generator=g, device="cuda").half() for _ in range(2))
+    q = torch.randn(B, H, dh, generator=g, device="cuda").half()
+    table = torch.arange(used, device="cuda").int().repeat(B, 1)
+    own = 7
+    table[own, 2] = used
+    kv, cu = [keys] * B, list(range(B + 1))
+    want = run_attn(P, q, kc, vc, table, cu, kv)
+    assert P.pi_last_device_status() == 0
+    vc[used, 0, 3, 5] = math.inf
+    P.pi_debug_set_wait_timeout(50_000_000)
+    try:
+        got = run_attn(P, q, kc, vc, table, cu, kv)
+        torch.cuda.synchronize()
+    finally:
+        P.pi_debug_set_wait_timeout(0)
+    assert P.pi_last_device_status() == 0
+    rest = torch.arange(B, device="cuda") != own
+    assert torch.equal(got[0][rest], want[0][rest]) and torch.equal(got[1][rest], want[1][rest])
+    exact, el, tol, ltol = R.attention(q[own:own + 1], kc, vc, table[own:own + 1], [0, 1], [keys])
+    fine = torch.arange(dh, device="cuda") != 5
+    R.check(got[0][own:own + 1][..., fine], exact[..., fine], tol[..., fine], "other elements")
+    R.check(got[1][own:own + 1], el, ltol, "lse")
+    assert bool((got[0][own, :, 5] == math.inf).all())
+
+
+@pytest.mark.parametrize("which", [1, 2])
+@pytest.mark.parametrize("dt", [F16, BF16])
+@pytest.mark.parametrize("lens,H,G,window", [([(300, 700)], 4, 1, 0), ([(130, 400), (1, 900)], 8, 8, 150), ([(1, 3000)], 4, 2, 0)])
+def test_bad_values_among_masked_places(P, lens, H, G, window, dt, which):
+    """Every 37th position holds a NaN or an infinity in one element: the rows that see one are as the formula has
+    them, the others as without it."""
+    q, kc, vc, table, cu, kv = paged_case(lens, H, G, 64, dt, 16, seed=17, window=window)
+    clean = (q, kc, vc, table, cu, kv)
+    want, wl, tol, ltol = R.attention(*clean, window)
+    kb, vb = kc.clone(), vc.clone()
+    hit = torch.zeros(want.shape, dtype=torch.bool, device="cuda")
+    for b, n in enumerate(kv):
+        new = cu[b + 1] - cu[b]
+        for i, t in enumerate(range(n - 20, max(0, n - 250), -37)):
+            g, e = i % G, (5 * i) % 64
+            (kb, vb)[which - 1][table[b, t // 16].long(), g, t % 16, e] = math.nan if i % 2 == 0 else math.inf
+            for j in range(new):
+                p = n - new + j
+                if t <= p and (window == 0 or t > p - window):
+                    heads = slice(g * (H // G), (g + 1) * (H // G))
+                    if which == 1:
+                        hit[cu[b] + j, heads] = True
+                    else:
+                        hit[cu[b] + j, heads, e] = True
+    out, lse = run_attn(P, q, kb, vb, table, cu, kv, window)
+    assert P.pi_last_device_status() == 0
+    R.check(out[~hit], want[~hit], tol[~hit], "the rest")
+    ok = ~hit.any(-1) if which == 1 else torch.ones_like(lse, dtype=torch.bool)
+    R.check(lse[ok], wl[ok], ltol[ok], "lse")
+    if which == 2:
+        assert not bool(torch.isfinite(out[hit]).any())
+    assert 0 < int(hit.sum())
+
+
+@pytest.mark.parametrize("a", range(1, 8))
+def test_parts_whose_sums_add_up_past_fp32(P, a):
+    """Two keys, 83.5 nats above the rest, in any two of eight key tiles: where their parts are summed under the
+    maximum of what came before, each part's sum of weights is 2^127.5, and the two parts' is past fp32."""
+    for b in range(a):
+        q, kc, vc, table, cu, kv = paged_case([(1, 1001)], 1, 1, 64, BF16, 16, seed=23)
+        q.zero_()
+        q[..., 0] = 16.0
+        kc.zero_()
+        vc *= 2.0 ** -6
+        for t in (128 * a + 5, 128 * b + 77):
+            kc[table[0, t // 16].long(), 0, t % 16, 0] = 41.75          # q . k / 8 = 83.5
+        compare(P, (q, kc, vc, table, cu, kv))
+
+
+def test_two_parts_whose_sums_add_up_past_fp32(P):
+    """The same in items of thirty tiles that a border cuts in two."""
+    B, G, n = 12, 16, 3800
+    q, kc, vc, table, cu, kv = paged_case([(1, n)] * B, G, G, 64, BF16, 16, seed=24)
+    q.zero_()
+    q[..., 0] = 16.0
+    kc.zero_()
+    vc *= 2.0 ** -6
+    r = random.Random(1)
+    for b in range(B):
+        for g in range(G):
+            for t in r.sample(range(n), 2):
+                kc[table[b, t // 16].long(), g, t % 16, 0] = 41.75
+    compare(P, (q, kc, vc, table, cu, kv))
+
+
 # ------------------------------------------------------------------ parts of an item that meet
 
 @pytest.mark.parametrize("lens,H,G", [([(1, 3800)] * 12, 16, 16), ([(1, 2600 + 100 * i) for i in range(9)], 64, 8),
