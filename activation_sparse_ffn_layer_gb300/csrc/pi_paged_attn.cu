@@ -300,6 +300,19 @@ PI_DEV uint32_t pack2(float a, float b, __nv_bfloat16) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
+// Whether outputs are finite, after their rounding (the weights are rounded and
+// their sum is not, so a mean of the largest fp16 values may round past them):
+// 0 x both values of w + acc, which stays at zeros until an infinity or a NaN
+PI_DEV uint32_t times0(uint32_t w, uint32_t acc, __half) {
+    const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&w), __half2half2(__half(0.f)), *reinterpret_cast<const __half2*>(&acc));
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+PI_DEV uint32_t times0(uint32_t w, uint32_t acc, __nv_bfloat16) {
+    const __nv_bfloat162 v = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w), __bfloat162bfloat162(__nv_bfloat16(0.f)),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&acc));
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+PI_DEV bool is_odd(uint32_t acc) { return (acc & 0x7fff7fffu) != 0; }   // zeros of either sign are not
 // two fp32 values in one 64-bit register pair: a * b + c on both
 PI_DEV uint64_t pair2(float x, float y) {
     uint64_t r;
@@ -698,7 +711,8 @@ __device__ __noinline__ bool join_parts(const PagedArgs& a, const Piece& p, bool
     T* dst = static_cast<T*>(a.out) + orow * a.o_stride + (long long)head * DH;
     const int end = (c0 + cols) / 4;
     float M = -INFINITY, L = 0.f, use = 0.f, inv = 0.f;
-    bool first = true, odd = false;
+    bool first = true;
+    uint32_t odd = 0;
     for (int c = c0 / 4 + cg; c < end; c += CS * step) {
         float4 v[CS];
 #pragma unroll
@@ -747,14 +761,14 @@ __device__ __noinline__ bool join_parts(const PagedArgs& a, const Piece& p, bool
 #pragma unroll
         for (int j = 0; j < CS; ++j)
             if (c + j * step < end) {
-                v[j] = make_float4(v[j].x * inv, v[j].y * inv, v[j].z * inv, v[j].w * inv);
-                odd |= !(fabsf(v[j].x) + fabsf(v[j].y) + fabsf(v[j].z) + fabsf(v[j].w) < INFINITY);
-                *reinterpret_cast<uint2*>(dst + 4 * (c + j * step)) = make_uint2(pack2(v[j].x, v[j].y, T()), pack2(v[j].z, v[j].w, T()));
+                const uint2 y = make_uint2(pack2(v[j].x * inv, v[j].y * inv, T()), pack2(v[j].z * inv, v[j].w * inv, T()));
+                *reinterpret_cast<uint2*>(dst + 4 * (c + j * step)) = y;
+                odd = times0(y.y, times0(y.x, odd, T()), T());
             }
     }
     if (a.lse != nullptr && c0 == 0 && cg == 0)
         a.lse[orow * a.heads + head] = L == 0.f ? -INFINITY : (M - kLift + log2f(L)) * kLn2;
-    return odd;
+    return is_odd(odd);
 }
 
 // ------------------------------------------------------------ softmax (warps 0-7)
@@ -937,7 +951,7 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
                     l = mine_k == 0 ? fmaf(x.y, f_there, l * f_here) : fmaf(l, f_here, x.y * f_there);
                     m = M;
                 }
-                bool odd = false;   // some output is not finite
+                uint32_t odd = 0;   // not 0: some output is not finite
                 const float inv = inverse(l);
                 const float4* pt = reinterpret_cast<const float4*>(a.part_o + (size_t)there * DH * a.part_rows) + (live ? r : 0);
                 // a whole item's 1 / l goes into what the groups' O count for
@@ -975,21 +989,15 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
                                                 : fmaf(v[e], f_here, fmaf(z, f_there, 0.f))) * inv;
                         }
                     }
-                    if (whole || last) {
-                        uint64_t check[2] = {0, 0};
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) check[(e >> 1) & 1] = fma2(pair2(v[e], v[e + 1]), 0, check[(e >> 1) & 1]);
-                        float z0, z1;
-                        split2(add2(check[0], check[1]), z0, z1);
-                        odd |= z0 + z1 != 0.f;   // NaN: some value is not finite
-                    }
                     if (live && (whole || last)) {
                         T* dst = static_cast<T*>(a.out) + orow * a.o_stride + (long long)head * DH + i;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-                            *reinterpret_cast<uint4*>(dst + e) =
-                                make_uint4(pack2(v[e], v[e + 1], T()), pack2(v[e + 2], v[e + 3], T()),
-                                           pack2(v[e + 4], v[e + 5], T()), pack2(v[e + 6], v[e + 7], T()));
+                        for (int e = 0; e < 32; e += 8) {
+                            const uint4 y = make_uint4(pack2(v[e], v[e + 1], T()), pack2(v[e + 2], v[e + 3], T()),
+                                                       pack2(v[e + 4], v[e + 5], T()), pack2(v[e + 6], v[e + 7], T()));
+                            *reinterpret_cast<uint4*>(dst + e) = y;
+                            odd = times0(y.w, times0(y.z, times0(y.y, times0(y.x, odd, T()), T()), T()), T());
+                        }
                     } else if (live) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
@@ -1000,8 +1008,8 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
                 if (whole || last) {
                     if (live && a.lse != nullptr && c0 == 0)
                         a.lse[orow * a.heads + head] = l == 0.f ? -INFINITY : (m - kLift + log2f(l)) * kLn2;
-                    odd = __any_sync(FULL, live && odd);
-                    if (lane == 0 && odd) sh.redo = 1;
+                    const bool again = __any_sync(FULL, is_odd(odd));
+                    if (lane == 0 && again) sh.redo = 1;
                     if (lane == 0 && last) {
                         *arrivals = 0;
                         atomicOr(&sh.joined[p.own], 1 << warp);
@@ -1024,12 +1032,11 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
                     continue;
                 }
                 const int rows = min(32, tile_rows - 32 * quad);
-                odd = join_parts<T, DH>(a, p, pair, w, 32 * quad, rows, tok0, c0, cols);
-                odd = __any_sync(FULL, odd);
+                const bool again = __any_sync(FULL, join_parts<T, DH>(a, p, pair, w, 32 * quad, rows, tok0, c0, cols));
                 if (lane == 0) {
                     *arrivals = 0;
                     atomicOr(&sh.joined[p.own], 1 << warp);
-                    if (odd) sh.redo = 1;
+                    if (again) sh.redo = 1;
                 }
                 break;
             }

@@ -227,6 +227,16 @@ def test_two_parts_whose_sums_add_up_past_fp32(P):
     compare(P, (q, kc, vc, table, cu, kv))
 
 
+@pytest.mark.parametrize("lens", [[(1, 1001), (1, 300)], [(200, 900)]])
+@pytest.mark.parametrize("value", [65504.0, -65504.0])
+def test_values_at_the_end_of_fp16(P, lens, value):
+    """Any mean of equal values is that value: weights rounded up must not push it over the largest fp16."""
+    q, kc, vc, table, cu, kv = paged_case(lens, 16, 4, 64, F16, 16, seed=25, gain=2.0)
+    kc *= torch.linspace(0.1, 1.0, kc.shape[0], device="cuda")[:, None, None, None].half()
+    vc.fill_(value)
+    compare(P, (q, kc, vc, table, cu, kv), scale=0.5)
+
+
 # ------------------------------------------------------------------ parts of an item that meet
 
 @pytest.mark.parametrize("lens,H,G", [([(1, 3800)] * 12, 16, 16), ([(1, 2600 + 100 * i) for i in range(9)], 64, 8),
