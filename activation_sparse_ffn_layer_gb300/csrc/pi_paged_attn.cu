@@ -90,6 +90,7 @@ constexpr int kMinUnits = 5;
 constexpr float kLift = 7.f;           // log2 of the factor that P, l and O share
 constexpr float kGrow = 8.f;           // fp16: growth (log2) of a maximum before m follows
 constexpr float kSum = 1073741824.f;   // bf16: sum of a tile's weights from which m follows
+constexpr float kSink = 31.f;          // rows taken again: -log2 of the factor of their weights
 constexpr float kLn2 = 0.69314718055994531f;
 
 template <int DH>
@@ -1063,6 +1064,10 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
 // been joined by different blocks, and each takes its half again.  No role waits
 // on this, so a long cache cannot make a wait run out.
 //
+// Weights carry a factor 2^-kSink, so that the sum of 2^30 of them, each 2^-31 at
+// most, times the largest bf16 value stays in fp32; weights down to 2^-118 of the
+// largest count in full.
+//
 // A warp per row, eight rows at a time over tiles of 64 keys in shared memory, a
 // lane per key for the scores and per column for the sums.  A tile starts at a
 // multiple of 64 whatever rows share it: same bits every time.
@@ -1201,7 +1206,7 @@ __device__ __noinline__ void redo_rows(const PagedArgs& a, PagedShared<DH>& sh, 
 #pragma unroll
                 for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, d));
                 const float use = top == -INFINITY ? 0.f : top, f = exp2f(m - use);
-                const float w[2] = {exp2f(s[0] - use), exp2f(s[1] - use)};
+                const float w[2] = {exp2f(s[0] - use - kSink), exp2f(s[1] - use - kSink)};
                 m = top;
                 l = l * f + (w[0] + w[1]);
 #pragma unroll
@@ -1233,7 +1238,7 @@ __device__ __noinline__ void redo_rows(const PagedArgs& a, PagedShared<DH>& sh, 
                     for (int e = 0; e < E; ++e) dst[e] = T(l == 0.f ? 0.f : o[e] / l);
                 }
                 if (a.lse != nullptr && (entry & 1) && lane == 0)
-                    a.lse[row * a.heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+                    a.lse[row * a.heads + head] = l == 0.f ? -INFINITY : (m + log2f(l * exp2f(kSink))) * kLn2;
             }
             __syncwarp();
         }

@@ -237,6 +237,14 @@ def test_values_at_the_end_of_fp16(P, lens, value):
     compare(P, (q, kc, vc, table, cu, kv), scale=0.5)
 
 
+@pytest.mark.parametrize("lens", [[(1, 1001), (1, 300)], [(200, 900)]])
+def test_values_near_the_end_of_bf16(P, lens):
+    """Values of up to 3.2e38: their weighted mean is finite, whatever factor the weights carry on the way."""
+    q, kc, vc, table, cu, kv = paged_case(lens, 4, 2, 64, BF16, 16, seed=26)
+    vc.copy_((vc.float().clamp(-3.2, 3.2) * 1e38))
+    compare(P, (q, kc, vc, table, cu, kv))
+
+
 # ------------------------------------------------------------------ parts of an item that meet
 
 @pytest.mark.parametrize("lens,H,G", [([(1, 3800)] * 12, 16, 16), ([(1, 2600 + 100 * i) for i in range(9)], 64, 8),
