@@ -170,7 +170,8 @@ struct PagedShared {
     int abort_flag;
     int redo;            // some row that this block has written is not finite
     int joined[2];       // warps that have written the outputs of a cut item (by Piece::own), a bit each
-    int odd_rows;        // rows of a piece to be taken again
+    int odd_rows, redo_rows;   // rows of a piece that are not finite, and those of them to be taken again
+    int bad_keys, bad_k;       // keys of a piece with values that are not finite, and whether a key itself has one
 };
 
 PI_DEV Request request(const PagedArgs& a, int b, bool* bad) {
@@ -1064,6 +1065,16 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
 // been joined by different blocks, and each takes its half again.  No role waits
 // on this, so a long cache cannot make a wait run out.
 //
+// Most such rows see the value themselves, and then it settles them without
+// their sums: a score of NaN or infinity makes the row NaN, and a weight is above
+// 0, so an element of the output is the sum of the infinities and NaN that its
+// column holds.  One pass over the piece's keys and values finds those (the first
+// kBadKeys of them, and per column which kinds there are); rows that it leaves
+// open (a value that the row does not see, an overflow) are taken again.  A chunk
+// of 4096 tokens behind 12288 with a NaN at its request's fourth position takes
+// 5.0 ms so and 417 with all rows taken again (1.13 without the NaN); a token
+// behind 131 thousand keys 7.0 ms, 17.4 and 0.33: one block reads its keys again.
+//
 // Weights carry a factor 2^-kSink, so that the sum of 2^30 of them, each 2^-31 at
 // most, times the largest bf16 value stays in fp32; weights down to 2^-118 of the
 // largest count in full.
@@ -1088,6 +1099,131 @@ PI_DEV void row_sees(const PagedArgs& a, const Piece& p, int t, int* lo, int* hi
     *lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
 }
 
+// where a key's elements are, or -1 for a page outside the cache (reads as zeros)
+PI_DEV long long key_at(const PagedArgs& a, const int32_t* pages, int g, int key, int shift) {
+    const int page = pages[key >> shift];
+    if (page < 0 || page >= a.num_pages) return -1;
+    return page * a.page_stride + g * a.head_stride + (key & (a.page_size - 1)) * a.token_stride;
+}
+
+constexpr int kBadKeys = 32;
+template <int DH>
+struct Bad {
+    uint32_t key[kBadKeys];   // 4 x position + 1 (the key is bad) + 2 (the value)
+    int kinds[DH];            // per column of the values: 1 NaN, 2 +inf, 4 -inf
+};
+
+// Finds the keys lo .. hi - 1 of one request and KV head that hold something not finite.
+template <typename T, int DH>
+PI_DEV void find_bad(const PagedArgs& a, PagedShared<DH>& sh, Bad<DH>& bad, const Piece& p, int shift) {
+    constexpr int CHUNKS = DH / 8, AT_ONCE = 256 / CHUNKS, N = 4;
+    const int tid = threadIdx.x, lane = tid & 31, chunk = tid % CHUNKS;
+    const int32_t* pages = a.table + (size_t)p.b * a.max_pages;
+    for (int base = p.lo; base < p.hi; base += N * AT_ONCE) {
+        uint4 k[N], v[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int key = base + i * AT_ONCE + tid / CHUNKS;
+            k[i] = v[i] = make_uint4(0u, 0u, 0u, 0u);
+            const long long at = key < p.hi ? key_at(a, pages, p.g, key, shift) : -1;
+            if (at < 0) continue;
+            k[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.k) + at + chunk * 8);
+            v[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v) + at + chunk * 8);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const bool bk = is_odd(times0(k[i].w, times0(k[i].z, times0(k[i].y, times0(k[i].x, 0u, T()), T()), T()), T()));
+            const bool bv = is_odd(times0(v[i].w, times0(v[i].z, times0(v[i].y, times0(v[i].x, 0u, T()), T()), T()), T()));
+            // the lanes of a key
+            const unsigned of = (CHUNKS == 16 ? 0xffffu : 0xffu) << (lane & ~(CHUNKS - 1));
+            const unsigned mk = __ballot_sync(FULL, bk) & of, mv = __ballot_sync(FULL, bv) & of;
+            if (bv) {
+                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    float f[2];
+                    widen2(w[e / 2], f[0], f[1], T());
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        if (!(fabsf(f[j]) < INFINITY))
+                            atomicOr(&bad.kinds[chunk * 8 + e + j], f[j] != f[j] ? 1 : f[j] > 0.f ? 2 : 4);
+                }
+            }
+            if ((mk | mv) != 0 && lane == __ffs(mk | mv) - 1) {
+                const int n = atomicAdd(&sh.bad_keys, 1);
+                if (n < kBadKeys)
+                    bad.key[n] = 4u * (uint32_t)(base + i * AT_ONCE + tid / CHUNKS) + (mk != 0 ? 1u : 0u) + (mv != 0 ? 2u : 0u);
+                if (mk != 0) sh.bad_k = 1;
+            }
+        }
+    }
+}
+
+// Settles a row (a warp; entry: 4 x row of the piece + halves) from the bad keys
+// that it sees.  False: it has to be taken again.
+template <typename T, int DH>
+PI_DEV bool settle_row(const PagedArgs& a, const PagedShared<DH>& sh, const Bad<DH>& bad, const Piece& p,
+                                        int entry, int shift) {
+    constexpr int E = DH / 32;
+    const int lane = threadIdx.x & 31, x = entry >> 2;
+    const long long row = p.cu + p.tok0 + x / a.group;
+    const int head = p.g * a.group + x % a.group;
+    const int32_t* pages = a.table + (size_t)p.b * a.max_pages;
+    const T* src = static_cast<const T*>(a.q) + row * a.q_stride + (long long)head * DH + lane * E;
+    T* dst = static_cast<T*>(a.out) + row * a.o_stride + (long long)head * DH + lane * E;
+    float q[E], o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        q[e] = to_f(src[e]);
+        o[e] = 0.f;
+    }
+    int lo, hi;
+    row_sees(a, p, x / a.group, &lo, &hi);
+    const bool all = sh.bad_keys <= kBadKeys;
+    bool none = false;   // a score of NaN or +inf: no element is a number
+    for (int i = 0; i < min(sh.bad_keys, kBadKeys) && !none; ++i) {
+        const uint32_t what = bad.key[i];
+        const int key = (int)(what >> 2);
+        if (key < lo || key >= hi) continue;
+        const long long at = key_at(a, pages, p.g, key, shift) + lane * E;
+        float s = 0.f;
+        if (what & 1u) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) s = fmaf(q[e], to_f(static_cast<const T*>(a.k)[at + e]), s);
+            s = warp_sum(s) * a.scale;
+            none = !(s < INFINITY);
+        }
+        if (what & 2u) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float v = to_f(static_cast<const T*>(a.v)[at + e]);
+                if (!(fabsf(v) < INFINITY)) o[e] += s == -INFINITY ? NAN : v;
+            }
+        }
+    }
+    const bool own = (entry >> (lane >> 4)) & 1;
+    bool open = false, every = true;
+    bool put[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        put[e] = !(fabsf(to_f(dst[e])) < INFINITY);   // the element is not finite
+        every &= put[e];
+        // its kind is known: NaN, or one infinity that is the only kind there is
+        const int kinds = bad.kinds[lane * E + e];
+        const bool known = o[e] != o[e] || (!(fabsf(o[e]) < INFINITY) && (all || (kinds & (kinds - 1)) == 0));
+        open |= put[e] && !known;
+    }
+    // where all elements are not finite, the row's sum of weights need not be
+    if (!none && (__any_sync(FULL, own && open) || __all_sync(FULL, !own || every) || (!all && sh.bad_k != 0))) return false;
+    if (own) {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (none || put[e]) dst[e] = T(none ? NAN : o[e]);
+    }
+    if (none && a.lse != nullptr && (entry & 1) && lane == 0) a.lse[row * a.heads + head] = NAN;
+    return true;
+}
+
 template <typename T, int DH>
 __device__ __noinline__ void redo_rows(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* smem, Walk walk) {
     constexpr int KT = 64, CHUNKS = DH / 8, ROW = DH * 2 + 16, E = DH / 32, EACH = KT * CHUNKS / 256;
@@ -1095,14 +1231,18 @@ __device__ __noinline__ void redo_rows(const PagedArgs& a, PagedShared<DH>& sh, 
     float* const q = reinterpret_cast<float*>(smem) + warp * DH;   // this warp's query
     unsigned char* const kt = smem + 8 * DH * 4;                    // keys, rows 16 bytes apart in banks
     unsigned char* const vt = kt + KT * ROW;
-    int* const list = reinterpret_cast<int*>(vt + KT * DH * 2);     // 4 x row + halves (bits)
+    int* const odd = reinterpret_cast<int*>(vt + KT * DH * 2);      // 4 x row + halves (bits)
+    int* const list = odd + 2 * kTileRows;                          // those that are taken again
+    Bad<DH>& bad = *reinterpret_cast<Bad<DH>*>(list + 2 * kTileRows);
+    const int shift = __ffs(a.page_size) - 1;
     const float c = a.scale / kLn2;
     for (;;) {
         sync_softmax();
         if (tid == 0) {
             sh.list[0] = walk.next(a);
-            sh.odd_rows = 0;
+            sh.odd_rows = sh.redo_rows = sh.bad_keys = sh.bad_k = 0;
         }
+        if (tid < DH) bad.kinds[tid] = 0;
         sync_softmax();
         const Piece p = sh.list[0];
         if (p.nt == 0) return;
@@ -1114,15 +1254,21 @@ __device__ __noinline__ void redo_rows(const PagedArgs& a, PagedShared<DH>& sh, 
             if (own == 0) continue;
             const T* o = static_cast<const T*>(a.out) + (long long)(p.cu + p.tok0 + t) * a.o_stride +
                          (long long)(p.g * a.group + x % a.group) * DH + lane * E;
-            bool odd = false;
+            bool some = false;
 #pragma unroll
-            for (int e = 0; e < E; ++e) odd |= !(fabsf(to_f(o[e])) < INFINITY);
-            const unsigned who = __ballot_sync(FULL, odd);
+            for (int e = 0; e < E; ++e) some |= !(fabsf(to_f(o[e])) < INFINITY);
+            const unsigned who = __ballot_sync(FULL, some);
             const int halves = own & ((who & 0xffffu ? 1 : 0) | (who >> 16 ? 2 : 0));
-            if (halves != 0 && lane == 0) list[atomicAdd(&sh.odd_rows, 1)] = 4 * x + halves;
+            if (halves != 0 && lane == 0) odd[atomicAdd(&sh.odd_rows, 1)] = 4 * x + halves;
         }
         sync_softmax();
-        const int n = sh.odd_rows;
+        if (sh.odd_rows == 0) continue;
+        find_bad<T, DH>(a, sh, bad, p, shift);
+        sync_softmax();
+        for (int i = warp; i < sh.odd_rows; i += 8)
+            if (!settle_row<T, DH>(a, sh, bad, p, odd[i], shift) && lane == 0) list[atomicAdd(&sh.redo_rows, 1)] = odd[i];
+        sync_softmax();
+        const int n = sh.redo_rows;
         const int32_t* pages = a.table + (size_t)p.b * a.max_pages;
         for (int i0 = 0; i0 < n; i0 += 8) {
             // the rows' keys together, and this warp's
@@ -1158,13 +1304,10 @@ __device__ __noinline__ void redo_rows(const PagedArgs& a, PagedShared<DH>& sh, 
                 for (int i = 0; i < EACH; ++i) {
                     const int at = tid + 256 * i, key = base + at / CHUNKS;
                     k[i] = v[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (key < from || key >= to) continue;
-                    const int page = pages[key / a.page_size];
-                    if (page < 0 || page >= a.num_pages) continue;   // reads as zeros
-                    const long long e = page * a.page_stride + p.g * a.head_stride + (key % a.page_size) * a.token_stride +
-                                        at % CHUNKS * 8;
-                    k[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.k) + e);
-                    v[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v) + e);
+                    const long long e = key >= from && key < to ? key_at(a, pages, p.g, key, shift) : -1;
+                    if (e < 0) continue;
+                    k[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.k) + e + at % CHUNKS * 8);
+                    v[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v) + e + at % CHUNKS * 8);
                 }
             };
             int base = from / KT * KT;
@@ -1211,22 +1354,32 @@ __device__ __noinline__ void redo_rows(const PagedArgs& a, PagedShared<DH>& sh, 
                 l = l * f + (w[0] + w[1]);
 #pragma unroll
                 for (int e = 0; e < E; ++e) o[e] *= f;
-                for (int x = max(lo - base, 0); x < min(hi - base, KT); ++x) {
-                    const float wx = __shfl_sync(FULL, x < 32 ? w[0] : w[1], x & 31);
+                const int x0 = max(lo - base, 0), x1 = min(hi - base, KT);
+                auto value = [&](int x, float (&y)[E]) {
                     const uint32_t* src = reinterpret_cast<const uint32_t*>(vt + (x * DH + lane * E) * 2);
-                    float y[E];
 #pragma unroll
                     for (int e = 0; e < E; e += 2) widen2(src[e / 2], y[e], y[e + 1], T());
-                    if (wx == 0.f) {
-                        // e^a is not 0 but for a = -inf, so infinities count although the weight's fp32 is 0
-                        const float sx = __shfl_sync(FULL, x < 32 ? s[0] : s[1], x & 31);
-#pragma unroll
-                        for (int e = 0; e < E; ++e)
-                            if (sx > -INFINITY && !(fabsf(y[e]) < INFINITY)) o[e] += y[e];
-                            else o[e] = fmaf(0.f, y[e], o[e]);
-                    } else {
+                };
+                if (!__any_sync(FULL, (w[0] == 0.f && s[0] > -INFINITY) || (w[1] == 0.f && s[1] > -INFINITY))) {
+#pragma unroll 8
+                    for (int x = x0; x < x1; ++x) {
+                        const float wx = __shfl_sync(FULL, x < 32 ? w[0] : w[1], x & 31);
+                        float y[E];
+                        value(x, y);
 #pragma unroll
                         for (int e = 0; e < E; ++e) o[e] = fmaf(wx, y[e], o[e]);
+                    }
+                } else {
+                    // e^a is not 0 but for a = -inf, so infinities count although the weight's fp32 is 0
+#pragma unroll 1
+                    for (int x = x0; x < x1; ++x) {
+                        const float wx = __shfl_sync(FULL, x < 32 ? w[0] : w[1], x & 31);
+                        const float sx = __shfl_sync(FULL, x < 32 ? s[0] : s[1], x & 31);
+                        float y[E];
+                        value(x, y);
+#pragma unroll
+                        for (int e = 0; e < E; ++e)
+                            o[e] = wx == 0.f && sx > -INFINITY && !(fabsf(y[e]) < INFINITY) ? o[e] + y[e] : fmaf(wx, y[e], o[e]);
                     }
                 }
             }

@@ -490,7 +490,10 @@ PI_API size_t pi_paged_workspace_bytes(const pi_paged_desc *desc, const pi_page_
  * cache's type, rows q_stride and out_stride elements apart (multiples of 8);
  * lse [max_tokens, heads] fp32, or NULL.  Rows past cu_new[batch] are left
  * alone.  Positions that no token of the request sees are not used, whatever
- * they hold.  Products of 16-bit values are summed in fp32; the weights
+ * they hold.  An infinity or NaN reaches the tokens that see it and no others.
+ * A call with any takes longer: the rows that are not finite are looked at again
+ * by the block that wrote them (a token behind 131 thousand keys 7 ms instead of
+ * 0.3, a chunk of 4096 tokens behind 12288 5 ms instead of 1.1).  Products of 16-bit values are summed in fp32; the weights
  * e^{a_t - m} enter the second product rounded to the cache's type.  The
  * result does not depend on timing (bitwise reproducible on one device).
  * An inconsistent row (cu_new decreasing or past max_tokens, more than max_new

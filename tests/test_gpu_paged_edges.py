@@ -196,6 +196,59 @@ def test_bad_values_among_masked_places(P, lens, H, G, window, dt, which):
     assert 0 < int(hit.sum())
 
 
+@pytest.mark.parametrize("dt", [F16, BF16])
+@pytest.mark.parametrize("lens,H,G,window", [([(300, 700), (1, 90)], 8, 2, 0), ([(1, 3000)], 4, 1, 0), ([(150, 900)], 2, 2, 333)])
+def test_many_bad_values_and_their_kinds(P, lens, H, G, window, dt):
+    """Far more bad values than one: column 5 holds +inf from position 400 on (at every position), column 6 +inf at 401
+    and -inf at 450, column 7 NaN and infinities, column 8 -inf at 640 alone.  An output element is the sum of what its
+    column shows the row; the other elements and the log-sums are as without."""
+    q, kc, vc, table, cu, kv = paged_case(lens, H, G, 64, dt, 16, seed=19, window=window)
+    want, wl, tol, ltol = R.attention(q, kc, vc, table, cu, kv, window)
+    inf, bad = math.inf, []
+    n = kv[0]
+    bad += [(5, t, inf) for t in range(400, n)] + [(6, 401, inf), (6, 450, -inf), (8, 640, -inf)]
+    bad += [(7, t, math.nan if t % 3 == 0 else inf) for t in range(500, min(n, 560), 2)]
+    for e, t, x in bad:
+        vc[table[0, t // 16].long(), 0, t % 16, e] = x
+    for i in range(lens[0][0]):
+        p = n - lens[0][0] + i
+        lo = max(0, p - window + 1) if window > 0 else 0
+        for e in (5, 6, 7, 8):
+            seen = [x for f, t, x in bad if f == e and lo <= t <= p]
+            if seen:
+                want[i, :H // G, e] = sum(seen)
+    out, lse = run_attn(P, q, kc, vc, table, cu, kv, window)
+    assert P.pi_last_device_status() == 0 and not bool(torch.isfinite(want).all())
+    R.check(out, want, tol, "out")
+    R.check(lse, wl, ltol, "lse")
+    assert torch.equal(out.double()[torch.isinf(want)], want[torch.isinf(want)])    # of the right sign
+
+
+@pytest.mark.parametrize("dt", [F16, BF16])
+@pytest.mark.parametrize("many", [1, 200])
+@pytest.mark.parametrize("lens,H,G", [([(200, 700)], 4, 2), ([(1, 3000)], 8, 1)])
+def test_infinite_keys(P, lens, H, G, many, dt):
+    """Keys with an infinity: rows whose query points along it have no number left, rows that point the other way are
+    as with a key that they give no weight."""
+    q, kc, vc, table, cu, kv = paged_case(lens, H, G, 64, dt, 16, seed=20)
+    q[..., 4] = torch.where(torch.arange(H, device="cuda") % 2 == 0, -2.0, 2.0).to(dt)
+    q[:, :, 4] *= torch.where(torch.arange(q.shape[0], device="cuda") % 3 == 0, -1.0, 1.0).to(dt)[:, None]
+    far, n = kc.clone(), kv[0]
+    at = range(100, 100 + many)
+    for t in at:
+        page = table[0, t // 16].long()
+        far[page, :, t % 16, 4] = 2000.0       # scores of -500 and less where the query points the other way
+        kc[page, :, t % 16, 4] = math.inf
+    want, wl, tol, ltol = R.attention(q, far, vc, table, cu, kv)
+    out, lse = run_attn(P, q, kc, vc, table, cu, kv)
+    assert P.pi_last_device_status() == 0
+    away = (q[..., 4] < 0)
+    assert bool(away.any()) and not bool(away.all())
+    R.check(out[away], want[away], tol[away], "out")
+    R.check(lse[away], wl[away], ltol[away], "lse")
+    assert bool(torch.isnan(out[~away]).all()) and not bool(torch.isfinite(lse[~away]).any())
+
+
 @pytest.mark.parametrize("a", range(1, 8))
 def test_parts_whose_sums_add_up_past_fp32(P, a):
     """Two keys, 83.5 nats above the rest, in any two of eight key tiles: where their parts are summed under the
