@@ -238,6 +238,12 @@ bool fc2_args_ok(const Plan& p, const float* h, const int32_t* idx, const int32_
                  const pi_layer_weights* w, const float* y);
 LayerPtrs layer_ptrs(const pi_layer_weights* w);
 
+// Whether two arrays of n rows share memory: rows of `width` bytes, `stride`
+// bytes apart.  Rows of one stride may lie side by side; of two strides, the
+// whole ranges have to be apart.
+bool rows_overlap(const void* a, long long a_stride, long long a_width, const void* b, long long b_stride,
+                  long long b_width, long long n);
+
 // Checks of a paged cache's description (sizes, strides, type).
 bool page_desc_ok(const pi_page_desc& c);
 

@@ -481,6 +481,17 @@ int page_shift(int page_size) { return page_size == 16 ? 4 : page_size == 32 ? 5
 
 }  // namespace
 
+bool rows_overlap(const void* a, long long a_stride, long long a_width, const void* b, long long b_stride,
+                  long long b_width, long long n) {
+    if (a == nullptr || b == nullptr || n < 1) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    if (x + (uintptr_t)((n - 1) * a_stride + a_width) <= y || y + (uintptr_t)((n - 1) * b_stride + b_width) <= x) return false;
+    if (n == 1 || a_stride != b_stride) return true;
+    // how far b's rows begin behind a's, within a stride
+    const long long d = y >= x ? (long long)((y - x) % a_stride) : (a_stride - (long long)((x - y) % a_stride)) % a_stride;
+    return d < a_width || d + b_width > a_stride;
+}
+
 bool page_desc_ok(const pi_page_desc& c) {
     if (c.kv_heads < 1 || c.kv_heads > 1024 || (c.head_dim != 64 && c.head_dim != 128) || !page_size_ok(c.page_size) ||
         c.num_pages < 1 || c.num_pages > (1 << 26) || (c.dtype != PI_T_F16 && c.dtype != PI_T_BF16))

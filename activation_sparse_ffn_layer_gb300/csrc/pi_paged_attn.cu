@@ -1666,6 +1666,8 @@ pi_status pi_paged_attn(const pi_paged_desc* desc, const pi_page_desc* cache, co
     const int blocks = paged_blocks();
     const PagedLayout lay(*desc, *cache, std::max(1, blocks));
     if (!aligned(workspace, 16) || ws_bytes < lay.total) return PI_ERR_WORKSPACE;
+    // rows that are not finite are computed again from q after outputs are written
+    if (rows_overlap(q, 2 * q_stride, 2 * width, out, 2 * out_stride, 2 * width, desc->max_tokens)) return PI_ERR_INVALID_ARG;
     PagedArgs a{};
     char* ws = static_cast<char*>(workspace);
     a.q = q;

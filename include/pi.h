@@ -487,7 +487,8 @@ PI_API size_t pi_paged_workspace_bytes(const pi_paged_desc *desc, const pi_page_
  * for each query head h with key/value head h / (heads / kv_heads).  A token
  * that sees nothing (its request has fewer positions than tokens, e.g. kv_len
  * 0) gets zeros and lse -inf.  q [max_tokens, heads, head_dim] and out have the
- * cache's type, rows q_stride and out_stride elements apart (multiples of 8);
+ * cache's type, rows q_stride and out_stride elements apart (multiples of 8),
+ * and share no memory (they may lie side by side in rows of one stride);
  * lse [max_tokens, heads] fp32, or NULL.  Rows past cu_new[batch] are left
  * alone.  Positions that no token of the request sees are not used, whatever
  * they hold.  An infinity or NaN reaches the tokens that see it and no others.

@@ -313,3 +313,27 @@ def test_parts_that_meet_give_the_same_bits(P, lens, H, G):
     for _ in range(60):
         again = run_attn(P, *case, ws=ws)
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+# ------------------------------------------------------------------ the cache object and the binding
+
+def test_outputs_beside_their_queries(P):
+    """Queries and outputs in one buffer: alternate parts of its rows, and one after the other."""
+    q, kc, vc, table, cu, kv = paged_case([(1, 700), (90, 90), (2, 33)], 8, 2, 64, F16, 16, seed=29)
+    want, _ = compare(P, (q, kc, vc, table, cu, kv))
+    T, row = q.shape[0], 8 * 64
+    both = torch.full((T, 2 * row), 3.0, device="cuda").half()
+    for a, b in ((0, row), (row, 0)):
+        x, y = (both[:, i:i + row].unflatten(1, (8, 64)) for i in (a, b))
+        x.copy_(q)
+        run_attn(P, x, kc, vc, table, cu, kv, out=y)
+        assert torch.equal(y, want) and torch.equal(x, q)
+    for a, b in ((0, T), (T, 0)):
+        line = both.view(2 * T, 8, 64)
+        x, y = line[a:a + T], line[b:b + T]
+        x.copy_(q)
+        run_attn(P, x, kc, vc, table, cu, kv, out=y)
+        assert torch.equal(y, want) and torch.equal(x, q)
+    for y in (x, line[1:1 + T] if a == 0 else line[T - 1:2 * T - 1]):
+        with pytest.raises(P.PiError):
+            run_attn(P, x, kc, vc, table, cu, kv, out=y)
