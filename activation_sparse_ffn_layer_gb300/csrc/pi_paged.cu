@@ -611,10 +611,19 @@ pi_status pi_rope_store(const pi_rope_plan* plan, const pi_page_desc* cache, con
     if (d.tokens == 0) return PI_OK;
     if (!positions || !aligned(positions, 4)) return PI_ERR_INVALID_ARG;
     if (has_q && (!q || !q_out || !aligned(q, 16) || !aligned(q_out, 16))) return PI_ERR_INVALID_ARG;
-    // in place: a thread reads all it writes first, if the elements lie alike
-    if (has_q && q == q_out && (d.dtype != cache->dtype || d.q_stride != d.out_stride)) return PI_ERR_INVALID_ARG;
     if (has_kv && (!k || !v || !kcache || !vcache || !slots || !aligned(k, 16) || !aligned(v, 16) ||
                    !aligned(kcache, 16) || !aligned(vcache, 16) || !aligned(slots, 8)))
+        return PI_ERR_INVALID_ARG;
+    // Rotated queries go over no input that another thread may still have to
+    // read.  In place a thread reads all it writes first, if the elements lie alike.
+    const long long in = d.dtype == PI_T_F32 ? 4 : 2, q_width = (long long)d.heads * cache->head_dim,
+                    k_width = (long long)cache->kv_heads * cache->head_dim;
+    auto over = [&](const void* x, long long stride, long long width) {
+        return rows_overlap(x, in * stride, in * width, q_out, 2 * d.out_stride, 2 * q_width, d.tokens);
+    };
+    const bool in_place = q == q_out && d.dtype == cache->dtype && d.q_stride == d.out_stride;
+    if (has_q && ((!in_place && over(q, d.q_stride, q_width)) ||
+                  (has_kv && (over(k, d.k_stride, k_width) || over(v, d.v_stride, k_width)))))
         return PI_ERR_INVALID_ARG;
     RopeArgs a{};
     a.q = q;

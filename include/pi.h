@@ -454,11 +454,12 @@ typedef struct {
  *   mscale (x1 cos a - x2 sin a), mscale (x2 cos a + x1 sin a);
  * the rest of the head and the values pass unchanged.  Arithmetic in fp32,
  * rounded once to the cache's type.  q_out [tokens, heads, head_dim] (type of
- * the cache; may be q where the types and strides agree); keys and values go
- * to slots[t] of kcache and vcache.  A token with slot -1 is rotated and not
- * stored; a slot past the cache or below -1 is not stored and sets the device
- * status to PI_ERR_INVALID_ARG.  q and q_out may both be NULL (store only), or
- * k, v, slots, kcache and vcache (rotate only).  All 16-byte aligned.
+ * the cache; may be q where the types and strides agree, and shares no other
+ * memory with q, k or v); keys and values go to slots[t] of kcache and
+ * vcache.  A token with slot -1 is rotated and not stored; a slot past the
+ * cache or below -1 is not stored and sets the device status to
+ * PI_ERR_INVALID_ARG.  q and q_out may both be NULL (store only), or k, v,
+ * slots, kcache and vcache (rotate only).  All 16-byte aligned.
  */
 PI_API pi_status pi_rope_store(const pi_rope_plan *plan, const pi_page_desc *cache, const pi_qkv_desc *desc,
                                const void *q, const void *k, const void *v, const int32_t *positions,
@@ -491,12 +492,13 @@ PI_API size_t pi_paged_workspace_bytes(const pi_paged_desc *desc, const pi_page_
  * and share no memory (they may lie side by side in rows of one stride);
  * lse [max_tokens, heads] fp32, or NULL.  Rows past cu_new[batch] are left
  * alone.  Positions that no token of the request sees are not used, whatever
- * they hold.  An infinity or NaN reaches the tokens that see it and no others.
- * A call with any takes longer: the rows that are not finite are looked at again
- * by the block that wrote them (a token behind 131 thousand keys 7 ms instead of
- * 0.3, a chunk of 4096 tokens behind 12288 5 ms instead of 1.1).  Products of 16-bit values are summed in fp32; the weights
- * e^{a_t - m} enter the second product rounded to the cache's type.  The
- * result does not depend on timing (bitwise reproducible on one device).
+ * they hold: an infinity or NaN reaches the tokens that see it and no others.
+ * A call that meets any takes longer, since the rows that are not finite are
+ * looked at again by the block that wrote them: 7 ms instead of 0.3 for a token
+ * behind 131 thousand keys, 5 ms instead of 1.1 for a chunk of 4096 tokens
+ * behind 12288.  Products of 16-bit values are summed in fp32; the weights
+ * e^{a_t - m} enter the second product rounded to the cache's type.  The result
+ * does not depend on timing (bitwise reproducible on one device).
  * An inconsistent row (cu_new decreasing or past max_tokens, more than max_new
  * tokens, kv_len outside 0 .. max_pages * page_size) is taken as one without
  * tokens (kv_len: without keys) and a page id outside the cache reads as

@@ -337,3 +337,20 @@ def test_outputs_beside_their_queries(P):
     for y in (x, line[1:1 + T] if a == 0 else line[T - 1:2 * T - 1]):
         with pytest.raises(P.PiError):
             run_attn(P, x, kc, vc, table, cu, kv, out=y)
+
+
+def test_rotation_in_place_of_packed_projections(P):
+    """Queries turned where they lie, between the keys and values that the same call stores."""
+    torch.manual_seed(2)
+    T, H, G, dh = 75, 6, 2, 64
+    packed = torch.randn(T, (H + 2 * G) * dh, device="cuda").half()
+    q, k, v = (x.unflatten(1, (-1, dh)) for x in packed.split([H * dh, G * dh, G * dh], dim=1))
+    pos, slots = torch.arange(T, device="cuda").int() * 77, torch.arange(T, device="cuda")
+    plan, got = P.rope_plan(dh, 32), []
+    for out in (torch.empty_like(q), q):
+        kc, vc = (torch.zeros(5, G, 16, dh, device="cuda").half() for _ in range(2))
+        P.pi_rope_store(plan, P.page_desc(kc, vc), q, k, v, pos, slots, out, kc, vc)
+        got.append((out.clone(), kc, vc))
+    assert all(torch.equal(a, b) for a, b in zip(*got)) and P.pi_last_device_status() == 0
+    with pytest.raises(P.PiError):
+        P.pi_rope_store(plan, P.page_desc(kc, vc), q, k, v, pos, slots, packed[:, 2 * dh:][:, :H * dh].unflatten(1, (H, dh)), kc, vc)
