@@ -401,6 +401,13 @@ def _flat(t: torch.Tensor, dtype: torch.dtype, least: int, name: str) -> int:
     return t.data_ptr()
 
 
+def _table(t: torch.Tensor, batch: int, max_pages: int) -> int:
+    """Address of a block table; with two dimensions its rows are max_pages apart."""
+    if t.dim() == 2 and t.shape[1] != max_pages:
+        raise ValueError(f"block_table: expected rows of {max_pages} entries")
+    return _flat(t, torch.int32, batch * max_pages, "block_table")
+
+
 def _rows(t: torch.Tensor, heads: int, head_dim: int, name: str) -> Tuple[int, int]:
     """Checks a [tokens, heads, head_dim] CUDA tensor whose tokens may be apart;
     returns its tokens and the elements between them."""
@@ -425,7 +432,7 @@ def pi_block_tables(desc, cached_len, new_len, held, held_out, block_table, free
     _check("pi_block_tables", lib().pi_block_tables(
         C.byref(desc), _flat(cached_len, i32, B, "cached_len"), _flat(new_len, i32, B, "new_len"),
         _flat(held, i32, B, "held"), _flat(held_out, i32, B, "held_out"),
-        _flat(block_table, i32, B * desc.max_pages, "block_table"), _flat(free_list, i32, desc.num_pages, "free_list"),
+        _table(block_table, B, desc.max_pages), _flat(free_list, i32, desc.num_pages, "free_list"),
         _flat(free_count, i32, 1, "free_count"), _flat(free_count_out, i32, 1, "free_count_out"),
         _flat(cu_new, i32, B + 1, "cu_new"), _flat(kv_len, i32, B, "kv_len"),
         _flat(slots, torch.int64, desc.max_tokens, "slots"), _flat(positions, i32, desc.max_tokens, "positions"),
@@ -528,7 +535,7 @@ def pi_paged_attn(desc, cache, q, kcache, vcache, block_table, cu_new, kv_len, o
         raise ValueError("q, out: expected max_tokens rows of the cache's type")
     _check("pi_paged_attn", lib().pi_paged_attn(
         C.byref(desc), C.byref(cache), q.data_ptr(), qs, _cache(cache, kcache, "kcache"),
-        _cache(cache, vcache, "vcache"), _flat(block_table, i32, B * desc.max_pages, "block_table"),
+        _cache(cache, vcache, "vcache"), _table(block_table, B, desc.max_pages),
         _flat(cu_new, i32, B + 1, "cu_new"), _flat(kv_len, i32, B, "kv_len"), out.data_ptr(), os_,
         None if lse is None else _flat(lse, torch.float32, T * H, "lse"), _flat(workspace, torch.uint8, 0, "workspace"),
         workspace.numel(), _stream()))

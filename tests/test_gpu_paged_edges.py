@@ -354,3 +354,17 @@ def test_rotation_in_place_of_packed_projections(P):
     assert all(torch.equal(a, b) for a, b in zip(*got)) and P.pi_last_device_status() == 0
     with pytest.raises(P.PiError):
         P.pi_rope_store(plan, P.page_desc(kc, vc), q, k, v, pos, slots, packed[:, 2 * dh:][:, :H * dh].unflatten(1, (H, dh)), kc, vc)
+
+
+def test_block_tables_of_another_width_are_refused(P):
+    """A table with more columns than the descriptor says would be read with the wrong row stride."""
+    q, kc, vc, table, cu, kv = paged_case([(1, 30), (1, 60)], 2, 1, 64, F16, 16)
+    wide = torch.cat([table, table], 1)
+    pg, d = P.page_desc(kc, vc), P.paged_desc(2, 2, 2, 1, table.shape[1])
+    ws = torch.zeros(P.pi_paged_workspace_bytes(d, pg), dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError, match="block_table"):
+        P.pi_paged_attn(d, pg, q, kc, vc, wide, i32(cu), i32(kv), torch.empty_like(q), None, ws)
+    with pytest.raises(ValueError, match="block_table"):
+        one, two = i32([1]), i32([1, 1])
+        P.pi_block_tables(P.tables_desc(2, 16, 8, 3, 2), two, two, two, two.clone(), i32([[0] * 4] * 2), i32([0] * 8), one,
+                          one.clone(), i32([0] * 3), two.clone(), torch.empty(2, dtype=torch.int64, device="cuda"), two.clone())
