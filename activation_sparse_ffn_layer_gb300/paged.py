@@ -82,7 +82,10 @@ class PagedCache:
                lse: Optional[torch.Tensor] = None) -> torch.Tensor:
         """Attention of the step's packed tokens in one layer: q [tokens, heads,
         head_dim], k and v [tokens, kv_heads, head_dim] as projected (fp16, bf16 or
-        fp32), out like q in the cache's type."""
+        fp32), out like q in the cache's type.  Rows of another number than the
+        step's tokens are refused: the attention would take a former step's."""
+        if q.shape[0] != self.tokens:
+            raise ValueError(f"expected the {self.tokens} tokens of the step")
         kc, vc, turned = self.kcache[layer], self.vcache[layer], self.q[:self.tokens]
         B.pi_rope_store(self.rope, self.pages, q, k, v, self.positions, self.slots, turned, kc, vc)
         B.pi_paged_attn(self.desc, self.pages, turned, kc, vc, self.table, self.cu, self.kv_len, out, lse, self.workspace)

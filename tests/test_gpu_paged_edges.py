@@ -368,3 +368,25 @@ def test_block_tables_of_another_width_are_refused(P):
         one, two = i32([1]), i32([1, 1])
         P.pi_block_tables(P.tables_desc(2, 16, 8, 3, 2), two, two, two, two.clone(), i32([[0] * 4] * 2), i32([0] * 8), one,
                           one.clone(), i32([0] * 3), two.clone(), torch.empty(2, dtype=torch.int64, device="cuda"), two.clone())
+
+
+def _small(**kw):
+    from activation_sparse_ffn_layer_gb300.paged import PagedCache
+    return PagedCache(4, 2, 64, 2, 64, 20, 30, page_size=16, **kw)
+
+
+def _qkv(T):
+    return torch.randn(T, 8, 64, device="cuda").half().split([4, 2, 2], 1)
+
+
+def test_attend_takes_the_tokens_of_its_step(P):
+    """Fewer rows than the step's tokens would leave the last step's queries in the rest."""
+    cache = _small()
+    cache.begin(i32([5, 4]), 9, 5)
+    cache.attend(0, *_qkv(9), torch.empty(9, 4, 64, device="cuda").half())
+    cache.begin(i32([2, 1]), 3, 2)
+    for T in (2, 4, 0):
+        with pytest.raises(ValueError):
+            cache.attend(0, *_qkv(T), torch.empty(3, 4, 64, device="cuda").half())
+    cache.attend(0, *_qkv(3), torch.empty(3, 4, 64, device="cuda").half())
+    assert P.pi_last_device_status() == 0
