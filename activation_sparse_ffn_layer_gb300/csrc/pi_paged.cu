@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kTabThreads) k_block_tables(const TablesArgs a
     int c[kTabPer], n[kTabPer], h[kTabPer];
     bool bad[kTabPer], over[kTabPer];
     // this thread's tokens (at most 2^42 over all rows), and from bit 44 on its
-    // rows that ask for more positions than their table row has
+    // rows whose positions leave their table row
     constexpr long long kOver = 1ll << 44;
     long long tok = 0;
     bool any_bad = false;
@@ -120,9 +120,9 @@ __global__ void __launch_bounds__(kTabThreads) k_block_tables(const TablesArgs a
             c[i] = a.cached[b];
             n[i] = a.fresh[b];
             h[i] = a.held[b];
-            bad[i] = c[i] < 0 || n[i] < 0 || h[i] < 0 || h[i] > a.max_pages || n[i] > capacity;
+            bad[i] = n[i] < 0 || h[i] < 0 || h[i] > a.max_pages || n[i] > capacity;
             if (bad[i]) n[i] = 0;
-            over[i] = !bad[i] && (long long)c[i] + n[i] > capacity;
+            over[i] = !bad[i] && (c[i] < 0 || (long long)c[i] + n[i] > capacity);
             bad[i] |= over[i];
             tok += n[i] + (over[i] ? kOver : 0);
         }
@@ -131,9 +131,9 @@ __global__ void __launch_bounds__(kTabThreads) k_block_tables(const TablesArgs a
     if (threadIdx.x == 0) free_in = *a.free_count;
     long long total_tok;
     long long tp = block_prefix(tok, warp_sums, &total_tok);
-    // the packed rows hold the tokens of rows that ask for too much as well, so
-    // those are counted (the rows after them would be moved); where the tokens
-    // do not all fit, the packed rows cannot hold them, and the others' are
+    // the packed rows hold the tokens of such rows as well, so those are counted
+    // (the rows after them would be moved); where the tokens do not all fit, the
+    // packed rows cannot hold them, and the others' are
     if (total_tok >= kOver) {
         if ((total_tok & (kOver - 1)) > a.max_tokens) {
             tok = 0;

@@ -378,13 +378,13 @@ typedef struct {
  * A row with a negative length or page count, with more positions than a
  * table row holds, or whose tokens pass max_tokens is not served, keeps its
  * pages and sets the device status to PI_ERR_INVALID_ARG.  The tokens of a
- * row with more positions than a table row holds are counted in cu_new, so
- * that the rows after it find theirs in the packed projections, where all
- * rows' tokens are max_tokens at most; where they are more, and where a length
- * or page count itself is out of range (new_len above what a table row holds
- * among them), the row's tokens are not counted.  cu_new stays within
- * max_tokens.  A free count outside 0 .. num_pages (taken as the nearest
- * bound) and a push past num_pages (dropped) set the same status.
+ * row whose positions leave its table row (cached_len negative, or too many
+ * with the new ones) are counted in cu_new, so that the rows after it find
+ * theirs in the packed projections, where all rows' tokens are max_tokens at
+ * most; where they are more, and where new_len (negative, or above what a table
+ * row holds) or held itself is out of range, the row's tokens are not counted.
+ * cu_new stays within max_tokens.  A free count outside 0 .. num_pages (taken
+ * as the nearest bound) and a push past num_pages (dropped) set the same status.
  */
 PI_API pi_status pi_block_tables(const pi_tables_desc *desc, const int32_t *cached_len, const int32_t *new_len,
                                  const int32_t *held, int32_t *held_out, int32_t *block_table, int32_t *free_list,

@@ -23,6 +23,13 @@ def test_a_row_past_its_table_row_leaves_the_others_in_place(P):
                        slots=[-1, 5 * 16 + 3, 4 * 16 + 3], pos=[64, 3, 3], status=True)
 
 
+def test_a_row_of_negative_length_leaves_the_others_in_place(P):
+    table, stack = [[0, 1, 2, 3], [5, -1, -1, -1], [4, -1, -1, -1]], [6, -1, -1, -1, -1, -1, -1]
+    got = run_tables(P, 16, 4, [-2, 3, 3], [2, 1, 1], [4, 1, 1], table, stack, 1)
+    assert got == dict(held=[4, 1, 1], table=table, stack=stack, count=1, cu=[0, 2, 3, 4], kv=[0, 4, 4],
+                       slots=[-1, -1, 5 * 16 + 3, 4 * 16 + 3], pos=[-2, -1, 3, 3], status=True)
+
+
 @pytest.mark.parametrize("B", [3, 300, 2100, 4096])
 @pytest.mark.parametrize("fits", [True, False])
 def test_rows_past_their_table_rows_at_random(P, B, fits):
