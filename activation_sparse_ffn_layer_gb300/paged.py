@@ -65,17 +65,21 @@ class PagedCache:
     def begin(self, new_len: torch.Tensor, tokens: int, max_new: int, keep: Optional[torch.Tensor] = None):
         """Opens a step in which row b receives new_len[b] tokens (int32, on the
         device), ``tokens`` in all and at most ``max_new`` in a row.  ``keep``: the
-        positions rows keep, where that is fewer than they have (0: the row's
-        request ended, its pages go back).  Rows the pool cannot serve have
-        kv_len 0 afterwards and keep what they had.  All state is updated in
-        place, so a captured step goes on from where the last replay ended."""
+        positions rows keep, at most those they have (0: the row's request
+        ended, its pages go back).  Rows that cannot be served (the pool ran out,
+        the row is full, a negative keep) have kv_len 0 afterwards and hold their
+        pages and the positions they kept; the latter two set the device status.
+        All state is updated in place, so a captured step goes on from where the
+        last replay ended."""
         if tokens > self.max_tokens or max_new > self.max_new:
             raise ValueError("more tokens than the cache was made for")
-        cached = self.cached if keep is None else keep
+        cached = self.cached if keep is None else torch.minimum(keep, self.cached)
         d = B.tables_desc(self.batch, self.pages.page_size, self.pages.num_pages, self.table.shape[1], tokens)
         B.pi_block_tables(d, cached, new_len, self.held, self.held, self.table, self.free, self.free_count,
                           self.free_count, self.cu, self.kv_len, self.slots, self.positions)
-        self.cached.copy_(torch.where(self.kv_len > 0, self.kv_len, cached))
+        if keep is not None:                      # a negative one changes nothing
+            self.cached.copy_(torch.where(cached < 0, self.cached, cached))
+        self.cached.copy_(torch.where(self.kv_len > 0, self.kv_len, self.cached))
         self.tokens, self.desc = tokens, self._desc(tokens, max(1, max_new))
 
     def attend(self, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,

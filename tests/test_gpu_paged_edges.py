@@ -397,3 +397,19 @@ def test_attend_takes_the_tokens_of_its_step(P):
             cache.attend(0, *_qkv(T), torch.empty(3, 4, 64, device="cuda").half())
     cache.attend(0, *_qkv(3), torch.empty(3, 4, 64, device="cuda").half())
     assert P.pi_last_device_status() == 0
+
+
+def test_rows_keep_no_more_than_they_have(P):
+    """keep above what a row has does not make positions visible that were never stored, and one below 0 (reported)
+    leaves the row as it was."""
+    cache = _small()
+    cache.begin(i32([5, 4]), 9, 5)
+    cache.attend(0, *_qkv(9), torch.empty(9, 4, 64, device="cuda").half())
+    cache.begin(i32([1, 1]), 2, 1, i32([40, 3]))
+    cache.attend(0, *_qkv(2), torch.empty(2, 4, 64, device="cuda").half())
+    assert cache.cached.tolist() == [6, 4] and cache.kv_len.tolist() == [6, 4] and P.pi_last_device_status() == 0
+    cache.begin(i32([1, 1]), 2, 1, i32([-3, 4]))
+    assert cache.cu.tolist() == [0, 1, 2] and cache.kv_len.tolist() == [0, 5]
+    assert P.pi_last_device_status() == 1 and cache.cached.tolist()[0] == 6
+    cache.begin(i32([1, 1]), 2, 1)
+    assert cache.cached.tolist()[0] == 7 and cache.kv_len.tolist()[0] == 7 and P.pi_last_device_status() == 0
