@@ -75,6 +75,11 @@ PI_DEV long long block_prefix(long long v, long long* warp_sums, long long* tota
     return __shfl_sync(FULL, w - mine, warp) + s - v;
 }
 
+// The same out of line, for a case that hardly occurs
+__device__ __noinline__ long long block_prefix_again(long long v, long long* warp_sums, long long* total) {
+    return block_prefix(v, warp_sums, total);
+}
+
 // The row b with first[b] <= x < first[b + 1] (first[0] <= x < first[n]).
 template <typename T>
 PI_DEV int row_of(const T* first, int n, T x) {
@@ -142,7 +147,7 @@ __global__ void __launch_bounds__(kTabThreads) k_block_tables(const TablesArgs a
                 if (over[i]) n[i] = 0;
                 tok += n[i];
             }
-            tp = block_prefix(tok, warp_sums, &total_tok);
+            tp = block_prefix_again(tok, warp_sums, &total_tok);
         }
         total_tok &= kOver - 1;
         tp &= kOver - 1;
