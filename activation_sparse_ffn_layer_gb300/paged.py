@@ -80,7 +80,7 @@ class PagedCache:
         if keep is not None:                      # a negative one changes nothing
             self.cached.copy_(torch.where(cached < 0, self.cached, cached))
         self.cached.copy_(torch.where(self.kv_len > 0, self.kv_len, self.cached))
-        self.tokens, self.desc = tokens, self._desc(tokens, max(1, max_new))
+        self.tokens, self.desc = tokens, self._desc(tokens, max(1, min(max_new, tokens)))
 
     def attend(self, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
                lse: Optional[torch.Tensor] = None) -> torch.Tensor:

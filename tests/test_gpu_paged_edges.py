@@ -413,3 +413,15 @@ def test_rows_keep_no_more_than_they_have(P):
     assert P.pi_last_device_status() == 1 and cache.cached.tolist()[0] == 6
     cache.begin(i32([1, 1]), 2, 1)
     assert cache.cached.tolist()[0] == 7 and cache.kv_len.tolist()[0] == 7 and P.pi_last_device_status() == 0
+
+
+def test_a_step_of_fewer_tokens_than_its_largest_chunk(P):
+    """max_new is an upper bound: a loop may pass its chunk size for a step of fewer tokens."""
+    a, b = _small(), _small()
+    x, y = _qkv(3), torch.empty(3, 4, 64, device="cuda").half()
+    a.begin(i32([2, 1]), 3, 20)
+    a.attend(0, *x, y)
+    z = torch.empty_like(y)
+    b.begin(i32([2, 1]), 3, 2)
+    b.attend(0, *x, z)
+    assert torch.equal(y, z) and P.pi_last_device_status() == 0
