@@ -1172,15 +1172,17 @@ PI_DEV bool settle_row(const PagedArgs& a, const PagedShared<DH>& sh, const Bad<
     const T* src = static_cast<const T*>(a.q) + row * a.q_stride + (long long)head * DH + lane * E;
     T* dst = static_cast<T*>(a.out) + row * a.o_stride + (long long)head * DH + lane * E;
     float q[E], o[E];
+    bool nan = false;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
         q[e] = to_f(src[e]);
+        nan |= q[e] != q[e];
         o[e] = 0.f;
     }
     int lo, hi;
     row_sees(a, p, x / a.group, &lo, &hi);
     const bool all = sh.bad_keys <= kBadKeys;
-    bool none = false;   // a score of NaN or +inf: no element is a number
+    bool none = __any_sync(FULL, nan) && lo < hi;   // a score of NaN or +inf: no element is a number
     for (int i = 0; i < min(sh.bad_keys, kBadKeys) && !none; ++i) {
         const uint32_t what = bad.key[i];
         const int key = (int)(what >> 2);

@@ -256,6 +256,24 @@ def test_infinite_keys(P, lens, H, G, many, dt):
     assert bool(torch.isnan(out[~away]).all()) and not bool(torch.isfinite(lse[~away]).any())
 
 
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_queries_that_are_not_finite(P, bad):
+    """They reach their own rows only, and none where the row sees nothing."""
+    q, kc, vc, table, cu, _ = paged_case([(90, 90), (1, 2000), (3, 40)], 8, 2, 64, F16, 16, seed=27)
+    kv = [60, 2000, 40]                       # the first 30 tokens see nothing
+    want, wl, tol, ltol = R.attention(q, kc, vc, table, cu, kv)
+    hit = torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda")
+    hit[10, 3] = hit[50, :] = hit[90, 5] = hit[92, 0] = True
+    q[hit, 7] = bad
+    out, lse = run_attn(P, q, kc, vc, table, cu, kv)
+    hit[10] = False
+    R.check(out[~hit], want[~hit], tol[~hit], "out")
+    R.check(lse[~hit], wl[~hit], ltol[~hit], "lse")
+    assert bool((out[:30] == 0).all()) and bool((lse[:30] == -math.inf).all())
+    assert bool(torch.isnan(out[hit]).all()) and not bool(torch.isfinite(lse[hit]).any())
+    assert P.pi_last_device_status() == 0
+
+
 @pytest.mark.parametrize("a", range(1, 8))
 def test_parts_whose_sums_add_up_past_fp32(P, a):
     """Two keys, 83.5 nats above the rest, in any two of eight key tiles: where their parts are summed under the
