@@ -72,8 +72,9 @@ constexpr int kTileRows = 128;         // rows of a tile at most
 constexpr int kPagedThreads = 384;
 constexpr int kListDepth = 4;          // pieces the work list runs ahead
 constexpr int kConsumers = 11;         // warps that read the work list: all but the one that writes it
-constexpr int kWalk = 16;              // items of a request that are counted one by one, not by formula (a prompt of
-                                       // 1999 tokens: 28.4 us so, 31.3 by formula; the walk grows with the prompt)
+constexpr int kWalk = 64;              // items of a request that are counted one by one, not by formula: one prompt of
+                                       // 16-32 items 22-40 us so, 26-44 by formula (63 items 84.5 and 88.5); of 125 items
+                                       // 61.7 by formula and 73.9 one by one (16 heads of 64), since the walk grows with it
 // What the work split counts, in units of half a microsecond or so: a key tile
 // for one tile of rows (memory), for two (products), an item besides its tiles
 // (kLead before them, the rest after: a border that falls there does not cut the
