@@ -129,6 +129,15 @@ def test_more_tokens_than_positions_under_any_window(P, n, kv, window):
     compare(P, (q, kc, vc, table, cu, [kv, 40]), window=window)
 
 
+@pytest.mark.parametrize("window", [0, 1, 300])
+def test_requests_of_many_items(P, window):
+    """Requests of 69 and more items, counted by formula: behind cached positions, and with fewer positions than tokens."""
+    q, kc, vc, table, cu, kv = paged_case([(1100, 1900), (1, 500), (1300, 1300), (20, 90), (1200, 1200)], 16, 1, 64, F16, 16,
+                                          seed=33, window=window)
+    kv[2], kv[4] = 900, 10
+    compare(P, (q, kc, vc, table, cu, kv), window=window)
+
+
 @pytest.mark.parametrize("B", [385, 1500, 4096])
 def test_thousands_of_small_requests(P, B):
     r = random.Random(B)
