@@ -27,7 +27,7 @@ namespace {
 // not overwritten, free-list entries below the old count are not written).
 //
 // Bound by latency, the chain from lengths over prefixes to table entries and
-// slots: 4.7 us for 8 decoding rows, 10.4 us for 2048 rows with 60 thousand
+// slots: 4.7 us for 8 decoding rows, 10.8 us for 2048 rows with 42 thousand
 // tokens (1.6 MB, 0.24 us of HBM).  Every block scans all rows
 // (three block prefixes) and takes its share of the writes.  Small steps are
 // one block.  Large ones are two grids: kTabMoves, as wide as the writes need,
@@ -537,7 +537,7 @@ pi_status pi_block_tables(const pi_tables_desc* desc, const int32_t* cached_len,
     // block takes 4.3 us and 1.2 more per 1024 tokens, two grids 6.8 us: 5.9
     // against 6.7 at 2048 tokens of 64 rows, 4.9 against 7.0 at 512 decoding
     // rows (6.6 against 7.1 if each gives back 4 pages), 10 against 6.9 at 8192
-    // tokens, 187 against 10.4 at 2048 rows with 60 thousand tokens.
+    // tokens, 187 against 10.4 at 2048 rows with 42 thousand tokens.
     const long long writes = desc->max_tokens + 4ll * desc->batch;
     cudaError_t e;
     if (writes <= 5 * kTabThreads / 2) {

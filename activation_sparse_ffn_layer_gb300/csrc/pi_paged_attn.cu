@@ -32,19 +32,19 @@
 //
 // Bounds and figures (GB300, 64 query and 8 KV heads of 128 unless said):
 //  - few rows per key (decoding): HBM.  Four sequences with 120-131 thousand
-//    keys, bf16: 300 us, 6.9 TB/s.  32 sequences with 500-8000 keys, fp16: 80
+//    keys, bf16: 300-308 us, 6.7-6.9 TB/s.  32 sequences with 500-8000 keys, fp16: 80
 //    us, 5.7 TB/s; DRAM reads are 1.006 of the keys and values, the start and
 //    the joins of cut items are the rest.  One sequence with 1001 keys: 13.3
 //    us of latency, two key tiles per block and a join.
 //  - many rows (a chunk of 4096 tokens behind 12288, bf16): the tensor cores.
-//    1.11-1.20 ms, 1.60-1.73 PFLOP/s.  Two tiles of rows keep them busy for
+//    1.11-1.22 ms, 1.58-1.73 PFLOP/s.  Two tiles of rows keep them busy for
 //    2048 cycles per key tile, which takes 2900: each group's chain of S, the
 //    softmax (1350 for both, 1170 of them for 2 x 128 x 128 exponentials) and
 //    P V is longer than the other's products beside it, and tensor memory has
 //    no room for a second S.  The copies of a tile's eight pages take 600 on
 //    each of two warps.
-//  - prompts of some thousand tokens and mixed steps: 28 us for a prompt of
-//    1999 tokens (12 heads of 64), 119 us for 16 sequences that decode or take
+//  - prompts of some thousand tokens and mixed steps: 29 us for a prompt of
+//    1999 tokens (12 heads of 64), 118 us for 16 sequences that decode or take
 //    100-700 tokens (32 heads, window of 2000).  A block has its SM to itself,
 //    so nothing hides its start, its items' outputs and the joins.
 #include <cuda.h>
@@ -79,8 +79,8 @@ constexpr int kWalk = 64;              // items of a request that are counted on
 // for one tile of rows (memory), for two (products), an item besides its tiles
 // (kLead before them, the rest after: a border that falls there does not cut the
 // item).  Without these weights a mixed step of 16 sequences that decode or take
-// 100-700 tokens took 131 us instead of 119.  Over 18 cases of all kinds the
-// geometric mean is 2 % below that of 6 units all before the tiles, 0.6 % below
+// 100-700 tokens took 131 us instead of 119.  Over 18 cases (four of the listed ones
+// of perf/operators.py and 14 drawn from its ranges) the geometric mean is 2 % below that of 6 units all before the tiles, 0.6 % below
 // 3 + 3 and 5 + 5, 0.7 % above 6 + 6 (32 decoding sequences 83 us instead of
 // 80); pair costs of 3.5 and 4 add 1 or 2 %.
 constexpr int kTileCost = 2, kPairCost = 3, kItemCost = 8, kLead = 4;
@@ -1073,8 +1073,8 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
 // kBadKeys of them, and per column which kinds there are); rows that it leaves
 // open (a value that the row does not see, an overflow) are taken again.  A chunk
 // of 4096 tokens behind 12288 with a NaN at its request's fourth position takes
-// 5.0 ms so and 417 with all rows taken again (1.13 without the NaN); a token
-// behind 131 thousand keys 7.0 ms, 17.4 and 0.33: one block reads its keys again.
+// 5.0 ms so and 209 with all rows taken again (1.13 without the NaN); a token
+// behind 131 thousand keys 7.0 ms, 16.5 and 0.33: one block reads its keys again.
 //
 // Weights carry a factor 2^-kSink, so that the sum of 2^30 of them, each 2^-31 at
 // most, times the largest bf16 value stays in fp32; weights down to 2^-118 of the
