@@ -359,6 +359,10 @@ PI_DEV Piece Walk::next(const PagedArgs& a) {
         const int c = tile_cost(a, toks);
         const long long i0 = u - off;   // the item's first unit
         const int stop = (int)min((long long)(kItemCost + nt * c), u1 - i0);
+        if (stop <= off) {   // the lengths changed under the kernel, off is past the item: stop
+            u = u1;
+            break;
+        }
         const int from = min((max(off - kLead, 0) + c - 1) / c, nt), to = min((max(stop - kLead, 0) + c - 1) / c, nt);
         p.nt = to - from;
         p.j0 = lo / kKeys + from;
@@ -372,9 +376,9 @@ PI_DEV Piece Walk::next(const PagedArgs& a) {
         p.cu = r.cu;
         p.parts = 1;
         p.own = from == 0;
-        if (p.nt != nt) {   // blocks that own its first and its last tile
-            p.block0 = (int)quotient((i0 + kLead + 1) * G - 1, U);
-            p.parts = (int)quotient((i0 + kLead + (nt - 1) * c + 1) * G - 1, U) - p.block0 + 1;
+        if (p.nt != nt) {   // blocks that own its first and its last tile (below G whatever the lengths have become)
+            p.block0 = min((int)quotient((i0 + kLead + 1) * G - 1, U), G - 1);
+            p.parts = min((int)quotient((i0 + kLead + (nt - 1) * c + 1) * G - 1, U), G - 1) - p.block0 + 1;
         }
         u = i0 + stop;
         off = 0;
