@@ -151,13 +151,26 @@ struct Request {
     int cu, n, first;   // first row of q, tokens, position of the first token
 };
 
+// What the work list goes by, as values: behind a function's reference to the
+// kernel's arguments each look is a load from memory, not from the constant bank
+// (31 requests of short and long items 58 us so, 62 by reference).
+struct Lengths {
+    const int32_t *cu, *kv;
+    int batch, kv_heads, max_tokens, max_new, max_pages, page_size, window, group, tile_tokens;
+
+    PI_DEV explicit Lengths(const PagedArgs& a)
+        : cu(a.cu), kv(a.kv), batch(a.batch), kv_heads(a.kv_heads), max_tokens(a.max_tokens), max_new(a.max_new),
+          max_pages(a.max_pages), page_size(a.page_size), window(a.window), group(a.group), tile_tokens(a.tile_tokens) {}
+};
+
 // Where a block's range of units starts, and how far its pieces have been walked.
 struct Walk {
     Request r;
     long long u, u1, U;   // unit reached, the range's end, units in all
     int G, b, g, tok0, off;   // blocks with work; request, KV head, first token and unit within the item at u
 
-    PI_DEV Piece next(const PagedArgs& a);   // nt = 0: none is left
+    template <typename A>
+    PI_DEV Piece next(const A& a);   // nt = 0: none is left
 };
 
 template <int DH>
@@ -175,7 +188,8 @@ struct PagedShared {
     int bad_keys, bad_k;       // keys of a piece with values that are not finite, and whether a key itself has one
 };
 
-PI_DEV Request request(const PagedArgs& a, int b, bool* bad) {
+template <typename A>
+PI_DEV Request request(const A& a, int b, bool* bad) {
     const int lo = a.cu[b], hi = a.cu[b + 1];
     int kv = a.kv[b];
     Request r{lo, hi - lo, 0};
@@ -193,7 +207,8 @@ PI_DEV Request request(const PagedArgs& a, int b, bool* bad) {
 
 // Keys that an item's tokens (from tok0 on) see, as key tiles (one tile, with
 // nothing to see in it, where they see none: it writes the zeros).
-PI_DEV int item_tiles(const PagedArgs& a, const Request& r, int tok0, int* toks, int* lo, int* hi) {
+template <typename A>
+PI_DEV int item_tiles(const A& a, const Request& r, int tok0, int* toks, int* lo, int* hi) {
     *toks = min(2 * a.tile_tokens, r.n - tok0);
     *hi = r.first + tok0 + *toks;
     *lo = a.window > 0 ? max(0, r.first + tok0 - a.window + 1) : 0;
@@ -226,7 +241,8 @@ PI_DEV long long floor_sum(long long n, long long m, long long a, long long b) {
     }
 }
 
-PI_DEV int tile_cost(const PagedArgs& a, int toks) { return toks > a.tile_tokens ? kPairCost : kTileCost; }
+template <typename A>
+PI_DEV int tile_cost(const A& a, int toks) { return toks > a.tile_tokens ? kPairCost : kTileCost; }
 
 // Cost of the first x items of one KV head of a request: kItemCost each, and
 // their tiles (as item_tiles counts them).
@@ -351,7 +367,8 @@ PI_DEV long long quotient(long long a, long long b) {
 // the rest of kItemCost.  A block does the tiles that begin in its range (a range is
 // longer than a tile's cost, so every block between an item's first and last
 // has one).
-PI_DEV Piece Walk::next(const PagedArgs& a) {
+template <typename A>
+PI_DEV Piece Walk::next(const A& a) {
     Piece p{};
     while (u < u1 && p.nt == 0) {   // again where only an item's cost falls into this block
         int toks, lo, hi;
@@ -359,12 +376,8 @@ PI_DEV Piece Walk::next(const PagedArgs& a) {
         const int c = tile_cost(a, toks);
         const long long i0 = u - off;   // the item's first unit
         const int stop = (int)min((long long)(kItemCost + nt * c), u1 - i0);
-        if (stop <= off) {   // the lengths changed under the kernel, off is past the item: stop
-            u = u1;
-            break;
-        }
         const int from = min((max(off - kLead, 0) + c - 1) / c, nt), to = min((max(stop - kLead, 0) + c - 1) / c, nt);
-        p.nt = to - from;
+        p.nt = max(to - from, 0);
         p.j0 = lo / kKeys + from;
         p.lo = lo;
         p.hi = hi;
@@ -376,11 +389,14 @@ PI_DEV Piece Walk::next(const PagedArgs& a) {
         p.cu = r.cu;
         p.parts = 1;
         p.own = from == 0;
-        if (p.nt != nt) {   // blocks that own its first and its last tile (below G whatever the lengths have become)
-            p.block0 = min((int)quotient((i0 + kLead + 1) * G - 1, U), G - 1);
-            p.parts = min((int)quotient((i0 + kLead + (nt - 1) * c + 1) * G - 1, U), G - 1) - p.block0 + 1;
+        // Blocks that own its first and its last tile.  Whatever the lengths become
+        // under the kernel, block0 is this block or one before it; parts may pass the
+        // blocks there are, and then no block finds that many arrivals.
+        if (p.nt != nt) {
+            p.block0 = (int)quotient((i0 + kLead + 1) * G - 1, U);
+            p.parts = (int)quotient((i0 + kLead + (nt - 1) * c + 1) * G - 1, U) - p.block0 + 1;
         }
-        u = i0 + stop;
+        u = stop > off ? i0 + stop : u1;   // (off past the item: the lengths changed under the kernel)
         off = 0;
         tok0 += 2 * a.tile_tokens;
         if (u < u1 && tok0 >= r.n) {
@@ -405,10 +421,10 @@ PI_DEV Piece Walk::next(const PagedArgs& a) {
 // With a piece go its query tiles, once the scores of the piece before are
 // done; tokens past the request's end or the last row come along or read as
 // zeros: a row of S depends on its own query alone.  A function of its own: in
-// line, its registers cost the other roles theirs (4096-token chunk 1.15 ms so,
-// 1.25 in line).
+// line, its registers cost the other roles theirs (4096-token chunk 1.12-1.16 ms so,
+// 1.21-1.26 in line).
 template <int DH>
-__device__ __noinline__ void list_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned char* qs, Walk walk, const Ctl& ctl) {
+__device__ __noinline__ void list_role(Lengths a, const CUtensorMap* qmap, PagedShared<DH>& sh, unsigned char* qs, Walk walk, Ctl ctl) {
     using C = PagedCfg<DH>;
     int n = 0;
     for (;;) {
@@ -423,7 +439,7 @@ __device__ __noinline__ void list_role(const PagedArgs& a, PagedShared<DH>& sh, 
         bar_arrive_expect_tx(&sh.qfull, (unsigned)(tiles * C::HALVES * a.tile_tokens * a.group) * 128u);
         for (int w = 0; w < tiles; ++w)
             for (int h = 0; h < C::HALVES; ++h)
-                tma_load_3d(qs + w * C::QTILE + h * (kTileRows * 128), &a.qmap, 64 * h, p.g * a.group,
+                tma_load_3d(qs + w * C::QTILE + h * (kTileRows * 128), qmap, 64 * h, p.g * a.group,
                             p.cu + p.tok0 + w * a.tile_tokens, &sh.qfull);
         ++n;
     }
@@ -1556,7 +1572,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_paged_attn(const __grid_co
             else if (warp == 10)
                 tile_role<DH, true>(a, sh, vring, ctl);
             else if (lane == 0)
-                list_role<DH>(a, sh, qs, sh.walk, ctl);
+                list_role<DH>(Lengths(a), &a.qmap, sh, qs, sh.walk, ctl);
         }
     }
     tc_before();
