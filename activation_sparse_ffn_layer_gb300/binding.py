@@ -80,6 +80,16 @@ class pi_paged_desc(C.Structure):
         [("scale", C.c_float)]
 
 
+class pi_page8_desc(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("kv_heads", "head_dim", "page_size", "num_pages")] + \
+        [(n, C.c_longlong) for n in ("page_stride", "head_stride", "token_stride")]
+
+
+class pi_read8_desc(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("batch", "max_pages", "max_rows", "dtype")] + \
+        [(n, C.c_longlong) for n in ("k_stride", "v_stride")]
+
+
 class PiError(RuntimeError):
     def __init__(self, fn: str, status: int, msg: str):
         super().__init__(f"{fn}: {msg} (status {status})")
@@ -94,7 +104,7 @@ EXPORTS = ("pi_workspace_bytes", "pi_workspace_layout", "pi_predict", "pi_compac
            "pi_sparse_fc2_noalloc", "pi_stack_plan", "pi_stack_plan_for", "pi_debug_set_wait_timeout",
            "pi_sparse_fc1_tiered", "pi_sparse_fc2_tiered", "pi_ffn_layer_tiered", "pi_attn_workspace_bytes",
            "pi_attn_heads", "pi_block_tables", "pi_rope_plan_init", "pi_rope_store", "pi_paged_workspace_bytes",
-           "pi_paged_attn")
+           "pi_paged_attn", "pi_rope_store8", "pi_page_read8", "pi_paged8_workspace_bytes", "pi_paged_attn8")
 
 
 def library_path() -> str:
@@ -144,6 +154,11 @@ def lib(path: Optional[str] = None):
         "pi_paged_workspace_bytes": (S, [C.POINTER(pi_paged_desc), C.POINTER(pi_page_desc)]),
         "pi_paged_attn": (I, [C.POINTER(pi_paged_desc), C.POINTER(pi_page_desc), P, C.c_longlong, P, P, P, P, P, P,
                               C.c_longlong, P, P, S, P]),
+        "pi_rope_store8": (I, [C.POINTER(pi_rope_plan), C.POINTER(pi_page8_desc), C.POINTER(pi_qkv_desc), I] + [P] * 11),
+        "pi_page_read8": (I, [C.POINTER(pi_read8_desc), C.POINTER(pi_page8_desc)] + [P] * 10),
+        "pi_paged8_workspace_bytes": (S, [C.POINTER(pi_paged_desc), C.POINTER(pi_page8_desc)]),
+        "pi_paged_attn8": (I, [C.POINTER(pi_paged_desc), C.POINTER(pi_page8_desc), I, P, C.c_longlong] + [P] * 8 +
+                           [C.c_longlong, P, P, S, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -539,3 +554,122 @@ def pi_paged_attn(desc, cache, q, kcache, vcache, block_table, cu_new, kv_len, o
         _flat(cu_new, i32, B + 1, "cu_new"), _flat(kv_len, i32, B, "kv_len"), out.data_ptr(), os_,
         None if lse is None else _flat(lse, torch.float32, T * H, "lse"), _flat(workspace, torch.uint8, 0, "workspace"),
         workspace.numel(), _stream()))
+
+
+# ------------------------------------------------------- the paged cache in 8 bits
+
+CODE8 = torch.float8_e4m3fn
+
+
+def page8_desc(kcache: torch.Tensor, vcache: torch.Tensor) -> pi_page8_desc:
+    """The description of two code tensors [pages, kv_heads, page_size, head_dim]
+    (torch.float8_e4m3fn) of one shape and layout; any order of the first three in
+    memory.  Their exponents are int8 tensors [pages, kv_heads, page_size / 16]."""
+    if kcache.dim() != 4 or kcache.shape != vcache.shape or kcache.dtype is not CODE8 or vcache.dtype is not CODE8 or \
+            kcache.stride(3) != 1 or vcache.stride(3) != 1:
+        raise ValueError("expected two [pages, kv_heads, page_size, head_dim] float8_e4m3fn tensors of one shape with "
+                         "contiguous heads")
+    pages, heads, page, dh = kcache.shape
+    # a dimension of one element is never stepped along
+    st = [kcache.stride(i) if n > 1 else dh for i, n in enumerate((pages, heads, page))]
+    if st != [vcache.stride(i) if n > 1 else dh for i, n in enumerate((pages, heads, page))]:
+        raise ValueError("expected key and value codes of the same strides")
+    d = pi_page8_desc(heads, dh, page, pages, st[0], st[1], st[2])
+    d.like = (CODE8, kcache.shape, kcache.stride())   # what _cache8 compares first
+    return d
+
+
+def _cache8(cache: pi_page8_desc, codes: torch.Tensor, exps: torch.Tensor, name: str) -> Tuple[int, int]:
+    """Addresses of the codes and exponents that a page8_desc describes."""
+    if not codes.is_cuda or getattr(cache, "like", None) != (codes.dtype, codes.shape, codes.stride()):
+        if not codes.is_cuda or codes.dtype is not CODE8 or \
+                tuple(codes.shape) != (cache.num_pages, cache.kv_heads, cache.page_size, cache.head_dim) or \
+                (codes.shape[0] > 1 and codes.stride(0) != cache.page_stride) or \
+                (codes.shape[1] > 1 and codes.stride(1) != cache.head_stride) or \
+                codes.stride(2) != cache.token_stride or codes.stride(3) != 1:
+            raise ValueError(f"{name}: not the codes that the page8_desc describes")
+    if exps.dtype is not torch.int8 or not exps.is_cuda or not exps.is_contiguous() or \
+            exps.shape != (cache.num_pages, cache.kv_heads, cache.page_size // 16):
+        raise ValueError(f"{name}: expected contiguous int8 exponents [pages, kv_heads, page_size / 16] on the GPU")
+    return codes.data_ptr(), exps.data_ptr()
+
+
+def pi_rope_store8(plan, cache, q, k, v, positions, slots, q_out, kcache, vcache, kexp, vexp):
+    """Rotates q [T, heads, dh] into q_out (fp16 or bf16) and k [T, kv_heads, dh],
+    and stores k and v as codes at `slots`, raising the exponents of the blocks
+    they join where needed.  q and q_out may be None (store only), or k, v, slots,
+    the caches and the exponents (rotate only)."""
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("expected q or k")
+    dh, dtype, heads, out = cache.head_dim, x.dtype, 1, PI_T_F16
+    qs = ks = vs = os_ = 0
+    qp = op = kp = vp = sp = kc = vc = ke = ve = None
+    if q is not None:
+        heads = q.shape[1]
+        (T, qs), (n, os_) = _rows(q, heads, dh, "q"), _rows(q_out, heads, dh, "q_out")
+        out = _DTYPES.get(q_out.dtype, -1)
+        if n < T:
+            raise ValueError("q_out: expected the shape of q")
+        qp, op = q.data_ptr(), q_out.data_ptr()
+    if k is not None:
+        (n, ks), (m, vs) = _rows(k, cache.kv_heads, dh, "k"), _rows(v, cache.kv_heads, dh, "v")
+        if q is None:
+            T = n
+        if n != T or m != T or k.dtype is not dtype or v.dtype is not dtype:
+            raise ValueError("k, v: expected the tokens and the type of q")
+        kp, vp, sp = k.data_ptr(), v.data_ptr(), _flat(slots, torch.int64, T, "slots")
+        (kc, ke), (vc, ve) = _cache8(cache, kcache, kexp, "kcache"), _cache8(cache, vcache, vexp, "vcache")
+    d = pi_qkv_desc(T, heads, _DTYPES.get(dtype, -1), qs, ks, vs, os_)
+    _check("pi_rope_store8", lib().pi_rope_store8(C.byref(plan), C.byref(cache), C.byref(d), out, qp, kp, vp,
+                                                  _flat(positions, torch.int32, T, "positions"), sp, op, kc, vc, ke, ve,
+                                                  _stream()))
+
+
+def read8_desc(batch: int, max_pages: int, max_rows: int) -> pi_read8_desc:
+    return pi_read8_desc(batch, max_pages, max_rows)
+
+
+def pi_page_read8(desc, cache, kcache, vcache, kexp, vexp, block_table, start, cu_rows, k_out, v_out):
+    """Positions start[b] .. (start None: from 0) of request b as rows cu_rows[b] ..
+    cu_rows[b + 1] - 1 of k_out and v_out [max_rows, kv_heads, dh] (fp16, bf16 or
+    fp32).  k_out or v_out may be None, with its codes and exponents."""
+    B, i32 = desc.batch, torch.int32
+    x = k_out if k_out is not None else v_out
+    if x is None:
+        raise ValueError("expected k_out or v_out")
+    at, strides = [], []
+    for codes, exps, out, name in ((kcache, kexp, k_out, "k"), (vcache, vexp, v_out, "v")):
+        if out is None:
+            at.append((None, None, None))
+            strides.append(0)
+            continue
+        n, stride = _rows(out, cache.kv_heads, cache.head_dim, name + "_out")
+        if n < desc.max_rows or out.dtype is not x.dtype:
+            raise ValueError(f"{name}_out: expected max_rows rows, of one type")
+        at.append((*_cache8(cache, codes, exps, name + "cache"), out.data_ptr()))
+        strides.append(stride)
+    (kc, ke, ko), (vc, ve, vo) = at
+    d = pi_read8_desc(B, desc.max_pages, desc.max_rows, _DTYPES.get(x.dtype, -1), *strides)
+    _check("pi_page_read8", lib().pi_page_read8(
+        C.byref(d), C.byref(cache), kc, vc, ke, ve, _table(block_table, B, desc.max_pages),
+        None if start is None else _flat(start, i32, B, "start"), _flat(cu_rows, i32, B + 1, "cu_rows"), ko, vo, _stream()))
+
+
+def pi_paged8_workspace_bytes(desc: pi_paged_desc, cache: pi_page8_desc) -> int:
+    return int(lib().pi_paged8_workspace_bytes(C.byref(desc), C.byref(cache)))
+
+
+def pi_paged_attn8(desc, cache, q, kcache, vcache, kexp, vexp, block_table, cu_new, kv_len, out, lse, workspace):
+    """pi_paged_attn over an 8-bit cache: q and out [max_tokens, heads, dh] in fp16
+    or bf16; workspace uint8, zero-filled before its first use."""
+    T, H, B, i32 = desc.max_tokens, desc.heads, desc.batch, torch.int32
+    (n, qs), (m, os_) = _rows(q, H, cache.head_dim, "q"), _rows(out, H, cache.head_dim, "out")
+    if n < T or m < T or out.dtype is not q.dtype:
+        raise ValueError("q, out: expected max_tokens rows of one type")
+    (kc, ke), (vc, ve) = _cache8(cache, kcache, kexp, "kcache"), _cache8(cache, vcache, vexp, "vcache")
+    _check("pi_paged_attn8", lib().pi_paged_attn8(
+        C.byref(desc), C.byref(cache), _DTYPES.get(q.dtype, -1), q.data_ptr(), qs, kc, vc, ke, ve,
+        _table(block_table, B, desc.max_pages), _flat(cu_new, i32, B + 1, "cu_new"), _flat(kv_len, i32, B, "kv_len"),
+        out.data_ptr(), os_, None if lse is None else _flat(lse, torch.float32, T * H, "lse"),
+        _flat(workspace, torch.uint8, 0, "workspace"), workspace.numel(), _stream()))

@@ -6,6 +6,9 @@ A step is ``begin`` (page accounting, block tables, slots and positions from the
 request lengths: ``pi_block_tables``), then per layer ``attend`` (rotary positions
 and the store into the cache: ``pi_rope_store``; attention over the cache:
 ``pi_paged_attn``).  No step synchronises the host; all lengths stay on the device.
+With ``bits=8`` the caches hold e4m3 codes with an exponent for each block of 16
+positions and head (``pi_rope_store8``, ``pi_paged_attn8``), and ``read`` gives rows of
+them back (``pi_page_read8``).
 
     python -m activation_sparse_ffn_layer_gb300.paged --config c4 --requests 16 --prompt 1000 --tokens 64
 
@@ -28,21 +31,32 @@ class PagedCache:
 
     ``num_pages`` pages of ``page_size`` positions serve all rows; a row holds at
     most ``max_seq`` positions and receives at most ``max_new`` tokens a step, the
-    rows together at most ``max_tokens``."""
+    rows together at most ``max_tokens``.  ``dtype`` is the type of queries and outputs,
+    and of the caches where ``bits`` is 16; with 8 they hold codes."""
 
     def __init__(self, heads: int, kv_heads: int, head_dim: int, batch: int, max_seq: int, max_new: int,
                  max_tokens: int, layers: int = 1, page_size: int = 16, num_pages: Optional[int] = None,
                  dtype: torch.dtype = torch.float16, rope: Optional[B.pi_rope_plan] = None, window: int = 0,
-                 device="cuda"):
+                 device="cuda", bits: int = 16):
+        if bits not in (8, 16):
+            raise ValueError("bits: expected 8 or 16")
         per_row = -(-max_seq // page_size)
         pages = batch * per_row if num_pages is None else num_pages
         self.batch, self.heads, self.kv_heads, self.head_dim = batch, heads, kv_heads, head_dim
         self.max_new, self.max_tokens, self.window = max_new, max_tokens, window
         self.rope = B.rope_plan(head_dim, 0) if rope is None else rope
         shape = (pages, kv_heads, page_size, head_dim)
-        self.kcache = [torch.zeros(shape, dtype=dtype, device=device) for _ in range(layers)]
-        self.vcache = [torch.zeros(shape, dtype=dtype, device=device) for _ in range(layers)]
-        self.pages = B.page_desc(self.kcache[0], self.vcache[0])
+        self.bits = bits
+        held = dict(dtype=dtype if bits == 16 else B.CODE8, device=device)
+        self.kcache = [torch.zeros(shape, **held) for _ in range(layers)]
+        self.vcache = [torch.zeros(shape, **held) for _ in range(layers)]
+        if bits == 16:
+            self.pages = B.page_desc(self.kcache[0], self.vcache[0])
+        else:
+            exps = dict(size=(pages, kv_heads, page_size // 16), dtype=torch.int8, device=device)
+            self.kexp = [torch.zeros(**exps) for _ in range(layers)]
+            self.vexp = [torch.zeros(**exps) for _ in range(layers)]
+            self.pages = B.page8_desc(self.kcache[0], self.vcache[0])
         i32 = dict(dtype=torch.int32, device=device)
         self.table = torch.full((batch, per_row), -1, **i32)
         self.free = torch.arange(pages - 1, -1, -1, **i32)      # lowest page on top
@@ -54,7 +68,8 @@ class PagedCache:
         self.q = torch.empty(max_tokens, heads, head_dim, dtype=dtype, device=device)
         self.tokens = 0
         # sized for the largest step: the partials depend on max_new alone
-        need = B.pi_paged_workspace_bytes(self._desc(max_tokens, max_new), self.pages)
+        size = B.pi_paged_workspace_bytes if bits == 16 else B.pi_paged8_workspace_bytes
+        need = size(self._desc(max_tokens, max_new), self.pages)
         if need == 0:
             raise ValueError("heads, cache shape or capacities rejected by the library")
         self.workspace = torch.zeros(need, dtype=torch.uint8, device=device)
@@ -91,9 +106,29 @@ class PagedCache:
         if q.shape[0] != self.tokens:
             raise ValueError(f"expected the {self.tokens} tokens of the step")
         kc, vc, turned = self.kcache[layer], self.vcache[layer], self.q[:self.tokens]
+        if self.bits == 8:
+            ke, ve = self.kexp[layer], self.vexp[layer]
+            B.pi_rope_store8(self.rope, self.pages, q, k, v, self.positions, self.slots, turned, kc, vc, ke, ve)
+            B.pi_paged_attn8(self.desc, self.pages, turned, kc, vc, ke, ve, self.table, self.cu, self.kv_len, out, lse,
+                             self.workspace)
+            return out
         B.pi_rope_store(self.rope, self.pages, q, k, v, self.positions, self.slots, turned, kc, vc)
         B.pi_paged_attn(self.desc, self.pages, turned, kc, vc, self.table, self.cu, self.kv_len, out, lse, self.workspace)
         return out
+
+    def read(self, layer: int, start: Optional[torch.Tensor], cu_rows: torch.Tensor, rows: int,
+             dtype: Optional[torch.dtype] = None):
+        """Keys and values of one layer of an 8-bit cache as rows [rows, kv_heads, head_dim]
+        (``dtype``: that of the queries unless given): request b's positions start[b] .. (None:
+        from 0) are rows cu_rows[b] .. cu_rows[b + 1] - 1, for a request that goes elsewhere."""
+        if self.bits != 8:
+            raise ValueError("read: expected a cache of 8 bits")
+        k = torch.zeros(rows, self.kv_heads, self.head_dim, dtype=dtype or self.q.dtype, device=self.q.device)
+        v = torch.zeros_like(k)
+        d = B.read8_desc(self.batch, self.table.shape[1], rows)
+        B.pi_page_read8(d, self.pages, self.kcache[layer], self.vcache[layer], self.kexp[layer], self.vexp[layer],
+                        self.table, start, cu_rows, k, v)
+        return k, v
 
 
 def main(argv=None) -> None:
@@ -107,6 +142,7 @@ def main(argv=None) -> None:
     ap.add_argument("--layers", type=int, default=4)
     ap.add_argument("--page", type=int, default=16)
     ap.add_argument("--window", type=int, default=0)
+    ap.add_argument("--bits", type=int, default=16, choices=(8, 16), help="of the cached keys and values")
     a = ap.parse_args(argv)
     c = ATTN_CONFIGS[a.config]
     H, G, dh, n = c.heads, c.kv_heads, c.head_dim, a.requests
@@ -118,7 +154,7 @@ def main(argv=None) -> None:
 
     def serve():
         cache = PagedCache(H, G, dh, n, a.prompt + a.tokens, a.chunk, a.chunk * n, layers=a.layers, page_size=a.page,
-                           rope=B.rope_plan(dh), window=a.window)
+                           rope=B.rope_plan(dh), window=a.window, bits=a.bits)
 
         def step(new):
             T = sum(new)

@@ -511,6 +511,102 @@ PI_API pi_status pi_paged_attn(const pi_paged_desc *desc, const pi_page_desc *ca
                                const int32_t *block_table, const int32_t *cu_new, const int32_t *kv_len, void *out,
                                long long out_stride, float *lse, void *workspace, size_t ws_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The paged cache in 8 bits.  Keys and values are held as e4m3 codes (one
+ * byte: sign, 4 bits of exponent, 3 of fraction; no infinities), and each
+ * block of 16 positions and each KV head has an exponent e for its keys and
+ * one for its values: a code c stands for c 2^e.  A cache takes half the
+ * bytes of a 16-bit one (and 1 / 128 more for heads of 128, 1 / 64 for 64: an
+ * int8 exponent for 16 head_dim codes).  Block tables, slots and positions are
+ * those of pi_block_tables.
+ *
+ * Element (page, head, position, i) of a code array is the byte at page *
+ * page_stride + head * head_stride + position * token_stride + i, so both
+ * [pages, heads, page_size, head_dim] and [pages, page_size, heads, head_dim]
+ * are described.  Strides are at least head_dim and multiples of 16; base
+ * pointers 16-byte aligned.  The exponents are int8 [num_pages, kv_heads,
+ * page_size / 16], kept apart for keys and for values, in the range -32 .. 32
+ * (others are taken as the nearest).
+ * ---------------------------------------------------------------------- */
+typedef struct {
+    int kv_heads;   /* 1 .. 1024                       */
+    int head_dim;   /* 64 or 128                       */
+    int page_size;  /* 16, 32, 64 or 128               */
+    int num_pages;  /* 1 .. 2^26                       */
+    long long page_stride, head_stride, token_stride;   /* bytes */
+} pi_page8_desc;
+
+/*
+ * Rotary positions and the store into an 8-bit cache: pi_rope_store with the
+ * rotated keys and the values quantised as they are written.  The new tokens
+ * of a block and head have the largest finite magnitude A; its exponent is the
+ * smallest e in -32 .. 32 with A <= 448 2^e, and no smaller than the block's
+ * present one where the block keeps earlier positions (the new tokens' first
+ * place in the block is not 0).  Where that raises it, the codes of those
+ * earlier positions are rounded again under the new exponent.  A code is x /
+ * 2^e rounded to nearest even, x in fp32 (magnitudes above 448 2^32 are held as
+ * that); an infinity or NaN is stored as NaN.  What a block holds behind the
+ * new tokens is given up.
+ *   The new tokens of a block are consecutive rows at consecutive slots, as
+ * pi_block_tables lists them: a row whose slot does not follow the row
+ * before's begins a block's new tokens, and a block has one such row in a call
+ * (of several, the block's contents are undefined).  Slots are as for
+ * pi_rope_store: -1 is not stored; below that or past the cache is not stored
+ * and sets the device status to PI_ERR_INVALID_ARG.
+ *   out_dtype is the type of q_out, PI_T_F16 or PI_T_BF16.  q_out may be q where
+ * types and strides agree, and shares no other memory with q, k or v.  q and
+ * q_out may both be NULL (store only), or k, v, slots, caches and exponents
+ * (rotate only).  All but the exponents 16-byte aligned.
+ */
+PI_API pi_status pi_rope_store8(const pi_rope_plan *plan, const pi_page8_desc *cache, const pi_qkv_desc *desc,
+                                int out_dtype, const void *q, const void *k, const void *v,
+                                const int32_t *positions, const int64_t *slots, void *q_out, void *kcache,
+                                void *vcache, int8_t *kexp, int8_t *vexp, void *stream);
+
+/* Rows that are read back from an 8-bit cache. */
+typedef struct {
+    int batch;      /* requests (1 .. 4096)                                      */
+    int max_pages;  /* entries per block-table row (max_pages * page_size <= 2^30) */
+    int max_rows;   /* rows of the outputs (0 .. 2^30)                            */
+    int dtype;      /* of the outputs: PI_T_F16, PI_T_BF16 or PI_T_F32            */
+    long long k_stride, v_stride;   /* elements from row to row, multiples of 8, at least kv_heads * head_dim */
+} pi_read8_desc;
+
+/*
+ * Keys and values of requests as rows of 16 or 32 bits.  Row cu_rows[b] + i of
+ * k_out and v_out becomes position start[b] + i of request b (start NULL: 0) for
+ * all KV heads [kv_heads, head_dim]: c 2^e rounded to the type (fp16 values that
+ * would round past 65504 are 65504).  Rows past cu_rows[batch] are left alone.
+ * A position outside 0 .. max_pages * page_size - 1 or a page id outside the
+ * cache reads as zeros, and an inconsistent request (cu_rows decreasing,
+ * negative or past max_rows) is not read; each sets the device status to
+ * PI_ERR_INVALID_ARG.  k_out or v_out may be NULL (with its codes and exponents).
+ */
+PI_API pi_status pi_page_read8(const pi_read8_desc *desc, const pi_page8_desc *cache, const void *kcache,
+                               const void *vcache, const int8_t *kexp, const int8_t *vexp,
+                               const int32_t *block_table, const int32_t *start, const int32_t *cu_rows,
+                               void *k_out, void *v_out, void *stream);
+
+/* Bytes of workspace pi_paged_attn8 needs (0 if a descriptor is invalid). */
+PI_API size_t pi_paged8_workspace_bytes(const pi_paged_desc *desc, const pi_page8_desc *cache);
+
+/*
+ * pi_paged_attn over an 8-bit cache: the same outputs from keys and values
+ * c 2^e.  q and out are of type `dtype`, PI_T_F16 or PI_T_BF16.  Rows of
+ * requests without tokens, rows past cu_new[batch], inconsistent rows and page
+ * ids are as for pi_paged_attn; a NaN in the cache reaches the tokens that see
+ * it and no others.  The result does not depend on timing (bitwise
+ * reproducible on one device).
+ * workspace: pi_paged8_workspace_bytes, 16-byte aligned, zero-filled before its
+ * first use (and again after a PI_ERR_TIMEOUT); one workspace serves any number
+ * of layers whose calls are stream-ordered.
+ */
+PI_API pi_status pi_paged_attn8(const pi_paged_desc *desc, const pi_page8_desc *cache, int dtype, const void *q,
+                                long long q_stride, const void *kcache, const void *vcache, const int8_t *kexp,
+                                const int8_t *vexp, const int32_t *block_table, const int32_t *cu_new,
+                                const int32_t *kv_len, void *out, long long out_stride, float *lse,
+                                void *workspace, size_t ws_bytes, void *stream);
+
 /* How one pi_ffn_stack step of `desc` (n_layers layers with the given ranks,
  * NULL: all desc->rank) is executed on the current device.  Diagnostics: lets a
  * caller or a test see which streaming mode the batch-1 persistent kernel
