@@ -124,6 +124,7 @@ struct PagedArgs {
     int tile_tokens;          // tokens of a tile, 128 / group
     int head_blocks;          // head stride in blocks of 64 elements
     int part_rows;            // rows of a partial
+    int few;                  // requests of this many tokens or fewer are left alone
     float scale;
     int* counters;            // [blocks][8] arrivals at a cut item
     float* part_ml;           // [blocks][2][2][part_rows][2]
@@ -156,11 +157,12 @@ struct Request {
 // (31 requests of short and long items 58 us so, 62 by reference).
 struct Lengths {
     const int32_t *cu, *kv;
-    int batch, kv_heads, max_tokens, max_new, max_pages, page_size, window, group, tile_tokens;
+    int batch, kv_heads, max_tokens, max_new, max_pages, page_size, window, group, tile_tokens, few;
 
     PI_DEV explicit Lengths(const PagedArgs& a)
         : cu(a.cu), kv(a.kv), batch(a.batch), kv_heads(a.kv_heads), max_tokens(a.max_tokens), max_new(a.max_new),
-          max_pages(a.max_pages), page_size(a.page_size), window(a.window), group(a.group), tile_tokens(a.tile_tokens) {}
+          max_pages(a.max_pages), page_size(a.page_size), window(a.window), group(a.group), tile_tokens(a.tile_tokens),
+          few(a.few) {}
 };
 
 // Where a block's range of units starts, and how far its pieces have been walked.
@@ -201,6 +203,7 @@ PI_DEV Request request(const A& a, int b, bool* bad) {
         *bad = true;
         kv = 0;
     }
+    if (r.n <= a.few) r.n = 0;
     r.first = kv - r.n;
     return r;
 }
@@ -1662,22 +1665,11 @@ cudaError_t launch_paged(const PagedArgs& a, int blocks, cudaStream_t s) {
 }
 
 }  // namespace
-}  // namespace pi
 
-using namespace pi;
-
-extern "C" {
-
-size_t pi_paged_workspace_bytes(const pi_paged_desc* desc, const pi_page_desc* cache) {
-    if (!desc || !cache || !paged_ok(*desc, *cache)) return 0;
-    // without a device (descriptors checked on a host), as for one SM
-    return PagedLayout(*desc, *cache, std::max(1, paged_blocks())).total;
-}
-
-pi_status pi_paged_attn(const pi_paged_desc* desc, const pi_page_desc* cache, const void* q, long long q_stride,
-                        const void* kcache, const void* vcache, const int32_t* block_table, const int32_t* cu_new,
-                        const int32_t* kv_len, void* out, long long out_stride, float* lse, void* workspace,
-                        size_t ws_bytes, void* stream) {
+pi_status paged_attn(const pi_paged_desc* desc, const pi_page_desc* cache, const void* q, long long q_stride,
+                     const void* kcache, const void* vcache, const int32_t* block_table, const int32_t* cu_new,
+                     const int32_t* kv_len, void* out, long long out_stride, float* lse, void* workspace,
+                     size_t ws_bytes, int few, void* stream) {
     if (!desc || !cache || !paged_ok(*desc, *cache)) return PI_ERR_INVALID_ARG;
     const long long width = (long long)desc->heads * cache->head_dim;
     if (q_stride % 8 != 0 || q_stride < width || out_stride % 8 != 0 || out_stride < width) return PI_ERR_INVALID_ARG;
@@ -1721,6 +1713,7 @@ pi_status pi_paged_attn(const pi_paged_desc* desc, const pi_page_desc* cache, co
     a.tile_tokens = kTileRows / a.group;
     a.head_blocks = (int)(cache->head_stride / 64);
     a.part_rows = lay.rows;
+    a.few = few;
     a.scale = desc->scale > 0.f ? desc->scale : 1.0f / sqrtf((float)cache->head_dim);
     a.counters = reinterpret_cast<int*>(ws);
     a.part_ml = reinterpret_cast<float*>(ws + lay.ml);
@@ -1738,6 +1731,26 @@ pi_status pi_paged_attn(const pi_paged_desc* desc, const pi_page_desc* cache, co
         e = cache->head_dim == 128 ? launch_paged<__nv_bfloat16, 128>(a, blocks, s)
                                    : launch_paged<__nv_bfloat16, 64>(a, blocks, s);
     return e == cudaSuccess ? PI_OK : PI_ERR_CUDA;
+}
+
+}  // namespace pi
+
+using namespace pi;
+
+extern "C" {
+
+size_t pi_paged_workspace_bytes(const pi_paged_desc* desc, const pi_page_desc* cache) {
+    if (!desc || !cache || !paged_ok(*desc, *cache)) return 0;
+    // without a device (descriptors checked on a host), as for one SM
+    return PagedLayout(*desc, *cache, std::max(1, paged_blocks())).total;
+}
+
+pi_status pi_paged_attn(const pi_paged_desc* desc, const pi_page_desc* cache, const void* q, long long q_stride,
+                        const void* kcache, const void* vcache, const int32_t* block_table, const int32_t* cu_new,
+                        const int32_t* kv_len, void* out, long long out_stride, float* lse, void* workspace,
+                        size_t ws_bytes, void* stream) {
+    return paged_attn(desc, cache, q, q_stride, kcache, vcache, block_table, cu_new, kv_len, out, out_stride, lse, workspace,
+                      ws_bytes, 0, stream);
 }
 
 }  // extern "C"
