@@ -8,7 +8,7 @@
 //
 // k_attn8_few: an item is up to 16 rows of one request and KV head (row = token *
 // group + head in the group).  A warp takes 16 keys at a time, one block of the
-// cache, straight from global memory into registers, two steps ahead:
+// cache, through a ring of its own in shared memory, three steps ahead:
 //     S = Q K^T           (codes as fp16, which holds them exactly; fp32 sums)
 //     x = c 2^ek S        (c = scale / ln 2; ek the exponent of the keys' block)
 //     P = 2^(x + ev - m)  (ev the exponent of the values' block)
@@ -32,6 +32,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <mutex>
 
 #include "pi_common.cuh"
 #include "pi_e4m3.cuh"
@@ -48,6 +49,7 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kTile = 16 * kWarps;   // keys of a unit of the work split
 constexpr int kLead = 2;             // units that an item counts besides its tiles
 constexpr int kMinUnits = 2;         // units of a block at least
+constexpr int kMostBlocks = 3;       // of an SM
 constexpr float kLift = 7.f;         // log2 of the factor that P, l and O share
 constexpr float kGrow = 8.f;         // growth (log2) of a maximum before m follows
 constexpr float kLn2 = 0.69314718055994531f;
@@ -223,71 +225,54 @@ PI_DEV uint32_t query2(uint32_t w, float f, __nv_bfloat16) {
 }
 PI_DEV uint32_t query2(uint32_t w, float, __half) { return w; }
 
-// The codes of 16 keys in registers.  Keys: keys 8 j + lane / 4, elements 16 q .. and
-// 64 + 16 q .. (q = lane % 4).  Values: keys 2 q, 2 q + 1, 2 q + 8, 2 q + 9, elements
-// (dh / 8) (lane / 4) ...
+// The codes of 16 keys, as a lane uses them.  Keys: keys 8 j + lane / 4, elements 16 q ..
+// and 64 + 16 q .. (q = lane % 4).  Values: keys 2 q, 2 q + 1, 2 q + 8, 2 q + 9, elements
+// (dh / 8) (lane / 4) ...  A lane copies what it uses itself, so a ring's slot is ordered
+// by lane and nothing but the lane's own wait is needed before it is read.
 template <int DH>
-struct Step8 {
+struct Slot8 {
     static constexpr int KC = DH / 64, VW = DH / 32;   // 16-byte chunks of a key, words of a value
-    uint4 k[2][KC];
-    uint32_t v[4][VW];
-    int ek, ev;
+    uint4 k[2 * KC][32];
+    uint32_t v[4][32][VW];
 };
 
-PI_DEV uint4 ld16(const uint8_t* p) { return ld_stream16(p); }
+template <int BYTES>
+PI_DEV void copy_async(void* to, const void* from, bool there) {   // zeros where not there
+    const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
+    const int n = there ? BYTES : 0;
+    if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from), "r"(n) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(at), "l"(from), "r"(n) : "memory");
+}
+PI_DEV void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+PI_DEV void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+// Asks for the codes of keys kb .. kb + 15 (page `id`, negative: zeros).
 template <int DH>
-PI_DEV void load_keys(const Few8Args& a, Step8<DH>& s, int id, int kb, int g) {
-    const int lane = threadIdx.x & 31, in_page = kb & ((1 << a.c.page_shift) - 1);
-    s.ek = 0;
-    if (id < 0) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int c = 0; c < Step8<DH>::KC; ++c) s.k[j][c] = make_uint4(0u, 0u, 0u, 0u);
-        return;
-    }
-    const uint8_t* const at = a.c.k + id * a.c.page_stride + g * a.c.head_stride + (in_page + (lane >> 2)) * a.c.token_stride + (lane & 3) * 16;
+PI_DEV void fetch(const Few8Args& a, Slot8<DH>& to, int id, int kb, int g) {
+    const int lane = threadIdx.x & 31, q4 = lane & 3, r8 = lane >> 2;
+    const bool there = id >= 0;
+    const long long at = there ? id * a.c.page_stride + g * a.c.head_stride + (kb & ((1 << a.c.page_shift) - 1)) * a.c.token_stride : 0;
+    const uint8_t* const k = a.c.k + at + r8 * a.c.token_stride + q4 * 16;
+    const uint8_t* const v = a.c.v + at + 2 * q4 * a.c.token_stride + r8 * (DH / 8);
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int c = 0; c < Step8<DH>::KC; ++c) s.k[j][c] = ld16(at + 8 * j * a.c.token_stride + 64 * c);
-    s.ek = a.c.ke[(((long long)id * a.c.kv_heads + g) << (a.c.page_shift - 4)) + in_page / kBlock];
+        for (int c = 0; c < Slot8<DH>::KC; ++c)
+            copy_async<16>(&to.k[j * Slot8<DH>::KC + c][lane], k + 8 * j * a.c.token_stride + 64 * c, there);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) copy_async<DH / 8>(to.v[x][lane], v + ((x & 1) + 8 * (x >> 1)) * a.c.token_stride, there);
 }
-template <int DH>
-PI_DEV void load_values(const Few8Args& a, Step8<DH>& s, int id, int kb, int g) {
-    const int lane = threadIdx.x & 31, in_page = kb & ((1 << a.c.page_shift) - 1);
-    s.ev = 0;
-    if (id < 0) {
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-#pragma unroll
-            for (int i = 0; i < Step8<DH>::VW; ++i) s.v[x][i] = 0u;
-        return;
-    }
-    const uint8_t* const at = a.c.v + id * a.c.page_stride + g * a.c.head_stride + (in_page + 2 * (lane & 3)) * a.c.token_stride + (lane >> 2) * (DH / 8);
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-        const uint8_t* const p = at + ((x & 1) + 8 * (x >> 1)) * a.c.token_stride;
-        if (DH == 128) {
-            const uint4 y = ld16(p);
-            s.v[x][0] = y.x;
-            s.v[x][1] = y.y;
-            s.v[x][DH / 32 - 2] = y.z;
-            s.v[x][DH / 32 - 1] = y.w;
-        } else {
-            const uint2 y = ld_stream8(p);
-            s.v[x][0] = y.x;
-            s.v[x][1] = y.y;
-        }
-    }
-    s.ev = a.c.ve[(((long long)id * a.c.kv_heads + g) << (a.c.page_shift - 4)) + in_page / kBlock];
-}
+
+constexpr int kStages = 4;           // slots of a warp's ring
 
 template <int DH>
 struct Few8Shared {
     static constexpr int CHUNKS = DH / 8;     // float4 of a thread's part of O
-    float4 o[kWarps][CHUNKS][32];
+    union {
+        Slot8<DH> ring[kWarps][kStages];
+        float4 o[kWarps][CHUNKS][32];         // a piece's sums, once its rings are empty
+    };
     float ml[kWarps][kRows][2];
     long long scratch[kWarps + 1];
     Walk8 walk;
@@ -302,12 +287,12 @@ struct Rows8 {
     float m[2], l[2];
 };
 
-// One step of 16 keys from kb on.
+// One step of 16 keys from kb on, whose blocks have exponents ek and ev.
 // HALF: rows 8 .. 15 hold nothing.
-template <int DH, bool HALF, typename Next>
-PI_DEV void step(const Piece8& p, Step8<DH>& s, int kb, bool edge, const uint32_t (&q)[DH / 16][4], Rows8& w,
-                 float (&o)[DH / 8][4], Next&& keys_read) {
-    constexpr int KC = Step8<DH>::KC, VW = Step8<DH>::VW, RH = HALF ? 1 : 2;
+template <int DH, bool HALF>
+PI_DEV void step(const Piece8& p, const Slot8<DH>& s, int ek, int ev, int kb, bool edge, const uint32_t (&q)[DH / 16][4],
+                 Rows8& w, float (&o)[DH / 8][4]) {
+    constexpr int KC = Slot8<DH>::KC, VW = Slot8<DH>::VW, RH = HALF ? 1 : 2;
     const int lane = threadIdx.x & 31, q4 = lane & 3;
     float acc[2][2][4];   // two chains for each 8 keys
 #pragma unroll
@@ -322,12 +307,25 @@ PI_DEV void step(const Piece8& p, Step8<DH>& s, int kb, bool edge, const uint32_
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const uint4 y = s.k[j][c];
+                const uint4 y = s.k[j * KC + c][lane];
                 const uint32_t word = i == 0 ? y.x : i == 1 ? y.y : i == 2 ? y.z : y.w;
                 mma16816(acc[j][i & 1], q[4 * c + i], widen2(word & 0xffffu), widen2(word >> 16));
             }
-    const int ek = bounded(s.ek), ev = bounded(s.ev);
-    keys_read();
+    uint32_t v[4][VW];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        if (DH == 128) {
+            const uint4 y = *reinterpret_cast<const uint4*>(s.v[x][lane]);
+            v[x][0] = y.x;
+            v[x][1] = y.y;
+            v[x][VW - 2] = y.z;
+            v[x][VW - 1] = y.w;
+        } else {
+            const uint2 y = *reinterpret_cast<const uint2*>(s.v[x][lane]);
+            v[x][0] = y.x;
+            v[x][1] = y.y;
+        }
+    }
     // x = c 2^ek S of this lane's keys kb + 8 j + 2 q + e
     float x[2][4];
     const float fk = pow2(ek), fev = (float)ev;
@@ -358,7 +356,7 @@ PI_DEV void step(const Piece8& p, Step8<DH>& s, int kb, bool edge, const uint32_
             const int key = kb + 8 * (y >> 1) + 2 * q4 + (y & 1);
             if (key < p.lo || key >= p.hi)
 #pragma unroll
-                for (int i = 0; i < VW; ++i) s.v[y][i] = 0u;
+                for (int i = 0; i < VW; ++i) v[y][i] = 0u;
         }
     }
     // m, where it has to move
@@ -405,7 +403,7 @@ PI_DEV void step(const Piece8& p, Step8<DH>& s, int kb, bool edge, const uint32_
 #pragma unroll
         for (int y = 0; y < 4; ++y)
 #pragma unroll
-            for (int i = 0; i < VW; ++i) nan |= (((s.v[y][i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
+            for (int i = 0; i < VW; ++i) nan |= (((v[y][i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
         if (__any_sync(FULL, nan)) {
             uint32_t seen[4];   // 1 where the row sees the key
 #pragma unroll
@@ -418,8 +416,8 @@ PI_DEV void step(const Piece8& p, Step8<DH>& s, int kb, bool edge, const uint32_
                 uint32_t one[4];
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
-                    const uint32_t is = (((s.v[y][i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
-                    s.v[y][i] &= ~(is * 255u);
+                    const uint32_t is = (((v[y][i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
+                    v[y][i] &= ~(is * 255u);
                     one[y] = is * 0x38u;   // the code of 1
                 }
 #pragma unroll
@@ -438,8 +436,8 @@ PI_DEV void step(const Piece8& p, Step8<DH>& s, int kb, bool edge, const uint32_
 #pragma unroll
     for (int i = 0; i < VW; ++i) {
         // bytes of two keys side by side: elements 4 i, 4 i + 1 and 4 i + 2, 4 i + 3
-        const uint32_t a0 = __byte_perm(s.v[0][i], s.v[1][i], 0x5140), a1 = __byte_perm(s.v[0][i], s.v[1][i], 0x7362);
-        const uint32_t b0 = __byte_perm(s.v[2][i], s.v[3][i], 0x5140), b1 = __byte_perm(s.v[2][i], s.v[3][i], 0x7362);
+        const uint32_t a0 = __byte_perm(v[0][i], v[1][i], 0x5140), a1 = __byte_perm(v[0][i], v[1][i], 0x7362);
+        const uint32_t b0 = __byte_perm(v[2][i], v[3][i], 0x5140), b1 = __byte_perm(v[2][i], v[3][i], 0x7362);
         mma16816(o[4 * i], pk, widen2(a0 & 0xffffu), widen2(b0 & 0xffffu));
         mma16816(o[4 * i + 1], pk, widen2(a0 >> 16), widen2(b0 >> 16));
         mma16816(o[4 * i + 2], pk, widen2(a1 & 0xffffu), widen2(b1 & 0xffffu));
@@ -457,10 +455,14 @@ PI_DEV void put4(__nv_bfloat16* p, float4 v) {
     *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
 }
 
+// Blocks of an SM: what registers and rings leave room for.
+template <int DH, bool HALF>
+constexpr int few_blocks() { return DH == 64 || HALF ? 3 : 2; }
+
 template <typename T, int DH, bool HALF>
-__global__ void __launch_bounds__(kThreads, 2) k_attn8_few(const __grid_constant__ Few8Args a) {
+__global__ void __launch_bounds__(kThreads, few_blocks<DH, HALF>()) k_attn8_few(const __grid_constant__ Few8Args a) {
     pdl_entry();
-    constexpr int KC = Step8<DH>::KC, OC = DH / 8, CHUNKS = HALF ? DH / 16 : DH / 8, RH = HALF ? 1 : 2;
+    constexpr int KC = Slot8<DH>::KC, OC = DH / 8, CHUNKS = HALF ? DH / 16 : DH / 8, RH = HALF ? 1 : 2;
     extern __shared__ __align__(16) unsigned char few_smem[];
     Few8Shared<DH>& sh = *reinterpret_cast<Few8Shared<DH>*>(few_smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q4 = lane & 3, r8 = lane >> 2;
@@ -521,19 +523,31 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn8_few(const __grid_constant
         // this warp's steps: keys 16 s of the piece's tiles that some row sees
         const int s_end = (min(p.hi, (p.j0 + p.nt) * kTile) + kBlock - 1) / kBlock;
         const int s0 = max(p.lo, p.j0 * kTile) / kBlock + warp;
-        auto page_of = [&](int s) {
-            if (s >= s_end) return -1;
-            const int id = pages[s >> (a.c.page_shift - 4)];
+        const int steps = s0 < s_end ? (s_end - s0 + kWarps - 1) / kWarps : 0;
+        // Pages and exponents of the warp's next 32 steps, a lane each; those of the 32
+        // behind them come while these run.
+        auto page_of = [&](int i) {
+            if (i >= steps) return -1;
+            const int id = pages[(s0 + i * kWarps) >> (a.c.page_shift - 4)];
             if (id >= 0 && id < a.c.num_pages) return id;
             atomicExch(a.status, (int)PI_ERR_INVALID_ARG);
             return -1;
         };
-        Step8<DH> x, y;
-        int id0 = page_of(s0), id1 = page_of(s0 + kWarps), id2 = page_of(s0 + 2 * kWarps), id3 = page_of(s0 + 3 * kWarps);
-        load_keys<DH>(a, x, id0, s0 * kBlock, p.g);
-        load_values<DH>(a, x, id0, s0 * kBlock, p.g);
-        load_keys<DH>(a, y, id1, (s0 + kWarps) * kBlock, p.g);
-        load_values<DH>(a, y, id1, (s0 + kWarps) * kBlock, p.g);
+        auto exponents_of = [&](int i, int id) {
+            if (id < 0) return 0;
+            const long long at = (((long long)id * a.c.kv_heads + p.g) << (a.c.page_shift - 4)) + ((s0 + i * kWarps) & ((1 << (a.c.page_shift - 4)) - 1));
+            return bounded(a.c.ke[at]) * 256 + bounded(a.c.ve[at]);
+        };
+        int id = page_of(lane), id_next = page_of(32 + lane);
+        Slot8<DH>* const ring = sh.ring[warp];
+        auto ask = [&](int i) {   // step i of the piece, at most 31 ahead of the one that runs
+            const int mine = __shfl_sync(FULL, i & 32 ? id_next : id, i & 31);
+            if (i < steps) fetch<DH>(a, ring[i % kStages], mine, (s0 + i * kWarps) * kBlock, p.g);
+            copies_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) ask(i);
+        int ex = exponents_of(lane, id), ex_next = 0;
 
         // queries, and what the rows see (rows of nothing: all, so that they do not ask for masking)
         uint32_t q[DH / 16][4];
@@ -604,19 +618,28 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn8_few(const __grid_constant
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
 
-        for (int s = s0; s < s_end; s += 2 * kWarps) {
-            auto one = [&](Step8<DH>& z, int at, int next_id) {
-                const int kb = at * kBlock, ahead = (at + 2 * kWarps) * kBlock;
-                step<DH, HALF>(p, z, kb, kb < lo_most || kb + kBlock > hi_least, q, w, o,
-                               [&] { load_keys<DH>(a, z, next_id, ahead, p.g); });
-                load_values<DH>(a, z, next_id, ahead, p.g);
-            };
-            const int id4 = page_of(s + 4 * kWarps), id5 = page_of(s + 5 * kWarps);
-            one(x, s, id2);
-            if (s + kWarps < s_end) one(y, s + kWarps, id3);
-            id2 = id4;
-            id3 = id5;
+        for (int i = 0; i < steps; ++i) {
+            const int in_32 = i & 31;
+            if (in_32 == 0 && i > 0) {
+                id = id_next;
+                ex = ex_next;
+                id_next = page_of(i + 32 + lane);
+            }
+            if (in_32 == 16) ex_next = exponents_of((i & ~31) + 32 + lane, id_next);
+            {   // the step kStages - 1 ahead
+                const int n = in_32 + kStages - 1;
+                const int mine = __shfl_sync(FULL, n & 32 ? id_next : id, n & 31);
+                if (i + kStages - 1 < steps)
+                    fetch<DH>(a, ring[(i + kStages - 1) % kStages], mine, (s0 + (i + kStages - 1) * kWarps) * kBlock, p.g);
+                copies_commit();
+            }
+            copies_wait<kStages - 1>();
+            const int e = __shfl_sync(FULL, ex, in_32), ev = (int)(signed char)(e & 255), ek = (e - ev) >> 8;
+            const int kb = (s0 + i * kWarps) * kBlock;
+            step<DH, HALF>(p, ring[i % kStages], ek, ev, kb, kb < lo_most || kb + kBlock > hi_least, q, w, o);
         }
+        copies_wait<0>();
+        __syncthreads();   // the rings are empty: their place is the sums'
 
         // the warps' sums, each scaled to the block's maximum
 #pragma unroll
@@ -896,7 +919,7 @@ struct Layout8 {
     int blocks;
     Layout8(const pi_paged_desc& d, const pi_page8_desc& c, int sms) {
         auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-        blocks = 2 * std::max(1, sms);
+        blocks = kMostBlocks * std::max(1, sms);
         ml = up((size_t)blocks * sizeof(int));
         o = up(ml + (size_t)blocks * 2 * kRows * 2 * sizeof(float));
         wide = up(o + (size_t)blocks * 2 * kRows * c.head_dim * sizeof(float));
@@ -913,12 +936,30 @@ struct Layout8 {
     }
 };
 
-template <typename T, int DH>
-cudaError_t launch_few(const Few8Args& a, bool half, int blocks, cudaStream_t s) {
-    constexpr size_t smem = sizeof(Few8Shared<DH>);
-    static_assert(smem <= 48 * 1024, "shared memory without opting in");
-    return half ? launch_pdl(k_attn8_few<T, DH, true>, blocks, kThreads, smem, s, a)
-                : launch_pdl(k_attn8_few<T, DH, false>, blocks, kThreads, smem, s, a);
+template <typename T, int DH, bool HALF>
+cudaError_t launch_few(const Few8Args& a, int sms, cudaStream_t s) {
+    static std::mutex mu;
+    static bool done[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    constexpr int smem = (int)sizeof(Few8Shared<DH>);
+    static_assert(few_blocks<DH, HALF>() * (smem + 1024) <= 228 * 1024, "shared memory of an SM");
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        if (!done[dev]) {
+            e = cudaFuncSetAttribute(k_attn8_few<T, DH, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return e;
+            done[dev] = true;
+        }
+    }
+    return launch_pdl(k_attn8_few<T, DH, HALF>, few_blocks<DH, HALF>() * sms, kThreads, smem, s, a);
+}
+template <typename T>
+cudaError_t launch_few(const Few8Args& a, int dh, bool half, int sms, cudaStream_t s) {
+    if (dh == 128) return half ? launch_few<T, 128, true>(a, sms, s) : launch_few<T, 128, false>(a, sms, s);
+    return half ? launch_few<T, 64, true>(a, sms, s) : launch_few<T, 64, false>(a, sms, s);
 }
 
 }  // namespace
@@ -983,11 +1024,8 @@ pi_status pi_paged_attn8(const pi_paged_desc* desc, const pi_page8_desc* cache, 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool half = std::min(desc->max_new, a.few) * a.group <= 8;   // no item has more than 8 rows
     const bool f16 = dtype == PI_T_F16;
-    cudaError_t e;
-    if (cache->head_dim == 128)
-        e = f16 ? launch_few<__half, 128>(a, half, lay.blocks, s) : launch_few<__nv_bfloat16, 128>(a, half, lay.blocks, s);
-    else
-        e = f16 ? launch_few<__half, 64>(a, half, lay.blocks, s) : launch_few<__nv_bfloat16, 64>(a, half, lay.blocks, s);
+    cudaError_t e = f16 ? launch_few<__half>(a, cache->head_dim, half, sms, s)
+                        : launch_few<__nv_bfloat16>(a, cache->head_dim, half, sms, s);
     if (e != cudaSuccess) return PI_ERR_CUDA;
     if (desc->max_new <= a.few) return PI_OK;
     Widen8Args w{a.c, block_table, cu_new, kv_len, ws + lay.k, ws + lay.v, desc->batch, desc->max_tokens, desc->max_new,
