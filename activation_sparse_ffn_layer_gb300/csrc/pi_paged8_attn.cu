@@ -737,33 +737,65 @@ __global__ void __launch_bounds__(kThreads, few_blocks<DH, HALF>()) k_attn8_few(
             if (sh.seen == p.parts - 1) {
                 // partial of block block0 + k: its second slot (k = 0, where the item starts) or its first
                 auto slot_of = [&](int k) { return (p.block0 + k) * 2 + (k == 0 ? 1 : 0); };
-                const float2* const ml = reinterpret_cast<const float2*>(a.part_ml);
                 const float4* const all = reinterpret_cast<const float4*>(a.part_o);
+                // m and l of all parts beside each other, up to as many as the rings' place holds at a time
+                const int most = kWarps * kStages * (int)sizeof(Slot8<DH>) / (kRows * (int)sizeof(float2));
+                float2* const ml = reinterpret_cast<float2*>(&sh.ring[0][0]);
                 float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, use[2] = {0.f, 0.f};
-                for (int k = 0; k < p.parts; ++k)
-#pragma unroll
-                    for (int h = 0; h < RH; ++h) m[h] = fmaxf(m[h], __ldcg(ml + slot_of(k) * kRows + r8 + 8 * h).x);
-#pragma unroll
-                for (int h = 0; h < RH; ++h) use[h] = m[h] == -INFINITY ? 0.f : m[h];
                 float4 v[CHUNKS / kWarps];
 #pragma unroll
                 for (int i = 0; i < CHUNKS / kWarps; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-                for (int k = 0; k < p.parts; ++k) {
-                    const int at = slot_of(k);
-                    float f[2] = {0.f, 0.f};
+                for (int k0 = 0; k0 < p.parts; k0 += most) {
+                    const int n = min(most, p.parts - k0);
+                    __syncthreads();
+                    for (int i = tid; i < n * kRows; i += kThreads)
+                        ml[i] = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + slot_of(k0 + i / kRows) * kRows + i % kRows);
+                    __syncthreads();
 #pragma unroll
                     for (int h = 0; h < RH; ++h) {
-                        const float2 z = __ldcg(ml + at * kRows + r8 + 8 * h);
-                        f[h] = ex2(z.x - use[h]);
-                        l[h] = fmaf(z.y, f[h], l[h]);
-                    }
+                        float top = m[h];
+#pragma unroll 4
+                        for (int k = 0; k < n; ++k) top = fmaxf(top, ml[k * kRows + r8 + 8 * h].x);
+                        use[h] = top == -INFINITY ? 0.f : top;
+                        const float f = ex2(m[h] - use[h]);   // of what the parts before these have summed
+                        m[h] = top;
+                        l[h] *= f;
 #pragma unroll
-                    for (int i = 0; i < CHUNKS / kWarps; ++i) {
-                        const int c = warp + i * kWarps;
-                        const float4 z = __ldcg(all + ((size_t)at * Few8Shared<DH>::CHUNKS + c) * 32 + lane);
-                        const float g = HALF || c < DH / 16 ? f[0] : f[1];
-                        v[i] = make_float4(fmaf(z.x, g, v[i].x), fmaf(z.y, g, v[i].y), fmaf(z.z, g, v[i].z), fmaf(z.w, g, v[i].w));
+                        for (int i = 0; i < CHUNKS / kWarps; ++i)
+                            if (HALF || (warp + i * kWarps) / (DH / 16) == h) {
+                                v[i].x *= f;
+                                v[i].y *= f;
+                                v[i].z *= f;
+                                v[i].w *= f;
+                            }
+                    }
+                    constexpr int AT_ONCE = 16 / (CHUNKS / kWarps);   // parts whose loads are in flight together
+                    for (int k = 0; k < n; k += AT_ONCE) {
+                        float4 z[AT_ONCE][CHUNKS / kWarps];
+#pragma unroll
+                        for (int x = 0; x < AT_ONCE; ++x) {   // past the end: the last one once more, left out below
+                            const int at = slot_of(k0 + min(k + x, n - 1));
+#pragma unroll
+                            for (int i = 0; i < CHUNKS / kWarps; ++i)
+                                z[x][i] = __ldcg(all + ((size_t)at * Few8Shared<DH>::CHUNKS + warp + i * kWarps) * 32 + lane);
+                        }
+#pragma unroll
+                        for (int x = 0; x < AT_ONCE; ++x) {
+                            if (k + x >= n) break;
+                            float f[2] = {0.f, 0.f};
+#pragma unroll
+                            for (int h = 0; h < RH; ++h) {
+                                const float2 y = ml[(k + x) * kRows + r8 + 8 * h];
+                                f[h] = ex2(y.x - use[h]);
+                                l[h] = fmaf(y.y, f[h], l[h]);
+                            }
+#pragma unroll
+                            for (int i = 0; i < CHUNKS / kWarps; ++i) {
+                                const float g = HALF || warp + i * kWarps < DH / 16 ? f[0] : f[1];
+                                v[i] = make_float4(fmaf(z[x][i].x, g, v[i].x), fmaf(z[x][i].y, g, v[i].y), fmaf(z[x][i].z, g, v[i].z),
+                                                   fmaf(z[x][i].w, g, v[i].w));
+                            }
+                        }
                     }
                 }
                 const float inv[2] = {inverse(l[0]), inverse(l[1])};
