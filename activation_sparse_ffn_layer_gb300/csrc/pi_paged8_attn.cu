@@ -26,9 +26,11 @@
 // piece's keys.  An item cut by a border leaves unnormalised partials (m, l, O)
 // in the workspace, and the block that arrives last adds them in block order
 // (the order is fixed, who does it is not: same bits).
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 #include <math.h>
 
 #include <algorithm>
@@ -37,24 +39,27 @@
 #include "pi_common.cuh"
 #include "pi_e4m3.cuh"
 #include "pi_internal.h"
+#include "pi_pipe.cuh"
+#include "pi_umma.cuh"
 
 namespace pi {
 namespace {
 
 using namespace e4m3;
+using namespace pipe;
 
 constexpr int kRows = 16;            // rows of an item
 constexpr int kFewRows = 64;         // rows of a request up to which it goes through k_attn8_few (or one token's)
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kTile = 16 * kWarps;   // keys of a unit of the work split
-constexpr int kLead = 2;             // units that an item counts besides its tiles
-constexpr int kMinUnits = 2;         // units of a block at least
-constexpr int kMostBlocks = 3;       // of an SM
+constexpr int kTile = 32;            // keys of a unit of the work split
+constexpr int kLead = 5;             // units that an item counts besides its tiles
+constexpr int kMinUnits = 4;         // units of a block at least
 constexpr float kLift = 7.f;         // log2 of the factor that P, l and O share
 constexpr float kGrow = 8.f;         // growth (log2) of a maximum before m follows
 constexpr float kLn2 = 0.69314718055994531f;
 
 struct Few8Args {
+    // {dh / 4 words, positions of a page, heads, pages}, box dh / 4 x 16 or 32
+    CUtensorMap kmap, vmap;
     Cache8 c;
     const void* q;
     const int32_t *table, *cu, *kv;
@@ -63,10 +68,12 @@ struct Few8Args {
     long long q_stride, o_stride;
     int heads, batch, max_tokens, max_new, max_pages, window, group, few;
     float scale;
-    int* counters;     // [blocks] arrivals at a cut item
-    float* part_ml;    // [blocks][2][16][2]
-    float* part_o;     // [blocks][2][chunks][32][4]
+    int* counters;     // [blocks] arrivals at an item that blocks share
+    float* part_ml;    // [blocks][2][16][2]: a block's sums of such items
+    float4* part_o;    // [blocks][2][chunks][32]
+    float4* warp_o;    // [blocks][warps][2][chunks][32]: a warp's sums of items that warps share
     int* status;
+    long long timeout_ns;
 };
 
 struct Request8 {
@@ -134,31 +141,30 @@ PI_DEV long long request_units(const Few8Args& a, const Request8& r) {   // of o
 
 // A range of key tiles of one item.
 struct Piece8 {
+    long long i0;    // the item's first unit
     int nt;          // key tiles (0: end)
-    int j0;          // first key tile
+    int from, all;   // the first of them and how many there are, counted from the item's first
     int lo, hi;      // keys that some row of the item sees
     int b, g, rt;
     int rows;        // of the item
     int first, cu;   // of the request
-    int block0, parts;   // blocks that hold a part of the item: the first, and how many
-    int own;         // this block's partial: 1 where the item starts here
 };
 
 struct Walk8 {
     Request8 r;
-    long long u, u1, U;   // unit reached, the range's end, units in all
-    int G, b, g, rt, off;   // blocks with work; request, KV head, row tile and unit within the item at u
+    long long u, u1;        // unit reached, the range's end
+    int b, g, rt, off;      // request, KV head, row tile and unit within the item at u
 
     PI_DEV Piece8 next(const Few8Args& a) {
         Piece8 p{};
-        while (u < u1 && p.nt == 0) {
+        while (u < u1 && p.nt == 0) {   // again where only an item's lead falls into this range
             int lo, hi;
             const int nt = item_range(a, r, rt, &lo, &hi);
-            const long long i0 = u - off;
-            const int stop = (int)min((long long)(kLead + nt), u1 - i0);
-            const int from = max(off - kLead, 0), to = max(stop - kLead, 0);
-            p.nt = max(to - from, 0);
-            p.j0 = lo / kTile + from;
+            p.i0 = u - off;
+            const int stop = (int)min((long long)(kLead + nt), u1 - p.i0);
+            p.from = max(off - kLead, 0);
+            p.nt = max(max(stop - kLead, 0) - p.from, 0);
+            p.all = nt;
             p.lo = lo;
             p.hi = hi;
             p.b = b;
@@ -167,15 +173,7 @@ struct Walk8 {
             p.rows = min(kRows, r.n * a.group - rt * kRows);
             p.first = r.first;
             p.cu = r.cu;
-            p.parts = 1;
-            p.own = from == 0;
-            if (p.nt != nt) {
-                // blocks that own its first and its last tile, in range whatever the lengths become under the kernel
-                const long long b0 = ((i0 + kLead + 1) * G - 1) / U, b1 = ((i0 + kLead + nt) * G - 1) / U;
-                p.block0 = (int)min(max(b0, 0ll), (long long)G - 1);
-                p.parts = (int)min(max(b1 - b0 + 1, 1ll), (long long)(G - p.block0));
-            }
-            u = stop > off ? i0 + stop : u1;
+            u = stop > off ? p.i0 + stop : u1;   // (off past the item: the lengths changed under the kernel)
             off = 0;
             if (u < u1 && ++rt >= row_tiles(a, r)) {
                 rt = 0;
@@ -195,6 +193,12 @@ struct Walk8 {
         return p;
     }
 };
+
+// a / b for positive numbers, in 32 bits where they fit (a 64-bit division is a call)
+PI_DEV long long quotient(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return (unsigned)a / (unsigned)b;
+    return a / b;
+}
 
 PI_DEV float ex2(float x) {
     float y;
@@ -225,59 +229,68 @@ PI_DEV uint32_t query2(uint32_t w, float f, __nv_bfloat16) {
 }
 PI_DEV uint32_t query2(uint32_t w, float, __half) { return w; }
 
-// The codes of 16 keys, as a lane uses them.  Keys: keys 8 j + lane / 4, elements 16 q ..
-// and 64 + 16 q .. (q = lane % 4).  Values: keys 2 q, 2 q + 1, 2 q + 8, 2 q + 9, elements
-// (dh / 8) (lane / 4) ...  A lane copies what it uses itself, so a ring's slot is ordered
-// by lane and nothing but the lane's own wait is needed before it is read.
+// The codes of a tile of 32 keys, a row a position, 16-byte pieces in the order that the
+// copies' swizzle gives them.  Of the keys of block b a lane uses 8 j + lane / 4, elements
+// 16 q .. and 64 + 16 q .. (q = lane % 4); of the values 2 q, 2 q + 1, 2 q + 8, 2 q + 9,
+// elements (dh / 8) (lane / 4) ..
 template <int DH>
 struct Slot8 {
-    static constexpr int KC = DH / 64, VW = DH / 32;   // 16-byte chunks of a key, words of a value
-    uint4 k[2 * KC][32];
-    uint32_t v[4][32][VW];
+    static constexpr int KC = DH / 64, VW = DH / 32;   // 16-byte pieces of a lane's key, words of its value
+    unsigned char k[kTile * DH], v[kTile * DH];
+
+    static PI_DEV int at(int row, int piece) {
+        return row * DH + ((DH == 128 ? piece ^ (row & 7) : piece ^ ((row >> 1) & 3)) * 16);
+    }
+    PI_DEV uint4 key(int b, int j, int c) const {
+        const int lane = threadIdx.x & 31;
+        return *reinterpret_cast<const uint4*>(k + at(16 * b + 8 * j + (lane >> 2), (lane & 3) + 4 * c));
+    }
+    PI_DEV void value(int b, int x, uint32_t (&w)[VW]) const {
+        const int lane = threadIdx.x & 31, row = 16 * b + 2 * (lane & 3) + (x & 1) + 8 * (x >> 1), r8 = lane >> 2;
+        if (DH == 128) {
+            const uint4 z = *reinterpret_cast<const uint4*>(v + at(row, r8));
+            w[0] = z.x;
+            w[1] = z.y;
+            w[VW - 2] = z.z;
+            w[VW - 1] = z.w;
+        } else {
+            const uint2 z = *reinterpret_cast<const uint2*>(v + at(row, r8 >> 1) + (r8 & 1) * 8);
+            w[0] = z.x;
+            w[1] = z.y;
+        }
+    }
 };
 
-template <int BYTES>
-PI_DEV void copy_async(void* to, const void* from, bool there) {   // zeros where not there
-    const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
-    const int n = there ? BYTES : 0;
-    if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from), "r"(n) : "memory");
-    else asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(at), "l"(from), "r"(n) : "memory");
-}
-PI_DEV void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-PI_DEV void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-// Asks for the codes of keys kb .. kb + 15 (page `id`, negative: zeros).
-template <int DH>
-PI_DEV void fetch(const Few8Args& a, Slot8<DH>& to, int id, int kb, int g) {
-    const int lane = threadIdx.x & 31, q4 = lane & 3, r8 = lane >> 2;
-    const bool there = id >= 0;
-    const long long at = there ? id * a.c.page_stride + g * a.c.head_stride + (kb & ((1 << a.c.page_shift) - 1)) * a.c.token_stride : 0;
-    const uint8_t* const k = a.c.k + at + r8 * a.c.token_stride + q4 * 16;
-    const uint8_t* const v = a.c.v + at + 2 * q4 * a.c.token_stride + r8 * (DH / 8);
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int c = 0; c < Slot8<DH>::KC; ++c)
-            copy_async<16>(&to.k[j * Slot8<DH>::KC + c][lane], k + 8 * j * a.c.token_stride + 64 * c, there);
-#pragma unroll
-    for (int x = 0; x < 4; ++x) copy_async<DH / 8>(to.v[x][lane], v + ((x & 1) + 8 * (x >> 1)) * a.c.token_stride, there);
+PI_DEV void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, unsigned long long* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(su32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(su32(bar))
+        : "memory");
 }
 
-constexpr int kStages = 4;           // slots of a warp's ring
+// Warps of a block, one block on an SM: what registers leave room for.
+template <int DH, bool HALF>
+struct Few8Cfg {
+    static constexpr int WARPS = HALF ? 12 : 8, THREADS = 32 * WARPS;
+    static constexpr int CHUNKS = HALF ? DH / 16 : DH / 8;   // float4 of a lane's part of O
+    static constexpr int STAGES = DH == 64 ? 4 : HALF ? 2 : 3;   // slots of a warp's ring
+};
+constexpr int kMostWarps = 12;
 
-template <int DH>
+template <int DH, bool HALF>
 struct Few8Shared {
-    static constexpr int CHUNKS = DH / 8;     // float4 of a thread's part of O
-    union {
-        Slot8<DH> ring[kWarps][kStages];
-        float4 o[kWarps][CHUNKS][32];         // a piece's sums, once its rings are empty
-    };
-    float ml[kWarps][kRows][2];
-    long long scratch[kWarps + 1];
-    Walk8 walk;
-    Piece8 piece;
-    int seen;
+    using C = Few8Cfg<DH, HALF>;
+    Slot8<DH> ring[C::WARPS][C::STAGES];
+    unsigned long long full[C::WARPS][C::STAGES];   // a slot's codes are there
+    int abort_flag;
+    float2 ml[C::WARPS][2][kRows];     // m and l of pieces that warps share, as of their O in warp_o
+    long long scratch[C::WARPS + 1];
+    long long before[C::THREADS];      // units of the requests before those that a thread has counted
+    Walk8 walk[C::WARPS];
+    Piece8 piece[C::WARPS][2];         // a warp's next pieces
+    Piece8 cut[C::WARPS][2];           // those that it shares: the one it does not begin, the one it does not end
+    Piece8 open[2];                    // items that the block shares with others, by whether it begins them
+    int parts[2], seen[2];
 };
 
 // This lane's rows r = lane / 4 and r + 8 of an item.
@@ -287,84 +300,77 @@ struct Rows8 {
     float m[2], l[2];
 };
 
-// One step of 16 keys from kb on, whose blocks have exponents ek and ev.
+// One tile: two blocks of 16 keys from kb on, with exponents ek and ev.
 // HALF: rows 8 .. 15 hold nothing.
 template <int DH, bool HALF>
-PI_DEV void step(const Piece8& p, const Slot8<DH>& s, int ek, int ev, int kb, bool edge, const uint32_t (&q)[DH / 16][4],
-                 Rows8& w, float (&o)[DH / 8][4]) {
-    constexpr int KC = Slot8<DH>::KC, VW = Slot8<DH>::VW, RH = HALF ? 1 : 2;
+PI_DEV void step(const Piece8& p, const Slot8<DH>& s, const int (&ek)[2], const int (&ev)[2], int kb, bool edge,
+                 const uint32_t (&q)[DH / 16][4], Rows8& w, float (&o)[DH / 8][4]) {
+    constexpr int KC = Slot8<DH>::KC, VW = Slot8<DH>::VW, RH = HALF ? 1 : 2, NB = 2;
     const int lane = threadIdx.x & 31, q4 = lane & 3;
-    float acc[2][2][4];   // two chains for each 8 keys
+    float acc[NB][2][4];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[j][i][e] = 0.f;
-#pragma unroll
-    for (int c = 0; c < KC; ++c)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint4 y = s.k[j * KC + c][lane];
-                const uint32_t word = i == 0 ? y.x : i == 1 ? y.y : i == 2 ? y.z : y.w;
-                mma16816(acc[j][i & 1], q[4 * c + i], widen2(word & 0xffffu), widen2(word >> 16));
-            }
-    uint32_t v[4][VW];
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-        if (DH == 128) {
-            const uint4 y = *reinterpret_cast<const uint4*>(s.v[x][lane]);
-            v[x][0] = y.x;
-            v[x][1] = y.y;
-            v[x][VW - 2] = y.z;
-            v[x][VW - 1] = y.w;
-        } else {
-            const uint2 y = *reinterpret_cast<const uint2*>(s.v[x][lane]);
-            v[x][0] = y.x;
-            v[x][1] = y.y;
-        }
-    }
-    // x = c 2^ek S of this lane's keys kb + 8 j + 2 q + e
-    float x[2][4];
-    const float fk = pow2(ek), fev = (float)ev;
-#pragma unroll
-    for (int h = 0; h < RH; ++h) {
-        const float f = fminf(w.c[h] * fk, 3e38f);
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) x[j][2 * h + e] = (acc[j][0][2 * h + e] + acc[j][1][2 * h + e]) * f;
-    }
-    uint32_t see = ~0u;    // bit 4 j + 2 h + e: the row sees the key
-    if (edge) {
-        see = 0;
+            for (int e = 0; e < 4; ++e) acc[b][j][e] = 0.f;
 #pragma unroll
-        for (int h = 0; h < RH; ++h)
+    for (int c = 0; c < KC; ++c) {
+        uint4 y[NB][2];
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) y[b][j] = s.key(b, j, c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t word = i == 0 ? y[b][j].x : i == 1 ? y[b][j].y : i == 2 ? y[b][j].z : y[b][j].w;
+                    mma16816(acc[b][j], q[4 * c + i], widen2(word & 0xffffu), widen2(word >> 16));
+                }
+    }
+    // x = c 2^ek S of this lane's keys kb + 16 b + 8 j + 2 q + e
+    float x[NB][2][4];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const float fk = pow2(ek[b]);
+#pragma unroll
+        for (int h = 0; h < RH; ++h) {
+            const float f = fminf(w.c[h] * fk, 3e38f);
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int key = kb + 8 * j + 2 * q4 + e;
-                    if (key >= w.lo[h] && key < w.hi[h]) see |= 1u << (4 * j + 2 * h + e);
-                    else x[j][2 * h + e] = -INFINITY;
-                }
-        // values of keys that no row sees are not used, whatever they are
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-            const int key = kb + 8 * (y >> 1) + 2 * q4 + (y & 1);
-            if (key < p.lo || key >= p.hi)
-#pragma unroll
-                for (int i = 0; i < VW; ++i) v[y][i] = 0u;
+                for (int e = 2 * h; e < 2 * h + 2; ++e)
+                    x[b][j][e] = acc[b][j][e] * f;
         }
+    }
+    uint32_t see = ~0u;    // bit 8 b + 4 j + 2 h + e: the row sees the key
+    if (edge) {
+        see = 0;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int h = 0; h < RH; ++h)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int key = kb + 16 * b + 8 * j + 2 * q4 + e;
+                        if (key >= w.lo[h] && key < w.hi[h]) see |= 1u << (8 * b + 4 * j + 2 * h + e);
+                        else x[b][j][2 * h + e] = -INFINITY;
+                    }
     }
     // m, where it has to move
     bool grown = false;
     float top[2];
 #pragma unroll
     for (int h = 0; h < RH; ++h) {
-        top[h] = fmaxf(fmaxf(x[0][2 * h], x[0][2 * h + 1]), fmaxf(x[1][2 * h], x[1][2 * h + 1])) + fev;
+        top[h] = -INFINITY;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+            top[h] = fmaxf(top[h], fmaxf(fmaxf(x[b][0][2 * h], x[b][0][2 * h + 1]), fmaxf(x[b][1][2 * h], x[b][1][2 * h + 1])) + (float)ev[b]);
         grown |= top[h] > w.m[h] + kGrow;
     }
     if (__any_sync(FULL, grown)) {
@@ -382,66 +388,81 @@ PI_DEV void step(const Piece8& p, const Slot8<DH>& s, int ek, int ev, int kb, bo
             }
         }
     }
-    uint32_t pk[4] = {0u, 0u, 0u, 0u};
-    const float back = pow2(-ev);
+    uint32_t pk[NB][4];
 #pragma unroll
-    for (int h = 0; h < RH; ++h) {
-        const float bias = kLift + fev - (w.m[h] == -INFINITY ? 0.f : w.m[h]);
-        float y[2][2], sum = 0.f;
+    for (int b = 0; b < NB; ++b) {
+        if (HALF) pk[b][1] = pk[b][3] = 0u;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int h = 0; h < RH; ++h) {
+            const float bias = kLift + (float)ev[b] - (w.m[h] == -INFINITY ? 0.f : w.m[h]);
+            float y[2][2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) sum += y[j][e] = ex2(x[j][2 * h + e] + bias);
-        w.l[h] = fmaf(sum, back, w.l[h]);
-        pk[h] = half2_of(y[0][0], y[0][1]);
-        pk[2 + h] = half2_of(y[1][0], y[1][1]);
-    }
-    if (edge) {
-        // 0 x NaN would reach rows that do not see the value: such codes leave the
-        // product, and the rows that see one become NaN there
-        bool nan = false;
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int y = 0; y < 4; ++y)
-#pragma unroll
-            for (int i = 0; i < VW; ++i) nan |= (((v[y][i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
-        if (__any_sync(FULL, nan)) {
-            uint32_t seen[4];   // 1 where the row sees the key
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int at = 4 * (i >> 1) + 2 * (i & 1);
-                seen[i] = HALF && (i & 1) ? 0u : ((see >> at) & 1 ? 0x3c00u : 0u) | ((see >> (at + 1)) & 1 ? 0x3c000000u : 0u);
-            }
-#pragma unroll
-            for (int i = 0; i < VW; ++i) {
-                uint32_t one[4];
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const uint32_t is = (((v[y][i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
-                    v[y][i] &= ~(is * 255u);
-                    one[y] = is * 0x38u;   // the code of 1
-                }
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float n[4] = {0.f, 0.f, 0.f, 0.f};
-                    const int sh = 8 * c;
-                    mma16816(n, seen, widen2(((one[0] >> sh) & 255u) | ((one[1] >> sh) & 255u) << 8),
-                             widen2(((one[2] >> sh) & 255u) | ((one[3] >> sh) & 255u) << 8));
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (n[e] > 0.f) o[4 * i + c][e] = NAN;
-                }
-            }
+                for (int e = 0; e < 2; ++e) y[j][e] = ex2(x[b][j][2 * h + e] + bias);
+            w.l[h] = fmaf((y[0][0] + y[0][1]) + (y[1][0] + y[1][1]), pow2(-ev[b]), w.l[h]);
+            pk[b][h] = half2_of(y[0][0], y[0][1]);
+            pk[b][2 + h] = half2_of(y[1][0], y[1][1]);
         }
     }
 #pragma unroll
-    for (int i = 0; i < VW; ++i) {
-        // bytes of two keys side by side: elements 4 i, 4 i + 1 and 4 i + 2, 4 i + 3
-        const uint32_t a0 = __byte_perm(v[0][i], v[1][i], 0x5140), a1 = __byte_perm(v[0][i], v[1][i], 0x7362);
-        const uint32_t b0 = __byte_perm(v[2][i], v[3][i], 0x5140), b1 = __byte_perm(v[2][i], v[3][i], 0x7362);
-        mma16816(o[4 * i], pk, widen2(a0 & 0xffffu), widen2(b0 & 0xffffu));
-        mma16816(o[4 * i + 1], pk, widen2(a0 >> 16), widen2(b0 >> 16));
-        mma16816(o[4 * i + 2], pk, widen2(a1 & 0xffffu), widen2(b1 & 0xffffu));
-        mma16816(o[4 * i + 3], pk, widen2(a1 >> 16), widen2(b1 >> 16));
+    for (int b = 0; b < NB; ++b) {
+        uint32_t v[4][VW];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) s.value(b, y, v[y]);
+        if (edge) {
+            // values of keys that no row sees are not used, whatever they are; and 0 x NaN
+            // would reach rows that do not see the value: such codes leave the product, and
+            // the rows that see one become NaN there
+            bool nan = false;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int key = kb + 16 * b + 8 * (y >> 1) + 2 * q4 + (y & 1);
+#pragma unroll
+                for (int i = 0; i < VW; ++i) {
+                    if (key < p.lo || key >= p.hi) v[y][i] = 0u;
+                    nan |= (((v[y][i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
+                }
+            }
+            if (__any_sync(FULL, nan)) {
+                uint32_t seen[4];   // 1 where the row sees the key
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int at = 8 * b + 4 * (i >> 1) + 2 * (i & 1);
+                    seen[i] = HALF && (i & 1) ? 0u : ((see >> at) & 1 ? 0x3c00u : 0u) | ((see >> (at + 1)) & 1 ? 0x3c000000u : 0u);
+                }
+#pragma unroll
+                for (int i = 0; i < VW; ++i) {
+                    uint32_t one[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const uint32_t is = (((v[y][i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
+                        v[y][i] &= ~(is * 255u);
+                        one[y] = is * 0x38u;   // the code of 1
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float n[4] = {0.f, 0.f, 0.f, 0.f};
+                        const int sh = 8 * c;
+                        mma16816(n, seen, widen2(((one[0] >> sh) & 255u) | ((one[1] >> sh) & 255u) << 8),
+                                 widen2(((one[2] >> sh) & 255u) | ((one[3] >> sh) & 255u) << 8));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (n[e] > 0.f) o[4 * i + c][e] = NAN;
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < VW; ++i) {
+            // bytes of two keys side by side: elements 4 i, 4 i + 1 and 4 i + 2, 4 i + 3
+            const uint32_t a0 = __byte_perm(v[0][i], v[1][i], 0x5140), a1 = __byte_perm(v[0][i], v[1][i], 0x7362);
+            const uint32_t b0 = __byte_perm(v[2][i], v[3][i], 0x5140), b1 = __byte_perm(v[2][i], v[3][i], 0x7362);
+            mma16816(o[4 * i], pk[b], widen2(a0 & 0xffffu), widen2(b0 & 0xffffu));
+            mma16816(o[4 * i + 1], pk[b], widen2(a0 >> 16), widen2(b0 >> 16));
+            mma16816(o[4 * i + 2], pk[b], widen2(a1 & 0xffffu), widen2(b1 & 0xffffu));
+            mma16816(o[4 * i + 3], pk[b], widen2(a1 >> 16), widen2(b1 >> 16));
+        }
     }
 }
 
@@ -455,99 +476,172 @@ PI_DEV void put4(__nv_bfloat16* p, float4 v) {
     *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
 }
 
-// Blocks of an SM: what registers and rings leave room for.
+// The key tiles of a warp's piece.  Pages and exponents of its blocks are looked up 32 at a
+// time (16 tiles), a lane each; those of the 32 behind them come while these run.
 template <int DH, bool HALF>
-constexpr int few_blocks() { return DH == 64 || HALF ? 3 : 2; }
+struct Run8 {
+    static constexpr int STAGES = Few8Cfg<DH, HALF>::STAGES;
+    int first, tiles;            // first block (of the request, even), tiles
+    int asked, taken;            // tiles asked for, and those of them that have been waited for
+    int slot, ask_slot, phase;   // of the ring: next to use, next to fill, the phase of the next's copies
+    int id, id_next, ex, ex_next;   // page of this lane's block (past the cache: zeros), ek * 256 + ev
+
+    PI_DEV int page_of(const Few8Args& a, const Piece8& p, int i) const {
+        if (i >= 2 * tiles || (first + i) * kBlock >= p.hi) return a.c.num_pages;
+        const int page = a.table[(size_t)p.b * a.max_pages + ((first + i) >> (a.c.page_shift - 4))];
+        if (page >= 0 && page < a.c.num_pages) return page;
+        if ((first + i + 1) * kBlock > p.lo) atomicExch(a.status, (int)PI_ERR_INVALID_ARG);
+        return a.c.num_pages;   // past the last page: the copy fills zeros
+    }
+    PI_DEV int exponents_of(const Few8Args& a, const Piece8& p, int i, int page) const {
+        if (page >= a.c.num_pages) return 0;
+        const int in_page = (first + i) & ((1 << (a.c.page_shift - 4)) - 1);
+        const long long at = (((long long)page * a.c.kv_heads + p.g) << (a.c.page_shift - 4)) + in_page;
+        return bounded(a.c.ke[at]) * 256 + bounded(a.c.ve[at]);
+    }
+    // asks for the next tile, if there is one (the lanes are done with its slot): a copy of 32
+    // positions for keys and for values, or two of 16 where pages hold no more
+    PI_DEV void ask(const Few8Args& a, const Piece8& p, Few8Shared<DH, HALF>& sh, int batch) {
+        if (asked >= tiles) return;
+        const int i = 2 * (asked - batch);   // 0 .. 62
+        const int page = __shfl_sync(FULL, i & 32 ? id_next : id, i & 31), page1 = __shfl_sync(FULL, i & 32 ? id_next : id, (i + 1) & 31);
+        if ((threadIdx.x & 31) == 0) {
+            Slot8<DH>& to = sh.ring[threadIdx.x >> 5][ask_slot];
+            unsigned long long* const bar = &sh.full[threadIdx.x >> 5][ask_slot];
+            const int pos = ((first + 2 * asked) & ((1 << (a.c.page_shift - 4)) - 1)) * kBlock;
+            bar_arrive_expect_tx(bar, 2 * kTile * DH);
+            tma_load_4d(to.k, &a.kmap, 0, pos, p.g, page, bar);
+            tma_load_4d(to.v, &a.vmap, 0, pos, p.g, page, bar);
+            if (a.c.page_shift == 4) {
+                tma_load_4d(to.k + kBlock * DH, &a.kmap, 0, 0, p.g, page1, bar);
+                tma_load_4d(to.v + kBlock * DH, &a.vmap, 0, 0, p.g, page1, bar);
+            }
+        }
+        ++asked;
+        if (++ask_slot == STAGES) ask_slot = 0;
+    }
+    // waits (bounded) for the next tile in the ring; false: gave up
+    PI_DEV bool take(Few8Shared<DH, HALF>& sh, const Ctl& ctl, const Slot8<DH>** at) {
+        const int warp = threadIdx.x >> 5;
+        *at = &sh.ring[warp][slot];
+        unsigned long long* const bar = &sh.full[warp][slot];
+        if (!__all_sync(FULL, bar_test(bar, phase)) && !__all_sync(FULL, bar_wait(bar, phase, ctl))) return false;
+        ++taken;
+        if (++slot == STAGES) {
+            slot = 0;
+            phase ^= 1;
+        }
+        return true;
+    }
+    // every copy asked for has landed before the block may exit
+    PI_DEV void drain(Few8Shared<DH, HALF>& sh) {
+        for (; taken < asked; ++taken) {
+            bar_drain(&sh.full[threadIdx.x >> 5][slot], phase, kDrainTimeoutNs);
+            if (++slot == STAGES) {
+                slot = 0;
+                phase ^= 1;
+            }
+        }
+    }
+    PI_DEV void start(const Few8Args& a, const Piece8& p, Few8Shared<DH, HALF>& sh) {
+        const int lane = threadIdx.x & 31;
+        first = 2 * (p.lo / kTile + p.from);
+        tiles = p.lo < p.hi ? p.nt : 0;
+        asked = taken = 0;
+        id = page_of(a, p, lane);
+        id_next = page_of(a, p, 32 + lane);
+        for (int i = 0; i < STAGES; ++i) ask(a, p, sh, 0);
+        ex = exponents_of(a, p, lane, id);
+        ex_next = 0;
+    }
+};
+
+// 1 / l (a sum of 0: the row sees nothing; one that is not a number stays one), and log sum e^a
+PI_DEV float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
+PI_DEV float log_sum(float m, float l) { return l == 0.f ? -INFINITY : (m - kLift + log2f(l)) * kLn2; }
 
 template <typename T, int DH, bool HALF>
-__global__ void __launch_bounds__(kThreads, few_blocks<DH, HALF>()) k_attn8_few(const __grid_constant__ Few8Args a) {
+__global__ void __launch_bounds__(Few8Cfg<DH, HALF>::THREADS, 1) k_attn8_few(const __grid_constant__ Few8Args a) {
     pdl_entry();
-    constexpr int KC = Slot8<DH>::KC, OC = DH / 8, CHUNKS = HALF ? DH / 16 : DH / 8, RH = HALF ? 1 : 2;
-    extern __shared__ __align__(16) unsigned char few_smem[];
-    Few8Shared<DH>& sh = *reinterpret_cast<Few8Shared<DH>*>(few_smem);
+    using C = Few8Cfg<DH, HALF>;
+    constexpr int KC = Slot8<DH>::KC, OC = DH / 8, CHUNKS = C::CHUNKS, RH = HALF ? 1 : 2, STAGES = C::STAGES;
+    constexpr int W = C::WARPS, THREADS = C::THREADS;
+    extern __shared__ __align__(1024) unsigned char few_smem[];
+    Few8Shared<DH, HALF>& sh = *reinterpret_cast<Few8Shared<DH, HALF>*>(few_smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q4 = lane & 3, r8 = lane >> 2;
 
-    // units of all requests, and where this block's range starts
-    const int per = (a.batch + kThreads - 1) / kThreads, b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
+    if ((su32(few_smem) & 1023u) != 0) {   // the copies' swizzle needs it; the whole block leaves
+        if (tid == 0) atomicExch(a.status, (int)PI_ERR_UNSUPPORTED);
+        return;
+    }
+    if (lane == 0) {
+        for (int i = 0; i < STAGES; ++i) bar_init(&sh.full[warp][i], 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (tid == 0) {
+        sh.abort_flag = 0;
+        tma_prefetch_map(&a.kmap);
+        tma_prefetch_map(&a.vmap);
+    }
+
+    // units of all requests, and where the warps' ranges start
+    const int per = (a.batch + THREADS - 1) / THREADS, b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
     long long own = 0, U = 0;
     bool bad = false;
     for (int b = b0; b < b1; ++b) own += a.c.kv_heads * request_units(a, request8(a, b, &bad));
     if (bad && blockIdx.x == 0) atomicExch(a.status, (int)PI_ERR_INVALID_ARG);
-    if (tid == 0) {
-        sh.walk = Walk8{};
-        sh.walk.u = 0x7fffffffffffffffll;
-    }
-    const long long pre = scan_before<kThreads>(own, sh.scratch, &U);
+    if (tid < W) sh.cut[tid][0].nt = sh.cut[tid][1].nt = 0;
+    if (tid < 2) sh.open[tid].nt = 0;
+    const long long pre = scan_before<THREADS>(own, sh.scratch, &U);
     const int G = (int)min((long long)gridDim.x, max(U / kMinUnits, U > 0 ? 1ll : 0ll));
     if ((int)blockIdx.x >= G) return;
-    const long long u0 = U * blockIdx.x / G, u1 = U * (blockIdx.x + 1) / G;
-    if (tid == 0) {
-        sh.walk.u1 = u1;
-        sh.walk.U = U;
-        sh.walk.G = G;
-    }
-    if (pre <= u0 && u0 < pre + own) {
-        long long left = u0 - pre;
-        for (int b = b0; b < b1; ++b) {
-            const Request8 r = request8(a, b, &bad);
-            const long long u = request_units(a, r);
-            if (left >= a.c.kv_heads * u) {
-                left -= a.c.kv_heads * u;
-                continue;
-            }
-            const int g = (int)(left / u);
-            left -= g * u;
-            int rt = 0, lo, hi;
-            for (;; ++rt) {
-                const int cost = kLead + item_range(a, r, rt, &lo, &hi);
-                if (left < cost) break;
-                left -= cost;
-            }
-            sh.walk.u = u0;
-            sh.walk.b = b;
-            sh.walk.g = g;
-            sh.walk.rt = rt;
-            sh.walk.off = (int)left;
-            sh.walk.r = r;
-            break;
-        }
-    }
+    const long long u0 = quotient(U * blockIdx.x, G), u1 = quotient(U * (blockIdx.x + 1), G);
+    sh.before[tid] = pre;
     __syncthreads();
+    if (lane == 0) {
+        const long long v0 = u0 + (u1 - u0) * warp / W, v1 = u0 + (u1 - u0) * (warp + 1) / W;
+        Walk8 walk{};
+        if (v0 < v1) {
+            // the last thread whose requests' units start at or before v0
+            int t = 0;
+            for (int d = 256; d > 0; d >>= 1)
+                if (t + d < THREADS && sh.before[t + d] <= v0) t += d;
+            long long left = v0 - sh.before[t];
+            const int e = min(min((t + 1) * per, a.batch), a.batch);
+            for (int b = min(t * per, a.batch); b < e; ++b) {
+                const Request8 r = request8(a, b, &bad);
+                const long long u = request_units(a, r);
+                if (left >= a.c.kv_heads * u) {
+                    left -= a.c.kv_heads * u;
+                    continue;
+                }
+                const int g = (int)quotient(left, u);
+                left -= g * u;
+                int rt = 0, lo, hi;
+                for (;; ++rt) {
+                    const int cost = kLead + item_range(a, r, rt, &lo, &hi);
+                    if (left < cost) break;
+                    left -= cost;
+                }
+                walk = Walk8{r, v0, v1, b, g, rt, (int)left};
+                break;
+            }
+        }
+        sh.walk[warp] = walk;
+        sh.piece[warp][0] = sh.walk[warp].next(a);
+    }
+    __syncwarp();
+    const Ctl ctl{a.status, a.timeout_ns, &sh.abort_flag};
+    Run8<DH, HALF> run;
+    run.slot = run.ask_slot = run.phase = 0;
+    run.start(a, sh.piece[warp][0], sh);
+    if (lane == 0) sh.piece[warp][1] = sh.walk[warp].next(a);
+    __syncwarp();
+    bool ok = true;
 
-    for (;;) {
-        if (tid == 0) sh.piece = sh.walk.next(a);
-        __syncthreads();
-        const Piece8 p = sh.piece;
-        if (p.nt == 0) return;
-        const int32_t* const pages = a.table + (size_t)p.b * a.max_pages;
-        // this warp's steps: keys 16 s of the piece's tiles that some row sees
-        const int s_end = (min(p.hi, (p.j0 + p.nt) * kTile) + kBlock - 1) / kBlock;
-        const int s0 = max(p.lo, p.j0 * kTile) / kBlock + warp;
-        const int steps = s0 < s_end ? (s_end - s0 + kWarps - 1) / kWarps : 0;
-        // Pages and exponents of the warp's next 32 steps, a lane each; those of the 32
-        // behind them come while these run.
-        auto page_of = [&](int i) {
-            if (i >= steps) return -1;
-            const int id = pages[(s0 + i * kWarps) >> (a.c.page_shift - 4)];
-            if (id >= 0 && id < a.c.num_pages) return id;
-            atomicExch(a.status, (int)PI_ERR_INVALID_ARG);
-            return -1;
-        };
-        auto exponents_of = [&](int i, int id) {
-            if (id < 0) return 0;
-            const long long at = (((long long)id * a.c.kv_heads + p.g) << (a.c.page_shift - 4)) + ((s0 + i * kWarps) & ((1 << (a.c.page_shift - 4)) - 1));
-            return bounded(a.c.ke[at]) * 256 + bounded(a.c.ve[at]);
-        };
-        int id = page_of(lane), id_next = page_of(32 + lane);
-        Slot8<DH>* const ring = sh.ring[warp];
-        auto ask = [&](int i) {   // step i of the piece, at most 31 ahead of the one that runs
-            const int mine = __shfl_sync(FULL, i & 32 ? id_next : id, i & 31);
-            if (i < steps) fetch<DH>(a, ring[i % kStages], mine, (s0 + i * kWarps) * kBlock, p.g);
-            copies_commit();
-        };
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) ask(i);
-        int ex = exponents_of(lane, id), ex_next = 0;
+    for (int n = 0;; ++n) {
+        const Piece8 p = sh.piece[warp][n & 1];
+        if (p.nt == 0) break;
 
         // queries, and what the rows see (rows of nothing: all, so that they do not ask for masking)
         uint32_t q[DH / 16][4];
@@ -618,193 +712,221 @@ __global__ void __launch_bounds__(kThreads, few_blocks<DH, HALF>()) k_attn8_few(
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
 
-        for (int i = 0; i < steps; ++i) {
-            const int in_32 = i & 31;
-            if (in_32 == 0 && i > 0) {
-                id = id_next;
-                ex = ex_next;
-                id_next = page_of(i + 32 + lane);
+        for (int i = 0; i < run.tiles; ++i) {
+            const int batch = i & ~15, x = 2 * (i & 15);
+            if (x == 0 && i > 0) {
+                run.id = run.id_next;
+                run.ex = run.ex_next;
+                run.id_next = run.page_of(a, p, 2 * i + 32 + lane);
             }
-            if (in_32 == 16) ex_next = exponents_of((i & ~31) + 32 + lane, id_next);
-            {   // the step kStages - 1 ahead
-                const int n = in_32 + kStages - 1;
-                const int mine = __shfl_sync(FULL, n & 32 ? id_next : id, n & 31);
-                if (i + kStages - 1 < steps)
-                    fetch<DH>(a, ring[(i + kStages - 1) % kStages], mine, (s0 + (i + kStages - 1) * kWarps) * kBlock, p.g);
-                copies_commit();
-            }
-            copies_wait<kStages - 1>();
-            const int e = __shfl_sync(FULL, ex, in_32), ev = (int)(signed char)(e & 255), ek = (e - ev) >> 8;
-            const int kb = (s0 + i * kWarps) * kBlock;
-            step<DH, HALF>(p, ring[i % kStages], ek, ev, kb, kb < lo_most || kb + kBlock > hi_least, q, w, o);
+            if (x == 16) run.ex_next = run.exponents_of(a, p, 2 * batch + 32 + lane, run.id_next);
+            const int e0 = __shfl_sync(FULL, run.ex, x), e1 = __shfl_sync(FULL, run.ex, x + 1);
+            const int v0 = (int)(signed char)(e0 & 255), v1 = (int)(signed char)(e1 & 255);
+            const int kb = (run.first + 2 * i) * kBlock, ek[2] = {(e0 - v0) >> 8, (e1 - v1) >> 8}, ev[2] = {v0, v1};
+            const Slot8<DH>* at;
+            if (!(ok = run.take(sh, ctl, &at))) break;
+            step<DH, HALF>(p, *at, ek, ev, kb, kb < lo_most || kb + kTile > hi_least, q, w, o);
+            __syncwarp();
+            run.ask(a, p, sh, batch);
         }
-        copies_wait<0>();
-        __syncthreads();   // the rings are empty: their place is the sums'
+        if (!ok) {
+            run.drain(sh);
+            break;
+        }
 
-        // the warps' sums, each scaled to the block's maximum
+        // the next piece's first blocks are on their way while this one is put away
+        run.start(a, sh.piece[warp][(n + 1) & 1], sh);
+        if (lane == 0) sh.piece[warp][n & 1] = sh.walk[warp].next(a);   // the piece after the next
 #pragma unroll
         for (int h = 0; h < RH; ++h) {
             w.l[h] += __shfl_xor_sync(FULL, w.l[h], 1);
             w.l[h] += __shfl_xor_sync(FULL, w.l[h], 2);
-            if (q4 == 0) {
-                sh.ml[warp][r8 + 8 * h][0] = w.m[h];
-                sh.ml[warp][r8 + 8 * h][1] = w.l[h];
-            }
         }
-        __syncthreads();
-        float M[2] = {-INFINITY, -INFINITY}, L[2] = {0.f, 0.f};   // of this lane's rows, over the block
-#pragma unroll
-        for (int h = 0; h < RH; ++h) {
-            float m[kWarps], l[kWarps];
-#pragma unroll
-            for (int i = 0; i < kWarps; ++i) {
-                m[i] = sh.ml[i][r8 + 8 * h][0];
-                l[i] = sh.ml[i][r8 + 8 * h][1];
-                M[h] = fmaxf(M[h], m[i]);
-            }
-            const float use = M[h] == -INFINITY ? 0.f : M[h], f = ex2(w.m[h] - use);
-#pragma unroll
-            for (int i = 0; i < kWarps; ++i) L[h] = fmaf(l[i], ex2(m[i] - use), L[h]);
-            // chunk (2 h + e) DH / 32 + i: elements 4 i .. of this lane's run e, of row r8 + 8 h
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-                for (int i = 0; i < DH / 32; ++i)
-                    sh.o[warp][(2 * h + e) * (DH / 32) + i][lane] =
-                        make_float4(o[4 * i][2 * h + e] * f, o[4 * i + 1][2 * h + e] * f, o[4 * i + 2][2 * h + e] * f, o[4 * i + 3][2 * h + e] * f);
-        }
-        __syncthreads();
-
-        // a thread's share: chunks warp, warp + 4, ... of its lane's rows
-        auto write = [&](int c, float4 v, const float (&inv)[2]) {
-            const int h = c / (DH / 16), e = c / (DH / 32) % 2, tr = r8 + 8 * h, row = p.rt * kRows + tr;
-            if (tr >= p.rows) return;
-            const int tok = row / a.group, head = p.g * a.group + row - tok * a.group;
-            const float f = inv[h];
-            put4(static_cast<T*>(a.out) + (long long)(p.cu + tok) * a.o_stride + (long long)head * DH + (2 * q4 + e) * (DH / 8) + c % (DH / 32) * 4,
-                 make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
-        };
-        auto write_lse = [&](const float (&m)[2], const float (&l)[2]) {
-            if (a.lse == nullptr || warp != 0 || q4 != 0) return;
+        if (p.nt == p.all) {
 #pragma unroll
             for (int h = 0; h < RH; ++h) {
                 const int tr = r8 + 8 * h, row = p.rt * kRows + tr;
                 if (tr >= p.rows) continue;
                 const int tok = row / a.group, head = p.g * a.group + row - tok * a.group;
-                a.lse[(long long)(p.cu + tok) * a.heads + head] = l[h] == 0.f ? -INFINITY : (m[h] - kLift + log2f(l[h])) * kLn2;
-            }
-        };
-        // (a sum of 0: the row sees nothing; one that is not a number stays one)
-        auto inverse = [](float l) { return l == 0.f ? 0.f : 1.f / l; };
-        if (p.parts == 1) {
-            const float inv[2] = {inverse(L[0]), inverse(L[1])};
+                T* const dst = static_cast<T*>(a.out) + (long long)(p.cu + tok) * a.o_stride + (long long)head * DH + 2 * q4 * (DH / 8);
+                const float f = inverse(w.l[h]);
 #pragma unroll
-            for (int c = warp; c < CHUNKS; c += kWarps) {
-                float4 v = sh.o[0][c][lane];
+                for (int e = 0; e < 2; ++e)
 #pragma unroll
-                for (int i = 1; i < kWarps; ++i) {
-                    const float4 z = sh.o[i][c][lane];
-                    v = make_float4(v.x + z.x, v.y + z.y, v.z + z.z, v.w + z.w);
-                }
-                write(c, v, inv);
+                    for (int i = 0; i < OC; i += 4)
+                        put4(dst + e * (DH / 8) + i, make_float4(o[i][2 * h + e] * f, o[i + 1][2 * h + e] * f, o[i + 2][2 * h + e] * f, o[i + 3][2 * h + e] * f));
+                if (a.lse != nullptr && q4 == 0) a.lse[(long long)(p.cu + tok) * a.heads + head] = log_sum(w.m[h], w.l[h]);
             }
-            write_lse(M, L);
         } else {
-            const int slot = (int)blockIdx.x * 2 + p.own;
-            float4* const po = reinterpret_cast<float4*>(a.part_o) + (size_t)slot * Few8Shared<DH>::CHUNKS * 32;
-            float2* const pm = reinterpret_cast<float2*>(a.part_ml) + slot * kRows;
+            const int slot = p.from == 0;   // a warp begins at most one piece that it does not end
+            float4* const po = a.warp_o + (((size_t)blockIdx.x * W + warp) * 2 + slot) * CHUNKS * 32 + lane;
 #pragma unroll
-            for (int c = warp; c < CHUNKS; c += kWarps) {
-                float4 v = sh.o[0][c][lane];
+            for (int h = 0; h < RH; ++h) {
+                if (q4 == 0) sh.ml[warp][slot][r8 + 8 * h] = make_float2(w.m[h], w.l[h]);
+                // chunk (2 h + e) DH / 32 + i: elements 4 i .. of this lane's run e, of row r8 + 8 h
 #pragma unroll
-                for (int i = 1; i < kWarps; ++i) {
-                    const float4 z = sh.o[i][c][lane];
-                    v = make_float4(v.x + z.x, v.y + z.y, v.z + z.z, v.w + z.w);
-                }
-                po[c * 32 + lane] = v;
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int i = 0; i < DH / 32; ++i)
+                        po[((2 * h + e) * (DH / 32) + i) * 32] = make_float4(o[4 * i][2 * h + e], o[4 * i + 1][2 * h + e], o[4 * i + 2][2 * h + e], o[4 * i + 3][2 * h + e]);
             }
-            if (warp == 0 && q4 == 0)
+            if (lane == 0) sh.cut[warp][slot] = p;
+        }
+        __syncwarp();
+    }
+
+    // ---- items that warps of this block share: each of them takes its share of the chunks
+    auto write = [&](const Piece8& p, int c, float4 v, const float (&inv)[2]) {
+        const int h = c / (DH / 16), e = c / (DH / 32) % 2, tr = r8 + 8 * h, row = p.rt * kRows + tr;
+        if (tr >= p.rows) return;
+        const int tok = row / a.group, head = p.g * a.group + row - tok * a.group;
+        const float f = inv[h];
+        put4(static_cast<T*>(a.out) + (long long)(p.cu + tok) * a.o_stride + (long long)head * DH + (2 * q4 + e) * (DH / 8) + c % (DH / 32) * 4,
+             make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
+    };
+    auto write_lse = [&](const Piece8& p, const float (&m)[2], const float (&l)[2]) {
+        if (a.lse == nullptr || q4 != 0) return;
 #pragma unroll
-                for (int h = 0; h < RH; ++h) pm[r8 + 8 * h] = make_float2(M[h], L[h]);
-            // the block's stores happen before thread 0's arrival (barrier, then release), the
-            // other blocks' before what any thread reads after it (acquire, then barrier)
-            __syncthreads();
-            if (tid == 0) {
-                sh.seen = arrive_gpu(a.counters + p.block0);
-                if (sh.seen == p.parts - 1) a.counters[p.block0] = 0;
+        for (int h = 0; h < RH; ++h) {
+            const int tr = r8 + 8 * h, row = p.rt * kRows + tr;
+            if (tr >= p.rows) continue;
+            const int tok = row / a.group, head = p.g * a.group + row - tok * a.group;
+            a.lse[(long long)(p.cu + tok) * a.heads + head] = log_sum(m[h], l[h]);
+        }
+    };
+    __syncthreads();
+    if (*(volatile int*)&sh.abort_flag) return;
+    const Piece8* const cuts = &sh.cut[0][0];
+    for (int slot = 0; slot < 2; ++slot) {
+        const Piece8& p = sh.cut[warp][slot];
+        if (p.nt == 0) continue;
+        const unsigned who = __ballot_sync(FULL, lane < 2 * W && cuts[lane].nt > 0 && cuts[lane].i0 == p.i0);   // in the order of the keys
+        const int k = __popc(who), mine = __popc(who & ((1u << (2 * warp + slot)) - 1u));
+        const Piece8 &first = cuts[__ffs(who) - 1], &last = cuts[31 - __clz(who)];
+        const bool begun = first.from == 0, whole = begun && last.from + last.nt == last.all;
+        float M[2] = {-INFINITY, -INFINITY}, L[2] = {0.f, 0.f}, use[2] = {0.f, 0.f};
+        for (unsigned x = who; x != 0; x &= x - 1)
+#pragma unroll
+            for (int h = 0; h < RH; ++h) M[h] = fmaxf(M[h], (&sh.ml[0][0][0])[(__ffs(x) - 1) * kRows + r8 + 8 * h].x);
+#pragma unroll
+        for (int h = 0; h < RH; ++h) use[h] = M[h] == -INFINITY ? 0.f : M[h];
+        const float4* const po = a.warp_o + (size_t)blockIdx.x * W * 2 * CHUNKS * 32 + lane;
+        const size_t at = (size_t)blockIdx.x * 2 + begun;
+        for (unsigned x = who; x != 0; x &= x - 1)
+#pragma unroll
+            for (int h = 0; h < RH; ++h) {
+                const float2 y = (&sh.ml[0][0][0])[(__ffs(x) - 1) * kRows + r8 + 8 * h];
+                L[h] = fmaf(y.y, ex2(y.x - use[h]), L[h]);
             }
-            __syncthreads();
-            if (sh.seen == p.parts - 1) {
-                // partial of block block0 + k: its second slot (k = 0, where the item starts) or its first
-                auto slot_of = [&](int k) { return (p.block0 + k) * 2 + (k == 0 ? 1 : 0); };
-                const float4* const all = reinterpret_cast<const float4*>(a.part_o);
-                // m and l of all parts beside each other, up to as many as the rings' place holds at a time
-                const int most = kWarps * kStages * (int)sizeof(Slot8<DH>) / (kRows * (int)sizeof(float2));
-                float2* const ml = reinterpret_cast<float2*>(&sh.ring[0][0]);
-                float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, use[2] = {0.f, 0.f};
-                float4 v[CHUNKS / kWarps];
+        const float inv[2] = {inverse(L[0]), inverse(L[1])};
+        for (int c = mine; c < CHUNKS; c += k) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (unsigned x = who; x != 0;) {   // four parts at a time (past the end: the last once more, left out below)
+                float4 z[4];
+                float f[4];
 #pragma unroll
-                for (int i = 0; i < CHUNKS / kWarps; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int k0 = 0; k0 < p.parts; k0 += most) {
-                    const int n = min(most, p.parts - k0);
-                    __syncthreads();
-                    for (int i = tid; i < n * kRows; i += kThreads)
-                        ml[i] = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + slot_of(k0 + i / kRows) * kRows + i % kRows);
-                    __syncthreads();
-#pragma unroll
-                    for (int h = 0; h < RH; ++h) {
-                        float top = m[h];
-#pragma unroll 4
-                        for (int k = 0; k < n; ++k) top = fmaxf(top, ml[k * kRows + r8 + 8 * h].x);
-                        use[h] = top == -INFINITY ? 0.f : top;
-                        const float f = ex2(m[h] - use[h]);   // of what the parts before these have summed
-                        m[h] = top;
-                        l[h] *= f;
-#pragma unroll
-                        for (int i = 0; i < CHUNKS / kWarps; ++i)
-                            if (HALF || (warp + i * kWarps) / (DH / 16) == h) {
-                                v[i].x *= f;
-                                v[i].y *= f;
-                                v[i].z *= f;
-                                v[i].w *= f;
-                            }
-                    }
-                    constexpr int AT_ONCE = 16 / (CHUNKS / kWarps);   // parts whose loads are in flight together
-                    for (int k = 0; k < n; k += AT_ONCE) {
-                        float4 z[AT_ONCE][CHUNKS / kWarps];
-#pragma unroll
-                        for (int x = 0; x < AT_ONCE; ++x) {   // past the end: the last one once more, left out below
-                            const int at = slot_of(k0 + min(k + x, n - 1));
-#pragma unroll
-                            for (int i = 0; i < CHUNKS / kWarps; ++i)
-                                z[x][i] = __ldcg(all + ((size_t)at * Few8Shared<DH>::CHUNKS + warp + i * kWarps) * 32 + lane);
-                        }
-#pragma unroll
-                        for (int x = 0; x < AT_ONCE; ++x) {
-                            if (k + x >= n) break;
-                            float f[2] = {0.f, 0.f};
-#pragma unroll
-                            for (int h = 0; h < RH; ++h) {
-                                const float2 y = ml[(k + x) * kRows + r8 + 8 * h];
-                                f[h] = ex2(y.x - use[h]);
-                                l[h] = fmaf(y.y, f[h], l[h]);
-                            }
-#pragma unroll
-                            for (int i = 0; i < CHUNKS / kWarps; ++i) {
-                                const float g = HALF || warp + i * kWarps < DH / 16 ? f[0] : f[1];
-                                v[i] = make_float4(fmaf(z[x][i].x, g, v[i].x), fmaf(z[x][i].y, g, v[i].y), fmaf(z[x][i].z, g, v[i].z),
-                                                   fmaf(z[x][i].w, g, v[i].w));
-                            }
-                        }
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    const int part = x != 0 ? __ffs(x) - 1 : 31 - __clz(who);
+                    z[i] = __ldcg(po + ((size_t)part * CHUNKS + c) * 32);
+                    f[i] = x != 0 ? ex2((&sh.ml[0][0][0])[part * kRows + r8 + (HALF || c < DH / 16 ? 0 : 8)].x - use[HALF || c < DH / 16 ? 0 : 1]) : -1.f;
+                    x &= x - 1;
                 }
-                const float inv[2] = {inverse(l[0]), inverse(l[1])};
 #pragma unroll
-                for (int i = 0; i < CHUNKS / kWarps; ++i) write(warp + i * kWarps, v[i], inv);
-                write_lse(m, l);
+                for (int i = 0; i < 4; ++i)
+                    if (!(f[i] < 0.f)) v = make_float4(fmaf(z[i].x, f[i], v.x), fmaf(z[i].y, f[i], v.y), fmaf(z[i].z, f[i], v.z), fmaf(z[i].w, f[i], v.w));
+            }
+            if (whole) write(p, c, v, inv);
+            else a.part_o[(at * CHUNKS + c) * 32 + lane] = v;
+        }
+        if (mine == 0) {
+            if (whole) {
+                write_lse(p, M, L);
+            } else {
+                if (q4 == 0)
+#pragma unroll
+                    for (int h = 0; h < RH; ++h) reinterpret_cast<float2*>(a.part_ml)[at * kRows + r8 + 8 * h] = make_float2(M[h], L[h]);
+                if (lane == 0) sh.open[begun] = p;
             }
         }
-        // (the next piece's sums are written behind its own barriers)
+    }
+    // the block's stores happen before thread 0's arrivals (barrier, then release), the other
+    // blocks' before what any thread reads after them (acquire, then barrier)
+    __syncthreads();
+    if (sh.open[0].nt == 0 && sh.open[1].nt == 0) return;
+    if (lane == 0 && warp < 2) {
+        const int x = warp;
+        const Piece8& p = sh.open[x];
+        sh.seen[x] = -1;
+        sh.parts[x] = 0;
+        if (p.nt != 0) {
+            // blocks that hold its first and its last tile, in range whatever the lengths become under the kernel
+            const long long f = quotient((p.i0 + kLead + 1) * G - 1, U), l = quotient((p.i0 + kLead + p.all) * G - 1, U);
+            const int block0 = (int)min(max(f, 0ll), (long long)G - 1);
+            sh.parts[x] = (int)min(max(l - f + 1, 1ll), (long long)(G - block0));
+            sh.seen[x] = arrive_gpu(a.counters + block0);
+            if (sh.seen[x] == sh.parts[x] - 1) a.counters[block0] = 0;
+            sh.open[x].from = block0;
+        }
+    }
+    __syncthreads();
+    for (int x = 0; x < 2; ++x) {
+        if (sh.open[x].nt == 0 || sh.seen[x] != sh.parts[x] - 1) continue;
+        const Piece8& p = sh.open[x];
+        const int parts = sh.parts[x], block0 = p.from;
+        constexpr int SHARE = (CHUNKS + W - 1) / W;   // chunks of a warp (some have none)
+        constexpr int AT_ONCE = 8 / SHARE;            // parts whose loads are in flight together
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        float4 v[SHARE];
+#pragma unroll
+        for (int i = 0; i < SHARE; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < parts; k += AT_ONCE) {
+            float4 z[AT_ONCE][SHARE];
+            float2 y[AT_ONCE][RH];
+#pragma unroll
+            for (int j = 0; j < AT_ONCE; ++j) {   // past the end: the last one once more, left out below
+                // partial of block block0 + k: its second place (k = 0, where the item begins) or its first
+                const int part = min(k + j, parts - 1);
+                const size_t at = (size_t)(block0 + part) * 2 + (part == 0 ? 1 : 0);
+#pragma unroll
+                for (int h = 0; h < RH; ++h) y[j][h] = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + at * kRows + r8 + 8 * h);
+#pragma unroll
+                for (int i = 0; i < SHARE; ++i) z[j][i] = __ldcg(a.part_o + (at * CHUNKS + min(warp + i * W, CHUNKS - 1)) * 32 + lane);
+            }
+            float use[2];
+#pragma unroll
+            for (int h = 0; h < RH; ++h) {
+                float top = m[h];
+#pragma unroll
+                for (int j = 0; j < AT_ONCE; ++j) top = fmaxf(top, y[j][h].x);
+                use[h] = top == -INFINITY ? 0.f : top;
+                const float f = ex2(m[h] - use[h]);   // of what the parts before these have summed
+                m[h] = top;
+                l[h] *= f;
+#pragma unroll
+                for (int i = 0; i < SHARE; ++i)
+                    if ((!HALF && warp + i * W >= DH / 16) == (h == 1)) v[i] = make_float4(v[i].x * f, v[i].y * f, v[i].z * f, v[i].w * f);
+            }
+#pragma unroll
+            for (int j = 0; j < AT_ONCE; ++j) {
+                if (k + j >= parts) break;
+                float f[2] = {0.f, 0.f};
+#pragma unroll
+                for (int h = 0; h < RH; ++h) {
+                    f[h] = ex2(y[j][h].x - use[h]);
+                    l[h] = fmaf(y[j][h].y, f[h], l[h]);
+                }
+#pragma unroll
+                for (int i = 0; i < SHARE; ++i) {
+                    const float g = HALF || warp + i * W < DH / 16 ? f[0] : f[1];
+                    v[i] = make_float4(fmaf(z[j][i].x, g, v[i].x), fmaf(z[j][i].y, g, v[i].y), fmaf(z[j][i].z, g, v[i].z), fmaf(z[j][i].w, g, v[i].w));
+                }
+            }
+        }
+        const float inv[2] = {inverse(l[0]), inverse(l[1])};
+#pragma unroll
+        for (int i = 0; i < SHARE; ++i)
+            if (warp + i * W < CHUNKS) write(p, warp + i * W, v[i], inv);
+        if (warp == 0) write_lse(p, m, l);
     }
 }
 
@@ -934,6 +1056,18 @@ int sm_count() {
     return n;
 }
 
+bool codes_map(CUtensorMap* m, const void* base, const pi_page8_desc& c) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim / 4, (cuuint64_t)c.page_size, (cuuint64_t)c.kv_heads, (cuuint64_t)c.num_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)c.token_stride, (cuuint64_t)c.head_stride, (cuuint64_t)c.page_stride};
+    const cuuint32_t box[4] = {(cuuint32_t)c.head_dim / 4, (cuuint32_t)std::min(c.page_size, kTile), 1u, 1u};
+    const cuuint32_t es[4] = {1u, 1u, 1u, 1u};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              c.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // tokens up to which a request goes through k_attn8_few
 int few_tokens(int group) { return std::max(1, kFewRows / group); }
 
@@ -944,17 +1078,17 @@ pi_page_desc wide_desc(const pi_page8_desc& c, int dtype) {
 }
 
 // Workspace: arrival counters at offset 0 (the same place for every descriptor),
-// the partials of two items per block; for steps with long requests the 16-bit
+// the partials of two items per block and per warp; for steps with long requests the 16-bit
 // attention's workspace and the copies of the caches' pages.
 struct Layout8 {
-    size_t ml, o, wide, wide_bytes, k, v, total;
-    int blocks;
+    size_t ml, o, warps, wide, wide_bytes, k, v, total;
     Layout8(const pi_paged_desc& d, const pi_page8_desc& c, int sms) {
         auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-        blocks = kMostBlocks * std::max(1, sms);
-        ml = up((size_t)blocks * sizeof(int));
-        o = up(ml + (size_t)blocks * 2 * kRows * 2 * sizeof(float));
-        wide = up(o + (size_t)blocks * 2 * kRows * c.head_dim * sizeof(float));
+        const size_t blocks = std::max(1, sms), item = (size_t)kRows * c.head_dim * sizeof(float);
+        ml = up(blocks * sizeof(int));
+        o = up(ml + blocks * 2 * kRows * sizeof(float2));
+        warps = up(o + blocks * 2 * item);
+        wide = up(warps + blocks * kMostWarps * 2 * item);
         k = v = total = wide;
         wide_bytes = 0;
         if (d.max_new > few_tokens(d.heads / c.kv_heads)) {
@@ -976,8 +1110,8 @@ cudaError_t launch_few(const Few8Args& a, int sms, cudaStream_t s) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    constexpr int smem = (int)sizeof(Few8Shared<DH>);
-    static_assert(few_blocks<DH, HALF>() * (smem + 1024) <= 228 * 1024, "shared memory of an SM");
+    constexpr int smem = (int)sizeof(Few8Shared<DH, HALF>);
+    static_assert(smem <= 232448, "shared memory of a block");
     {
         std::lock_guard<std::mutex> lk(mu);
         if (!done[dev]) {
@@ -986,7 +1120,7 @@ cudaError_t launch_few(const Few8Args& a, int sms, cudaStream_t s) {
             done[dev] = true;
         }
     }
-    return launch_pdl(k_attn8_few<T, DH, HALF>, few_blocks<DH, HALF>() * sms, kThreads, smem, s, a);
+    return launch_pdl(k_attn8_few<T, DH, HALF>, sms, Few8Cfg<DH, HALF>::THREADS, smem, s, a);
 }
 template <typename T>
 cudaError_t launch_few(const Few8Args& a, int dh, bool half, int sms, cudaStream_t s) {
@@ -1050,9 +1184,11 @@ pi_status pi_paged_attn8(const pi_paged_desc* desc, const pi_page8_desc* cache, 
     a.scale = desc->scale > 0.f ? desc->scale : 1.0f / sqrtf((float)cache->head_dim);
     a.counters = reinterpret_cast<int*>(ws);
     a.part_ml = reinterpret_cast<float*>(ws + lay.ml);
-    a.part_o = reinterpret_cast<float*>(ws + lay.o);
+    a.part_o = reinterpret_cast<float4*>(ws + lay.o);
+    a.warp_o = reinterpret_cast<float4*>(ws + lay.warps);
     a.status = status_word();
-    if (sms < 1 || a.status == nullptr) return PI_ERR_CUDA;
+    a.timeout_ns = wait_timeout_ns();
+    if (sms < 1 || a.status == nullptr || !codes_map(&a.kmap, kcache, *cache) || !codes_map(&a.vmap, vcache, *cache)) return PI_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool half = std::min(desc->max_new, a.few) * a.group <= 8;   // no item has more than 8 rows
     const bool f16 = dtype == PI_T_F16;

@@ -503,26 +503,33 @@ def test_attention_inconsistent_requests(P):
     vc, ve = quantised(20, 2, 16, 64, "hnd", 2)
     q = torch.randn(6, 4, 64, device="cuda").half()
     table = tables([40, 40, 40], 16, 20)
-    good, _ = attn(P, q, kc, ke, vc, ve, table, [0, 2, 4, 6], [40, 33, 20])
+    # (the order of a row's sums goes by all requests of the step, so rows are held to the bound of their own sums)
+    good, _, tol, _ = R.attention(q, kc, ke, vc, ve, i32(table), [0, 2, 4, 6], [40, 33, 20])
+    out, _ = attn(P, q, kc, ke, vc, ve, table, [0, 2, 4, 6], [40, 33, 20])
     assert P.pi_last_device_status() == 0
+    R16.check(out, good, tol)
     out, _ = attn(P, q, kc, ke, vc, ve, table, [0, 2, 4, 6], [40, 49, 20])      # more than a table row holds
     assert P.pi_last_device_status() == 1
-    assert torch.equal(out[[0, 1, 4, 5]], good[[0, 1, 4, 5]]) and bool((out[2:4] == 0).all())
+    R16.check(out[[0, 1, 4, 5]], good[[0, 1, 4, 5]], tol[[0, 1, 4, 5]])
+    assert bool((out[2:4] == 0).all())
     out, _ = attn(P, q, kc, ke, vc, ve, table, [0, 2, 9, 6], [40, 33, 20], max_new=6)   # past the rows, then decreasing
     assert P.pi_last_device_status() == 1
-    assert torch.equal(out[:2], good[:2]) and bool((out[2:] == 7).all())
+    R16.check(out[:2], good[:2], tol[:2])
+    assert bool((out[2:] == 7).all())
     out, _ = attn(P, q, kc, ke, vc, ve, table, [0, 2, 4, 6], [40, -1, 20])
-    assert P.pi_last_device_status() == 1 and torch.equal(out[4:], good[4:])
+    assert P.pi_last_device_status() == 1
+    R16.check(out[4:], good[4:], tol[4:])
     # a page outside the cache: scores of zero and values of zero
     bad = [list(r) for r in table]
     bad[0][1] = 20
     out, _ = attn(P, q, kc, ke, vc, ve, bad, [0, 2, 4, 6], [40, 33, 20])
-    assert P.pi_last_device_status() == 1 and torch.equal(out[2:], good[2:])
+    assert P.pi_last_device_status() == 1
+    R16.check(out[2:], good[2:], tol[2:])
     k2, v2 = kc.clone(), vc.clone()
     k2.view(torch.uint8)[table[0][1]] = 0
     v2.view(torch.uint8)[table[0][1]] = 0
-    same, _ = attn(P, q, k2, ke, v2, ve, table, [0, 2, 4, 6], [40, 33, 20])
-    R16.check(out[:2], same[:2].double(), 2.0 ** -10 * same[:2].double().abs() + 1e-6, "zeros")
+    zeros, _, tol, _ = R.attention(q, k2, ke, v2, ve, i32(table), [0, 2, 4, 6], [40, 33, 20])
+    R16.check(out[:2], zeros[:2], tol[:2])
 
 
 def test_attention_strides_and_no_lse(P):
