@@ -952,29 +952,28 @@ PI_DEV int seen_pages(const Widen8Args& a, const Request8& r, int* first) {
     return ((hi + (1 << a.c.page_shift) - 1) >> a.c.page_shift) - *first;
 }
 
-PI_DEV void put16(__half* p, const uint4& c, float scale) {
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-    uint32_t o[8];
+// 8 codes times `scale` in 16 bits (fp16: finite ones past 65504 are that)
+PI_DEV void put_wide(__half* p, const uint2& c, float scale) {
+    const uint32_t w[2] = {c.x, c.y};
+    uint32_t o[4];
     auto in = [](float x) { return fabsf(x) > 65504.f ? copysignf(65504.f, x) : x; };
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
         const float2 u = values2((w[i / 2] >> (16 * (i & 1))) & 0xffffu);
         o[i] = half2_of(in(u.x * scale), in(u.y * scale));
     }
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
 }
-PI_DEV void put16(__nv_bfloat16* p, const uint4& c, float scale) {
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-    uint32_t o[8];
+PI_DEV void put_wide(__nv_bfloat16* p, const uint2& c, float scale) {
+    const uint32_t w[2] = {c.x, c.y};
+    uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
         const float2 u = values2((w[i / 2] >> (16 * (i & 1))) & 0xffffu);
         const __nv_bfloat162 y = __floats2bfloat162_rn(u.x * scale, u.y * scale);
         o[i] = *reinterpret_cast<const uint32_t*>(&y);
     }
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 template <typename T>
@@ -1009,7 +1008,7 @@ __global__ void __launch_bounds__(kWidenThreads) k_widen8(const __grid_constant_
     __syncthreads();
     int b = at_b, page = at_page, head = at_head;
     if (b >= a.batch) return;   // (the lengths changed under the kernel)
-    const int per_pos = a.dh / 16, chunks = per_pos << a.c.page_shift;
+    const int pos_shift = a.dh == 128 ? 4 : 3, chunks = 1 << (pos_shift + a.c.page_shift);   // pieces of 8 codes: of a position, of a head
     int count = seen_pages(a, request8(a, b, &bad), &first);
     for (long long u = u0; u < u1; ++u) {
         const int col = first + page;
@@ -1018,12 +1017,24 @@ __global__ void __launch_bounds__(kWidenThreads) k_widen8(const __grid_constant_
             const long long src = id * a.c.page_stride + head * a.c.head_stride;
             const long long ex = ((long long)id * a.c.kv_heads + head) << (a.c.page_shift - 4);
             const long long dst = ((long long)id * a.c.kv_heads + head) * ((long long)a.dh << a.c.page_shift);
-            for (int i = tid; i < 2 * chunks; i += kWidenThreads) {
-                const bool values = i >= chunks;
-                const int x = values ? i - chunks : i, pos = x / per_pos, c = x % per_pos;
-                const uint4 y = ld_stream16((values ? a.c.v : a.c.k) + src + pos * a.c.token_stride + c * 16);
-                const float f = pow2(bounded((values ? a.c.ve : a.c.ke)[ex + pos / kBlock]));
-                put16(static_cast<T*>(values ? a.v : a.k) + dst + (long long)x * 16, y, f);
+            // (2 chunks is 256 or more)
+            for (int i0 = tid; i0 < 2 * chunks; i0 += 4 * kWidenThreads) {
+                uint2 y[4];
+                int e[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int i = min(i0 + j * kWidenThreads, 2 * chunks - 1);
+                    const bool values = i >= chunks;
+                    const int x = i & (chunks - 1), pos = x >> pos_shift, c = x & ((1 << pos_shift) - 1);
+                    y[j] = ld_stream8((values ? a.c.v : a.c.k) + src + pos * a.c.token_stride + c * 8);
+                    e[j] = (values ? a.c.ve : a.c.ke)[ex + pos / kBlock];
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int i = i0 + j * kWidenThreads;
+                    if (i < 2 * chunks)
+                        put_wide(static_cast<T*>(i >= chunks ? a.v : a.k) + dst + (long long)(i & (chunks - 1)) * 8, y[j], pow2(bounded(e[j])));
+                }
             }
         }
         if (++head == a.c.kv_heads) {
