@@ -204,14 +204,14 @@ PI_DEV void store_codes(const Store8Args& a, float2* table, unsigned long long* 
             }
         }
         const float f = pow2(-e);
+        uint8_t* to = codes + (r + sub) * a.token_stride;
 #pragma unroll 4
-        for (int row = sub; row < count; row += SIDE) {
+        for (int row = sub; row < count; row += SIDE, to += SIDE * a.token_stride) {
             float x[4];
             turned(row, x);
             if (some)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[e] = fabsf(x[e]) < INFINITY ? x[e] : NAN;
-            uint8_t* const to = codes + (r + row) * a.token_stride;
             const uint32_t lo = encode2(x[0] * f, x[1] * f), hi = encode2(x[2] * f, x[3] * f);
             if (apart) {
                 *reinterpret_cast<uint16_t*>(to + e0) = (uint16_t)lo;
@@ -375,7 +375,6 @@ struct Read8Args {
     long long k_stride, v_stride;
     int batch, max_pages, max_rows, rows;   // rows of a block
     int head_shift, per_row;                 // pieces of 8 codes: of a head (log2), of a row
-    unsigned inverse;                        // ceil(2^32 / per_row)
     int* status;
 };
 
@@ -445,40 +444,38 @@ __global__ void __launch_bounds__(256) k_page_read8(const __grid_constant__ Read
         if (bad) atomicExch(a.status, (int)PI_ERR_INVALID_ARG);
     }
     __syncthreads();
-    const int first_array = a.k_out ? 0 : 1, arrays = (a.k_out ? 1 : 0) + (a.v_out ? 1 : 0), all = arrays * a.rows * a.per_row;
-    auto split = [&](int i, bool* values, int* r, int* piece) {
-        const int row = (int)__umulhi((unsigned)i, a.inverse);
-        *piece = i - row * a.per_row;
-        *values = row >= a.rows || first_array == 1;
-        *r = row >= a.rows ? row - a.rows : row;
-    };
-    for (int i0 = threadIdx.x; i0 < all; i0 += 4 * 256) {
-        uint2 c[4];
-        int e[4];
+    // a thread keeps its piece of the rows (of keys or values) and goes from row to row
+    const int first_array = a.k_out ? 0 : 1, pieces = ((a.k_out ? 1 : 0) + (a.v_out ? 1 : 0)) * a.per_row;
+    const int beside = max(1, 256 / pieces), r0 = pieces < 256 ? threadIdx.x / pieces : 0;   // rows that a pass takes
+    for (int i = threadIdx.x - r0 * pieces; i < pieces && r0 < beside; i += 256) {
+        const bool values = i >= a.per_row || first_array == 1;
+        const int piece = i >= a.per_row ? i - a.per_row : i, h = piece >> a.head_shift;
+        const uint8_t* const codes = (values ? a.c.v : a.c.k) + h * a.c.head_stride + (piece & ((1 << a.head_shift) - 1)) * 8;
+        const int8_t* const exps = (values ? a.c.ve : a.c.ke) + ((long long)h << (a.c.page_shift - 4));
+        const long long stride = values ? a.v_stride : a.k_stride;
+        O* to = static_cast<O*>(values ? a.v_out : a.k_out) + (row0 + r0) * stride + piece * 8;
+        for (int r = r0; r < a.rows; r += 4 * beside) {
+            uint2 c[4];
+            int e[4];
+            long long at[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            bool values;
-            int r, piece;
-            c[x] = make_uint2(0u, 0u);
-            e[x] = 0;
-            if (i0 + 256 * x >= all) break;
-            split(i0 + 256 * x, &values, &r, &piece);
-            const long long at = code_at[r];
-            if (at < 0) continue;
-            const int h = piece >> a.head_shift;
-            c[x] = ld_stream8((values ? a.c.v : a.c.k) + at + h * a.c.head_stride + (piece & ((1 << a.head_shift) - 1)) * 8);
-            e[x] = (values ? a.c.ve : a.c.ke)[exp_at[r] + ((long long)h << (a.c.page_shift - 4))];
-        }
+            for (int x = 0; x < 4; ++x) {
+                const int row = r + x * beside;
+                at[x] = row < a.rows ? code_at[row] : -2;
+                c[x] = make_uint2(0u, 0u);
+                e[x] = 0;
+                if (at[x] >= 0) {
+                    c[x] = ld_stream8(codes + at[x]);
+                    e[x] = exps[exp_at[row]];
+                }
+            }
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            bool values;
-            int r, piece;
-            if (i0 + 256 * x >= all) break;
-            split(i0 + 256 * x, &values, &r, &piece);
-            if (code_at[r] == -2) continue;
-            float f[8];
-            values8(c[x], pow2(bounded(e[x])), f);
-            put_values(static_cast<O*>(values ? a.v_out : a.k_out) + (long long)(row0 + r) * (values ? a.v_stride : a.k_stride) + piece * 8, f);
+            for (int x = 0; x < 4; ++x, to += beside * stride) {
+                if (at[x] == -2) continue;
+                float f[8];
+                values8(c[x], pow2(bounded(e[x])), f);
+                put_values(to, f);
+            }
         }
     }
 }
@@ -657,14 +654,10 @@ pi_status pi_page_read8(const pi_read8_desc* desc, const pi_page8_desc* cache, c
     a.max_rows = d.max_rows;
     a.head_shift = cache->head_dim == 128 ? 4 : 3;
     a.per_row = cache->kv_heads << a.head_shift;
-    a.inverse = (unsigned)(((1ull << 32) + a.per_row - 1) / a.per_row);
     a.status = status_word();
     if (a.status == nullptr) return PI_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     a.rows = std::min(kReadRows, std::max(1, d.max_rows / kReadBlocks));
-    // i * inverse >> 32 is i / per_row while i times inverse's excess stays below 2^32 (8 rows always do)
-    const unsigned long long excess = (unsigned long long)a.inverse * a.per_row - (1ull << 32);
-    while (2ull * a.rows * a.per_row * excess >> 32) a.rows /= 2;
     const unsigned blocks = (unsigned)((d.max_rows + (long long)a.rows - 1) / a.rows);
     const cudaError_t e = d.dtype == PI_T_F16    ? launch_pdl(k_page_read8<__half>, blocks, 256, 0, s, a)
                           : d.dtype == PI_T_BF16 ? launch_pdl(k_page_read8<__nv_bfloat16>, blocks, 256, 0, s, a)
