@@ -58,8 +58,11 @@ constexpr float kGrow = 8.f;         // growth (log2) of a maximum before m foll
 constexpr float kLn2 = 0.69314718055994531f;
 
 struct Few8Args {
-    // {dh / 4 words, positions of a page, heads, pages}, box dh / 4 x 16 or 32
+    // {dh / 4 words, positions of a page, heads, pages, arrays}, box dh / 4 x 16 or 32 positions
+    // of every array: keys and values of the lower address first, where `both`, else an array each
     CUtensorMap kmap, vmap;
+    int both;
+    int k_at, v_at, block_step;   // bytes: keys, values of a slot's first block, and the second block behind the first
     Cache8 c;
     const void* q;
     const int32_t *table, *cu, *kv;
@@ -230,43 +233,40 @@ PI_DEV uint32_t query2(uint32_t w, float f, __nv_bfloat16) {
 PI_DEV uint32_t query2(uint32_t w, float, __half) { return w; }
 
 // The codes of a tile of 32 keys, a row a position, 16-byte pieces in the order that the
-// copies' swizzle gives them.  Of the keys of block b a lane uses 8 j + lane / 4, elements
-// 16 q .. and 64 + 16 q .. (q = lane % 4); of the values 2 q, 2 q + 1, 2 q + 8, 2 q + 9,
-// elements (dh / 8) (lane / 4) ..
+// copies' swizzle gives them.  One copy brings keys and values of 32 positions (of 16 where
+// pages hold no more): a copy costs 60 cycles besides 4 for each row of 128 bytes, and with
+// copies of their own for keys and for values, of 16 rows each, 32 decoding sequences' codes
+// come at 5.0 TB/s.  Of the keys of a block a lane uses 8 j + lane / 4, elements 16 q .. and
+// 64 + 16 q .. (q = lane % 4); of the values 2 q, 2 q + 1, 2 q + 8, 2 q + 9, elements
+// (dh / 8) (lane / 4) ..
 template <int DH>
 struct Slot8 {
     static constexpr int KC = DH / 64, VW = DH / 32;   // 16-byte pieces of a lane's key, words of its value
-    unsigned char k[kTile * DH], v[kTile * DH];
+    unsigned char bytes[2 * kTile * DH];
 
     static PI_DEV int at(int row, int piece) {
         return row * DH + ((DH == 128 ? piece ^ (row & 7) : piece ^ ((row >> 1) & 3)) * 16);
     }
-    PI_DEV uint4 key(int b, int j, int c) const {
+    // (block: where the block's keys, or its values, begin)
+    PI_DEV uint4 key(int block, int j, int c) const {
         const int lane = threadIdx.x & 31;
-        return *reinterpret_cast<const uint4*>(k + at(16 * b + 8 * j + (lane >> 2), (lane & 3) + 4 * c));
+        return *reinterpret_cast<const uint4*>(bytes + block + at(8 * j + (lane >> 2), (lane & 3) + 4 * c));
     }
-    PI_DEV void value(int b, int x, uint32_t (&w)[VW]) const {
-        const int lane = threadIdx.x & 31, row = 16 * b + 2 * (lane & 3) + (x & 1) + 8 * (x >> 1), r8 = lane >> 2;
+    PI_DEV void value(int block, int x, uint32_t (&w)[VW]) const {
+        const int lane = threadIdx.x & 31, row = 2 * (lane & 3) + (x & 1) + 8 * (x >> 1), r8 = lane >> 2;
         if (DH == 128) {
-            const uint4 z = *reinterpret_cast<const uint4*>(v + at(row, r8));
+            const uint4 z = *reinterpret_cast<const uint4*>(bytes + block + at(row, r8));
             w[0] = z.x;
             w[1] = z.y;
             w[VW - 2] = z.z;
             w[VW - 1] = z.w;
         } else {
-            const uint2 z = *reinterpret_cast<const uint2*>(v + at(row, r8 >> 1) + (r8 & 1) * 8);
+            const uint2 z = *reinterpret_cast<const uint2*>(bytes + block + at(row, r8 >> 1) + (r8 & 1) * 8);
             w[0] = z.x;
             w[1] = z.y;
         }
     }
 };
-
-PI_DEV void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, unsigned long long* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(su32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(su32(bar))
-        : "memory");
-}
 
 // Warps of a block, one block on an SM: what registers leave room for.
 template <int DH, bool HALF>
@@ -289,6 +289,7 @@ struct Few8Shared {
     Walk8 walk[C::WARPS];
     Piece8 piece[C::WARPS][2];         // a warp's next pieces
     Piece8 cut[C::WARPS][2];           // those that it shares: the one it does not begin, the one it does not end
+    bool stays[C::WARPS][2];           // their sums are in the warp's ring (else in warp_o)
     Piece8 open[2];                    // items that the block shares with others, by whether it begins them
     int parts[2], seen[2];
 };
@@ -303,7 +304,7 @@ struct Rows8 {
 // One tile: two blocks of 16 keys from kb on, with exponents ek and ev.
 // HALF: rows 8 .. 15 hold nothing.
 template <int DH, bool HALF>
-PI_DEV void step(const Piece8& p, const Slot8<DH>& s, const int (&ek)[2], const int (&ev)[2], int kb, bool edge,
+PI_DEV void step(const Few8Args& a, const Piece8& p, const Slot8<DH>& s, const int (&ek)[2], const int (&ev)[2], int kb, bool edge,
                  const uint32_t (&q)[DH / 16][4], Rows8& w, float (&o)[DH / 8][4]) {
     constexpr int KC = Slot8<DH>::KC, VW = Slot8<DH>::VW, RH = HALF ? 1 : 2, NB = 2;
     const int lane = threadIdx.x & 31, q4 = lane & 3;
@@ -320,7 +321,7 @@ PI_DEV void step(const Piece8& p, const Slot8<DH>& s, const int (&ek)[2], const 
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) y[b][j] = s.key(b, j, c);
+            for (int j = 0; j < 2; ++j) y[b][j] = s.key(a.k_at + b * a.block_step, j, c);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -409,7 +410,7 @@ PI_DEV void step(const Piece8& p, const Slot8<DH>& s, const int (&ek)[2], const 
     for (int b = 0; b < NB; ++b) {
         uint32_t v[4][VW];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) s.value(b, y, v[y]);
+        for (int y = 0; y < 4; ++y) s.value(a.v_at + b * a.block_step, y, v[y]);
         if (edge) {
             // values of keys that no row sees are not used, whatever they are; and 0 x NaN
             // would reach rows that do not see the value: such codes leave the product, and
@@ -499,8 +500,7 @@ struct Run8 {
         const long long at = (((long long)page * a.c.kv_heads + p.g) << (a.c.page_shift - 4)) + in_page;
         return bounded(a.c.ke[at]) * 256 + bounded(a.c.ve[at]);
     }
-    // asks for the next tile, if there is one (the lanes are done with its slot): a copy of 32
-    // positions for keys and for values, or two of 16 where pages hold no more
+    // asks for the next tile, if there is one (the lanes are done with its slot)
     PI_DEV void ask(const Few8Args& a, const Piece8& p, Few8Shared<DH, HALF>& sh, int batch) {
         if (asked >= tiles) return;
         const int i = 2 * (asked - batch);   // 0 .. 62
@@ -510,11 +510,11 @@ struct Run8 {
             unsigned long long* const bar = &sh.full[threadIdx.x >> 5][ask_slot];
             const int pos = ((first + 2 * asked) & ((1 << (a.c.page_shift - 4)) - 1)) * kBlock;
             bar_arrive_expect_tx(bar, 2 * kTile * DH);
-            tma_load_4d(to.k, &a.kmap, 0, pos, p.g, page, bar);
-            tma_load_4d(to.v, &a.vmap, 0, pos, p.g, page, bar);
+            tma_load_5d(to.bytes, &a.kmap, 0, pos, p.g, page, 0, bar);
+            if (!a.both) tma_load_5d(to.bytes + a.v_at, &a.vmap, 0, pos, p.g, page, 0, bar);
             if (a.c.page_shift == 4) {
-                tma_load_4d(to.k + kBlock * DH, &a.kmap, 0, 0, p.g, page1, bar);
-                tma_load_4d(to.v + kBlock * DH, &a.vmap, 0, 0, p.g, page1, bar);
+                tma_load_5d(to.bytes + a.block_step, &a.kmap, 0, 0, p.g, page1, 0, bar);
+                if (!a.both) tma_load_5d(to.bytes + a.v_at + a.block_step, &a.vmap, 0, 0, p.g, page1, 0, bar);
             }
         }
         ++asked;
@@ -581,7 +581,6 @@ __global__ void __launch_bounds__(Few8Cfg<DH, HALF>::THREADS, 1) k_attn8_few(con
     if (tid == 0) {
         sh.abort_flag = 0;
         tma_prefetch_map(&a.kmap);
-        tma_prefetch_map(&a.vmap);
     }
 
     // units of all requests, and where the warps' ranges start
@@ -725,7 +724,7 @@ __global__ void __launch_bounds__(Few8Cfg<DH, HALF>::THREADS, 1) k_attn8_few(con
             const int kb = (run.first + 2 * i) * kBlock, ek[2] = {(e0 - v0) >> 8, (e1 - v1) >> 8}, ev[2] = {v0, v1};
             const Slot8<DH>* at;
             if (!(ok = run.take(sh, ctl, &at))) break;
-            step<DH, HALF>(p, *at, ek, ev, kb, kb < lo_most || kb + kTile > hi_least, q, w, o);
+            step<DH, HALF>(a, p, *at, ek, ev, kb, kb < lo_most || kb + kTile > hi_least, q, w, o);
             __syncwarp();
             run.ask(a, p, sh, batch);
         }
@@ -759,7 +758,10 @@ __global__ void __launch_bounds__(Few8Cfg<DH, HALF>::THREADS, 1) k_attn8_few(con
             }
         } else {
             const int slot = p.from == 0;   // a warp begins at most one piece that it does not end
-            float4* const po = a.warp_o + (((size_t)blockIdx.x * W + warp) * 2 + slot) * CHUNKS * 32 + lane;
+            // the last piece's sums stay in the ring, which holds nothing any more
+            static_assert(CHUNKS * 32 * sizeof(float4) <= sizeof(sh.ring[0]), "a ring holds a piece's sums");
+            const bool stays = run.tiles == 0;
+            float4* const po = (stays ? reinterpret_cast<float4*>(&sh.ring[warp][0]) : a.warp_o + (((size_t)blockIdx.x * W + warp) * 2 + slot) * CHUNKS * 32) + lane;
 #pragma unroll
             for (int h = 0; h < RH; ++h) {
                 if (q4 == 0) sh.ml[warp][slot][r8 + 8 * h] = make_float2(w.m[h], w.l[h]);
@@ -770,7 +772,10 @@ __global__ void __launch_bounds__(Few8Cfg<DH, HALF>::THREADS, 1) k_attn8_few(con
                     for (int i = 0; i < DH / 32; ++i)
                         po[((2 * h + e) * (DH / 32) + i) * 32] = make_float4(o[4 * i][2 * h + e], o[4 * i + 1][2 * h + e], o[4 * i + 2][2 * h + e], o[4 * i + 3][2 * h + e]);
             }
-            if (lane == 0) sh.cut[warp][slot] = p;
+            if (lane == 0) {
+                sh.cut[warp][slot] = p;
+                sh.stays[warp][slot] = stays;
+            }
         }
         __syncwarp();
     }
@@ -827,7 +832,8 @@ __global__ void __launch_bounds__(Few8Cfg<DH, HALF>::THREADS, 1) k_attn8_few(con
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int part = x != 0 ? __ffs(x) - 1 : 31 - __clz(who);
-                    z[i] = __ldcg(po + ((size_t)part * CHUNKS + c) * 32);
+                    z[i] = sh.stays[part >> 1][part & 1] ? reinterpret_cast<const float4*>(&sh.ring[part >> 1][0])[c * 32 + lane]
+                                                         : __ldcg(po + ((size_t)part * CHUNKS + c) * 32);
                     f[i] = x != 0 ? ex2((&sh.ml[0][0][0])[part * kRows + r8 + (HALF || c < DH / 16 ? 0 : 8)].x - use[HALF || c < DH / 16 ? 0 : 1]) : -1.f;
                     x &= x - 1;
                 }
@@ -845,7 +851,14 @@ __global__ void __launch_bounds__(Few8Cfg<DH, HALF>::THREADS, 1) k_attn8_few(con
                 if (q4 == 0)
 #pragma unroll
                     for (int h = 0; h < RH; ++h) reinterpret_cast<float2*>(a.part_ml)[at * kRows + r8 + 8 * h] = make_float2(M[h], L[h]);
-                if (lane == 0) sh.open[begun] = p;
+                if (lane == 0) {
+                    // blocks that hold its first and its last tile, in range whatever the lengths become under the kernel
+                    const long long f = quotient((p.i0 + kLead + 1) * G - 1, U), l = quotient((p.i0 + kLead + p.all) * G - 1, U);
+                    const int block0 = (int)min(max(f, 0ll), (long long)G - 1);
+                    sh.parts[begun] = (int)min(max(l - f + 1, 1ll), (long long)(G - block0));
+                    sh.open[begun] = p;
+                    sh.open[begun].from = block0;
+                }
             }
         }
     }
@@ -853,20 +866,10 @@ __global__ void __launch_bounds__(Few8Cfg<DH, HALF>::THREADS, 1) k_attn8_few(con
     // blocks' before what any thread reads after them (acquire, then barrier)
     __syncthreads();
     if (sh.open[0].nt == 0 && sh.open[1].nt == 0) return;
-    if (lane == 0 && warp < 2) {
-        const int x = warp;
-        const Piece8& p = sh.open[x];
-        sh.seen[x] = -1;
-        sh.parts[x] = 0;
-        if (p.nt != 0) {
-            // blocks that hold its first and its last tile, in range whatever the lengths become under the kernel
-            const long long f = quotient((p.i0 + kLead + 1) * G - 1, U), l = quotient((p.i0 + kLead + p.all) * G - 1, U);
-            const int block0 = (int)min(max(f, 0ll), (long long)G - 1);
-            sh.parts[x] = (int)min(max(l - f + 1, 1ll), (long long)(G - block0));
-            sh.seen[x] = arrive_gpu(a.counters + block0);
-            if (sh.seen[x] == sh.parts[x] - 1) a.counters[block0] = 0;
-            sh.open[x].from = block0;
-        }
+    if (lane == 0 && warp < 2 && sh.open[warp].nt != 0) {
+        int* const count = a.counters + sh.open[warp].from;
+        sh.seen[warp] = arrive_gpu(count);
+        if (sh.seen[warp] == sh.parts[warp] - 1) *count = 0;
     }
     __syncthreads();
     for (int x = 0; x < 2; ++x) {
@@ -1067,16 +1070,31 @@ int sm_count() {
     return n;
 }
 
-bool codes_map(CUtensorMap* m, const void* base, const pi_page8_desc& c) {
+bool codes_map(CUtensorMap* m, const void* base, const pi_page8_desc& c, int arrays, unsigned long long apart) {
     PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
     if (fn == nullptr) return false;
-    const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim / 4, (cuuint64_t)c.page_size, (cuuint64_t)c.kv_heads, (cuuint64_t)c.num_pages};
-    const cuuint64_t strides[3] = {(cuuint64_t)c.token_stride, (cuuint64_t)c.head_stride, (cuuint64_t)c.page_stride};
-    const cuuint32_t box[4] = {(cuuint32_t)c.head_dim / 4, (cuuint32_t)std::min(c.page_size, kTile), 1u, 1u};
-    const cuuint32_t es[4] = {1u, 1u, 1u, 1u};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    const cuuint64_t dims[5] = {(cuuint64_t)c.head_dim / 4, (cuuint64_t)c.page_size, (cuuint64_t)c.kv_heads, (cuuint64_t)c.num_pages,
+                                (cuuint64_t)arrays};
+    const cuuint64_t strides[4] = {(cuuint64_t)c.token_stride, (cuuint64_t)c.head_stride, (cuuint64_t)c.page_stride, apart};
+    const cuuint32_t box[5] = {(cuuint32_t)c.head_dim / 4, (cuuint32_t)std::min(c.page_size, kTile), 1u, 1u, (cuuint32_t)arrays};
+    const cuuint32_t es[5] = {1u, 1u, 1u, 1u, 1u};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 5, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
               c.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Both arrays as one tensor, the distance of their addresses a stride (16 .. 2^40 bytes), or one each.
+bool codes_maps(Few8Args* a, const void* k, const void* v, const pi_page8_desc& c) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(k), y = reinterpret_cast<uintptr_t>(v), apart = x < y ? y - x : x - y;
+    const int block = kBlock * c.head_dim, box = std::min(c.page_size, kTile) * c.head_dim;   // bytes of an array
+    a->both = apart > 0 && apart < (1ull << 40);
+    const bool keys_first = !a->both || x < y;
+    // boxes of 32 positions: 32 rows of one array, then of the other; of 16: a block of one, of the other, twice
+    a->k_at = keys_first ? 0 : box;
+    a->v_at = keys_first ? box : 0;
+    a->block_step = c.page_size < kTile ? 2 * block : block;
+    return a->both ? codes_map(&a->kmap, keys_first ? k : v, c, 2, apart)
+                   : codes_map(&a->kmap, k, c, 1, 16) && codes_map(&a->vmap, v, c, 1, 16);
 }
 
 // tokens up to which a request goes through k_attn8_few
@@ -1199,7 +1217,7 @@ pi_status pi_paged_attn8(const pi_paged_desc* desc, const pi_page8_desc* cache, 
     a.warp_o = reinterpret_cast<float4*>(ws + lay.warps);
     a.status = status_word();
     a.timeout_ns = wait_timeout_ns();
-    if (sms < 1 || a.status == nullptr || !codes_map(&a.kmap, kcache, *cache) || !codes_map(&a.vmap, vcache, *cache)) return PI_ERR_CUDA;
+    if (sms < 1 || a.status == nullptr || !codes_maps(&a, kcache, vcache, *cache)) return PI_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool half = std::min(desc->max_new, a.few) * a.group <= 8;   // no item has more than 8 rows
     const bool f16 = dtype == PI_T_F16;
