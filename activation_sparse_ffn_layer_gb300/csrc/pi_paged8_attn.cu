@@ -69,7 +69,7 @@ struct Few8Args {
     void* out;
     float* lse;
     long long q_stride, o_stride;
-    int heads, batch, max_tokens, max_new, max_pages, window, group, few;
+    int heads, batch, max_tokens, max_new, max_pages, window, group, few, rows;   // rows of an item: 8 or 16
     float scale;
     int* counters;     // [blocks] arrivals at an item that blocks share
     float* part_ml;    // [blocks][2][16][2]: a block's sums of such items
@@ -125,7 +125,7 @@ PI_DEV long long scan_before(long long v, long long* scratch, long long* all) {
 // Keys that rows 16 rt .. of a request see together, and their tiles (one, with
 // nothing to see in it, where there are none: it writes the zeros).
 PI_DEV int item_range(const Few8Args& a, const Request8& r, int rt, int* lo, int* hi) {
-    const int t0 = rt * kRows / a.group, t1 = min(rt * kRows + kRows - 1, r.n * a.group - 1) / a.group;
+    const int t0 = rt * a.rows / a.group, t1 = min(rt * a.rows + a.rows - 1, r.n * a.group - 1) / a.group;
     *hi = r.first + t1 + 1;
     *lo = a.window > 0 ? max(0, r.first + t0 - a.window + 1) : 0;
     if (*hi <= *lo) {
@@ -134,7 +134,7 @@ PI_DEV int item_range(const Few8Args& a, const Request8& r, int rt, int* lo, int
     }
     return (*hi + kTile - 1) / kTile - *lo / kTile;
 }
-PI_DEV int row_tiles(const Few8Args& a, const Request8& r) { return r.n > a.few ? 0 : (r.n * a.group + kRows - 1) / kRows; }
+PI_DEV int row_tiles(const Few8Args& a, const Request8& r) { return r.n > a.few ? 0 : (r.n * a.group + a.rows - 1) / a.rows; }
 PI_DEV long long request_units(const Few8Args& a, const Request8& r) {   // of one KV head
     long long u = 0;
     int lo, hi;
@@ -173,7 +173,7 @@ struct Walk8 {
             p.b = b;
             p.g = g;
             p.rt = rt;
-            p.rows = min(kRows, r.n * a.group - rt * kRows);
+            p.rows = min(a.rows, r.n * a.group - rt * a.rows);
             p.first = r.first;
             p.cu = r.cu;
             u = stop > off ? p.i0 + stop : u1;   // (off past the item: the lengths changed under the kernel)
@@ -658,7 +658,7 @@ __global__ void __launch_bounds__(Few8Cfg<DH, HALF>::THREADS, 1) k_attn8_few(con
                 for (int i = 0; i < DH / 16; ++i) q[i][h] = q[i][2 + h] = 0u;
                 continue;
             }
-            const int tr = r8 + 8 * h, row = p.rt * kRows + tr;
+            const int tr = r8 + 8 * h, row = p.rt * a.rows + tr;
             uint32_t raw[DH / 8];
 #pragma unroll
             for (int i = 0; i < DH / 8; ++i) raw[i] = 0u;
@@ -744,7 +744,7 @@ __global__ void __launch_bounds__(Few8Cfg<DH, HALF>::THREADS, 1) k_attn8_few(con
         if (p.nt == p.all) {
 #pragma unroll
             for (int h = 0; h < RH; ++h) {
-                const int tr = r8 + 8 * h, row = p.rt * kRows + tr;
+                const int tr = r8 + 8 * h, row = p.rt * a.rows + tr;
                 if (tr >= p.rows) continue;
                 const int tok = row / a.group, head = p.g * a.group + row - tok * a.group;
                 T* const dst = static_cast<T*>(a.out) + (long long)(p.cu + tok) * a.o_stride + (long long)head * DH + 2 * q4 * (DH / 8);
@@ -782,7 +782,7 @@ __global__ void __launch_bounds__(Few8Cfg<DH, HALF>::THREADS, 1) k_attn8_few(con
 
     // ---- items that warps of this block share: each of them takes its share of the chunks
     auto write = [&](const Piece8& p, int c, float4 v, const float (&inv)[2]) {
-        const int h = c / (DH / 16), e = c / (DH / 32) % 2, tr = r8 + 8 * h, row = p.rt * kRows + tr;
+        const int h = c / (DH / 16), e = c / (DH / 32) % 2, tr = r8 + 8 * h, row = p.rt * a.rows + tr;
         if (tr >= p.rows) return;
         const int tok = row / a.group, head = p.g * a.group + row - tok * a.group;
         const float f = inv[h];
@@ -793,7 +793,7 @@ __global__ void __launch_bounds__(Few8Cfg<DH, HALF>::THREADS, 1) k_attn8_few(con
         if (a.lse == nullptr || q4 != 0) return;
 #pragma unroll
         for (int h = 0; h < RH; ++h) {
-            const int tr = r8 + 8 * h, row = p.rt * kRows + tr;
+            const int tr = r8 + 8 * h, row = p.rt * a.rows + tr;
             if (tr >= p.rows) continue;
             const int tok = row / a.group, head = p.g * a.group + row - tok * a.group;
             a.lse[(long long)(p.cu + tok) * a.heads + head] = log_sum(m[h], l[h]);
@@ -935,9 +935,9 @@ __global__ void __launch_bounds__(Few8Cfg<DH, HALF>::THREADS, 1) k_attn8_few(con
 
 // ------------------------------------------------ pages of long requests in 16 bits
 //
-// A unit is one KV head of one page that a request of many rows sees; a block
-// takes a contiguous range of units.  Page p of the cache is page p of the copy.
-constexpr int kWidenThreads = 256;
+// A unit is one KV head of one page that a request of many rows sees; a warp takes a
+// contiguous range of units.  Page p of the cache is page p of the copy.
+constexpr int kWidenThreads = 256, kWidenBlocks = 4;   // of a block; blocks of an SM
 
 struct Widen8Args {
     Cache8 c;
@@ -980,63 +980,59 @@ PI_DEV void put_wide(__nv_bfloat16* p, const uint2& c, float scale) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kWidenThreads) k_widen8(const __grid_constant__ Widen8Args a) {
+__global__ void __launch_bounds__(kWidenThreads, kWidenBlocks) k_widen8(const __grid_constant__ Widen8Args a) {
     pdl_entry();
-    __shared__ long long scratch[kWidenThreads / 32 + 1];
-    __shared__ int at_b, at_page, at_head;
-    const int tid = threadIdx.x;
+    __shared__ long long scratch[kWidenThreads / 32 + 1], before[kWidenThreads];
+    const int tid = threadIdx.x, lane = tid & 31;
     const int per = (a.batch + kWidenThreads - 1) / kWidenThreads, b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
     long long own = 0, U = 0;
     bool bad = false;
     int first;
     for (int b = b0; b < b1; ++b) own += (long long)a.c.kv_heads * seen_pages(a, request8(a, b, &bad), &first);
-    const long long pre = scan_before<kWidenThreads>(own, scratch, &U);
-    const long long u0 = U * blockIdx.x / gridDim.x, u1 = U * (blockIdx.x + 1) / gridDim.x;
+    before[tid] = scan_before<kWidenThreads>(own, scratch, &U);
+    __syncthreads();
+    const long long warps = (long long)gridDim.x * (kWidenThreads / 32), w = (long long)blockIdx.x * (kWidenThreads / 32) + (tid >> 5);
+    const long long u0 = quotient(U * w, warps), u1 = quotient(U * (w + 1), warps);
     if (u0 >= u1) return;
-    if (tid == 0) at_b = a.batch;
-    __syncthreads();
-    if (pre <= u0 && u0 < pre + own) {
-        long long left = u0 - pre;
-        for (int b = b0; b < b1; ++b) {
-            const long long u = (long long)a.c.kv_heads * seen_pages(a, request8(a, b, &bad), &first);
-            if (left < u) {
-                at_page = (int)(left / a.c.kv_heads);
-                at_head = (int)(left % a.c.kv_heads);
-                at_b = b;
-                break;
-            }
-            left -= u;
-        }
+    // where the range starts: the last thread whose requests' units start at or before u0, then its requests
+    int t = 0;
+    for (int d = kWidenThreads / 2; d > 0; d >>= 1)
+        if (before[t + d] <= u0) t += d;
+    int b = min(t * per, a.batch), count = 0;
+    long long left = u0 - before[t];
+    for (; b < a.batch; ++b) {
+        count = seen_pages(a, request8(a, b, &bad), &first);
+        if (left < (long long)a.c.kv_heads * count) break;
+        left -= (long long)a.c.kv_heads * count;
     }
-    __syncthreads();
-    int b = at_b, page = at_page, head = at_head;
     if (b >= a.batch) return;   // (the lengths changed under the kernel)
+    int page = (int)quotient(left, a.c.kv_heads), head = (int)(left - (long long)page * a.c.kv_heads);
     const int pos_shift = a.dh == 128 ? 4 : 3, chunks = 1 << (pos_shift + a.c.page_shift);   // pieces of 8 codes: of a position, of a head
-    int count = seen_pages(a, request8(a, b, &bad), &first);
+    int id = -1, at = -1;        // page of the cache, and the column it was looked up for
     for (long long u = u0; u < u1; ++u) {
         const int col = first + page;
-        const int id = col < a.max_pages ? a.table[(size_t)b * a.max_pages + col] : -1;
+        if (col != at) {
+            id = col < a.max_pages ? a.table[(size_t)b * a.max_pages + col] : -1;
+            at = col;
+        }
         if (id >= 0 && id < a.c.num_pages) {   // (others read as zeros and are reported by the attention)
             const long long src = id * a.c.page_stride + head * a.c.head_stride;
             const long long ex = ((long long)id * a.c.kv_heads + head) << (a.c.page_shift - 4);
             const long long dst = ((long long)id * a.c.kv_heads + head) * ((long long)a.dh << a.c.page_shift);
-            // (2 chunks is 256 or more)
-            for (int i0 = tid; i0 < 2 * chunks; i0 += 4 * kWidenThreads) {
-                uint2 y[4];
-                int e[4];
+            for (int i0 = lane; i0 < 2 * chunks; i0 += 8 * 32) {   // (2 chunks is a multiple of 256)
+                uint2 y[8];
+                int e[8];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int i = min(i0 + j * kWidenThreads, 2 * chunks - 1);
+                for (int j = 0; j < 8; ++j) {
+                    const int i = i0 + 32 * j, x = i & (chunks - 1), pos = x >> pos_shift, c = x & ((1 << pos_shift) - 1);
                     const bool values = i >= chunks;
-                    const int x = i & (chunks - 1), pos = x >> pos_shift, c = x & ((1 << pos_shift) - 1);
                     y[j] = ld_stream8((values ? a.c.v : a.c.k) + src + pos * a.c.token_stride + c * 8);
                     e[j] = (values ? a.c.ve : a.c.ke)[ex + pos / kBlock];
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int i = i0 + j * kWidenThreads;
-                    if (i < 2 * chunks)
-                        put_wide(static_cast<T*>(i >= chunks ? a.v : a.k) + dst + (long long)(i & (chunks - 1)) * 8, y[j], pow2(bounded(e[j])));
+                for (int j = 0; j < 8; ++j) {
+                    const int i = i0 + 32 * j;
+                    put_wide(static_cast<T*>(i >= chunks ? a.v : a.k) + dst + (long long)(i & (chunks - 1)) * 8, y[j], pow2(bounded(e[j])));
                 }
             }
         }
@@ -1044,6 +1040,7 @@ __global__ void __launch_bounds__(kWidenThreads) k_widen8(const __grid_constant_
             head = 0;
             if (++page >= count) {
                 page = 0;
+                at = -1;
                 do {
                     if (++b >= a.batch) return;
                     count = seen_pages(a, request8(a, b, &bad), &first);
@@ -1097,8 +1094,12 @@ bool codes_maps(Few8Args* a, const void* k, const void* v, const pi_page8_desc& 
                    : codes_map(&a->kmap, k, c, 1, 16) && codes_map(&a->vmap, v, c, 1, 16);
 }
 
-// tokens up to which a request goes through k_attn8_few
-int few_tokens(int group) { return std::max(1, kFewRows / group); }
+// Whether a step may hold requests for the 16-bit kernel, and the tokens up to which one goes
+// through k_attn8_few: 64 rows (or a token) where all requests are that short, else 8, so that
+// decode steps beside prompts take the 8-row items (16 sequences that decode or take 100-700
+// tokens 177 us so, 186 with items of 16 rows for up to 64).
+bool has_long(int max_new, int group) { return max_new > std::max(1, kFewRows / group); }
+int few_tokens(int max_new, int group) { return std::max(1, (has_long(max_new, group) ? 8 : kFewRows) / group); }
 
 // The copy's description: [pages, heads, positions, elements].
 pi_page_desc wide_desc(const pi_page8_desc& c, int dtype) {
@@ -1120,7 +1121,7 @@ struct Layout8 {
         wide = up(warps + blocks * kMostWarps * 2 * item);
         k = v = total = wide;
         wide_bytes = 0;
-        if (d.max_new > few_tokens(d.heads / c.kv_heads)) {
+        if (has_long(d.max_new, d.heads / c.kv_heads)) {
             const pi_page_desc w = wide_desc(c, PI_T_F16);
             wide_bytes = pi_paged_workspace_bytes(&d, &w);
             const size_t pages = up((size_t)c.num_pages * w.page_stride * 2);
@@ -1209,7 +1210,9 @@ pi_status pi_paged_attn8(const pi_paged_desc* desc, const pi_page8_desc* cache, 
     // sums with first positions (down to -2^24) stay far from the ends of int
     a.window = (long long)desc->window >= (long long)desc->max_pages * cache->page_size ? 0 : desc->window;
     a.group = desc->heads / cache->kv_heads;
-    a.few = few_tokens(a.group);
+    a.few = few_tokens(desc->max_new, a.group);
+    const bool half = std::min(desc->max_new, a.few) * a.group <= 8;   // no item has more than 8 rows
+    a.rows = half ? 8 : 16;
     a.scale = desc->scale > 0.f ? desc->scale : 1.0f / sqrtf((float)cache->head_dim);
     a.counters = reinterpret_cast<int*>(ws);
     a.part_ml = reinterpret_cast<float*>(ws + lay.ml);
@@ -1219,16 +1222,15 @@ pi_status pi_paged_attn8(const pi_paged_desc* desc, const pi_page8_desc* cache, 
     a.timeout_ns = wait_timeout_ns();
     if (sms < 1 || a.status == nullptr || !codes_maps(&a, kcache, vcache, *cache)) return PI_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const bool half = std::min(desc->max_new, a.few) * a.group <= 8;   // no item has more than 8 rows
     const bool f16 = dtype == PI_T_F16;
     cudaError_t e = f16 ? launch_few<__half>(a, cache->head_dim, half, sms, s)
                         : launch_few<__nv_bfloat16>(a, cache->head_dim, half, sms, s);
     if (e != cudaSuccess) return PI_ERR_CUDA;
-    if (desc->max_new <= a.few) return PI_OK;
+    if (!has_long(desc->max_new, a.group)) return PI_OK;
     Widen8Args w{a.c, block_table, cu_new, kv_len, ws + lay.k, ws + lay.v, desc->batch, desc->max_tokens, desc->max_new,
                  desc->max_pages, a.window, a.few, cache->head_dim, a.status};
-    e = f16 ? launch_pdl(k_widen8<__half>, 4 * sms, kWidenThreads, 0, s, w)
-            : launch_pdl(k_widen8<__nv_bfloat16>, 4 * sms, kWidenThreads, 0, s, w);
+    e = f16 ? launch_pdl(k_widen8<__half>, kWidenBlocks * sms, kWidenThreads, 0, s, w)
+            : launch_pdl(k_widen8<__nv_bfloat16>, kWidenBlocks * sms, kWidenThreads, 0, s, w);
     if (e != cudaSuccess) return PI_ERR_CUDA;
     const pi_page_desc wide = wide_desc(*cache, dtype);
     return paged_attn(desc, &wide, q, q_stride, w.k, w.v, block_table, cu_new, kv_len, out, out_stride, lse, ws + lay.wide,
