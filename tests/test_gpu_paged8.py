@@ -674,3 +674,167 @@ def test_the_command_serves_with_eight_bits(P, capsys):
     from activation_sparse_ffn_layer_gb300 import paged
     paged.main(["--config", "c4", "--requests", "3", "--prompt", "50", "--chunk", "20", "--tokens", "4", "--layers", "2", "--bits", "8"])
     assert "decode steps" in capsys.readouterr().out
+
+
+# ------------------------------------------------------------------ wide batches, layouts, limits
+
+@pytest.mark.parametrize("B,long", [(700, 0), (4096, 0), (600, 5)])
+def test_attention_of_many_requests(P, B, long):
+    """More requests than threads of a block, most of one token, some without tokens, some (`long`) of 80."""
+    rng = random.Random(B)
+    H, G, dh, page = 2, 2, 64, 16
+    n = [rng.choice((1, 1, 1, 0)) for _ in range(B)]
+    for i in range(long):
+        n[rng.randrange(B)] = 80
+    kv = [x + rng.randint(0, 40) if x else 0 for x in n]
+    check(P, H, G, dh, F16, page, "hnd", n, kv, seed=B, extra=1)
+
+
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("how", ["keys first", "values first", "one array", "far apart"])
+def test_attention_where_the_arrays_lie(P, page, dh, how):
+    """Keys below values in memory, above them, the same array for both, and two arrays far from one another."""
+    G, H, kv = 2, 8, [300, 45]
+    used = sum(-(-x // page) for x in kv)
+    a, ea = quantised(used, G, page, dh, "hnd", 1)
+    b, eb = quantised(used, G, page, dh, "hnd", 2)
+    if how in ("keys first", "values first"):
+        both = torch.empty(2, *a.shape, dtype=torch.uint8, device="cuda")
+        i = 0 if how == "keys first" else 1
+        both[i], both[1 - i] = a.view(torch.uint8), b.view(torch.uint8)
+        kc, vc = both[i].view(R.CODE), both[1 - i].view(R.CODE)
+        assert (kc.data_ptr() < vc.data_ptr()) == (i == 0)
+    elif how == "one array":
+        kc, vc = a, a
+    else:
+        spacer = torch.empty(3 << 30, dtype=torch.uint8, device="cuda")
+        kc, vc = a.view(torch.uint8).clone().view(R.CODE), b
+        del spacer
+    q = torch.randn(2, H, dh, device="cuda").half()
+    table = tables(kv, page, used, 1)
+    out, lse = attn(P, q, kc, ea, vc, eb, table, [0, 1, 2], kv)
+    want, wl, tol, ltol = R.attention(q, kc, ea, vc, eb, i32(table), [0, 1, 2], kv)
+    R16.check(out, want, tol, "out")
+    R16.check(lse, wl, ltol, "lse")
+    assert P.pi_last_device_status() == 0
+
+
+@pytest.mark.parametrize("page", [16, 32, 128])
+def test_attention_behind_a_window_whose_pages_are_gone(P, page):
+    """Table entries of positions that no token sees any more are not looked at."""
+    G, H, dh, kv, window = 2, 8, 64, 1000, 75
+    used = -(-kv // page)
+    kc, ke = quantised(used, G, page, dh, "hnd", 1)
+    vc, ve = quantised(used, G, page, dh, "hnd", 2)
+    table = tables([kv], page, used, 2)
+    for n in (1, 4, 90):
+        q = torch.randn(n, H, dh, device="cuda").to(BF16)
+        want, wl, tol, ltol = R.attention(q, kc, ke, vc, ve, i32(table), [0, n], [kv], window)
+        gone = [list(table[0])]
+        for j in range((kv - n - window + 1) // page):
+            gone[0][j] = -1
+        out, lse = attn(P, q, kc, ke, vc, ve, gone, [0, n], [kv], window)
+        assert P.pi_last_device_status() == 0
+        R16.check(out, want, tol, f"{n}")
+        R16.check(lse, wl, ltol, f"{n}")
+
+
+@pytest.mark.parametrize("n,kv,H,G", [([1] * 6, [30000, 20000, 300, 25000, 17, 30000], 64, 8), ([4] * 3, [30000, 8000, 30000], 64, 8),
+                                      ([300, 1], [4000, 2000], 4, 2)])
+def test_attention_whose_waits_run_out(P, n, kv, H, G):
+    """With a wait limit of 1 ns a wait that is not satisfied at its first tries gives up: the warps wait for their own
+    copies and return, and the status is PI_ERR_TIMEOUT.  The kernel of few rows waits for nothing but copies that it has
+    asked for, and a try lasts longer than those, so that its waits end well; the 16-bit kernel's, in a step with a long
+    request, run out.  After a zero fill of the workspace the same call gives the bits of a clean run."""
+    dh, page = 128, 16
+    used = sum(-(-x // page) for x in kv)
+    kc, ke = quantised(used, G, page, dh, "hnd", 1)
+    vc, ve = quantised(used, G, page, dh, "hnd", 2)
+    q = torch.randn(sum(n), H, dh, device="cuda").half()
+    table, cu = tables(kv, page, used, 1), starts(n)
+    d = P.paged_desc(H, len(kv), sum(n), max(n), len(table[0]))
+    ws = torch.zeros(P.pi_paged8_workspace_bytes(d, P.page8_desc(kc, vc)), dtype=torch.uint8, device="cuda")
+    want = attn(P, q, kc, ke, vc, ve, table, cu, kv, ws=ws)
+    assert P.pi_last_device_status() == 0
+    seen = []
+    for limit in (1, 1, 1, 1, 3000):
+        P.pi_debug_set_wait_timeout(limit)
+        try:
+            attn(P, q, kc, ke, vc, ve, table, cu, kv, ws=ws)
+            torch.cuda.synchronize()
+        finally:
+            P.pi_debug_set_wait_timeout(0)
+        seen.append(P.pi_last_device_status())
+        ws.zero_()
+        for _ in range(3):
+            got = attn(P, q, kc, ke, vc, ve, table, cu, kv, ws=ws)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert P.pi_last_device_status() == 0
+    assert set(seen) <= {0, 4} and (4 in seen or max(n) < 64)
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_steps_of_many_shapes_on_one_workspace(P, seed):
+    """Decodes, proposals, chunks and empty rows, cut anywhere by the blocks' and warps' borders, one step after the
+    other on one workspace that is filled with zeros only once."""
+    r = random.Random(100 + seed)
+    ws = torch.zeros(1 << 28, dtype=torch.uint8, device="cuda")
+    for _ in range(4):
+        H, G = r.choice([(4, 4), (8, 2), (16, 1), (64, 8), (24, 8)])
+        dh, dt, page, window = r.choice([64, 128]), r.choice([F16, BF16]), r.choice([16, 32, 128]), r.choice([0, 0, 1, 300])
+        n, kv = [], []
+        for _ in range(r.choice([1, 2, 5, 40])):
+            n.append(r.choice([0, 1, 1, 1, r.randint(2, 12), r.randint(30, 200)]))
+            kv.append(n[-1] + r.choice([0, r.randint(0, 100), r.randint(100, 1500)]))
+        if not any(n):
+            n.append(1), kv.append(700)
+        used = sum(-(-x // page) for x in kv)
+        kc, ke = quantised(used, G, page, dh, r.choice(("hnd", "nhd")), 1)
+        vc, ve = quantised(used, G, page, dh, "hnd" if kc.is_contiguous() else "nhd", 2)
+        q = torch.randn(sum(n), H, dh, device="cuda").to(dt)
+        table, cu = tables(kv, page, used, seed), starts(n)
+        out, lse = attn(P, q, kc, ke, vc, ve, table, cu, kv, window, ws=ws)
+        want, wl, tol, ltol = R.attention(q, kc, ke, vc, ve, i32(table), cu, kv, window)
+        R16.check(out, want, tol, "out")
+        R16.check(lse, wl, ltol, "lse")
+    assert P.pi_last_device_status() == 0
+
+
+@pytest.mark.parametrize("T", [600, 3000])
+def test_store_of_many_single_tokens(P, T):
+    """Steps of many decoding rows (the windows of 1, 4 and 16 tokens): a block each."""
+    G, dh, page = 4, 64, 16
+    kc, ke = make_cache(T, G, page, dh, "nhd", 1)
+    vc, ve = make_cache(T, G, page, dh, "nhd", 2)
+    rng = random.Random(T)
+    ids = list(range(T))
+    rng.shuffle(ids)
+    slots = [i * page + rng.randrange(16) if rng.random() < 0.95 else -1 for i in ids]
+    kv = torch.randn(T, 2 * G, dh, device="cuda").to(BF16) * 8
+    k, v = kv[:, :G].contiguous(), kv[:, G:].contiguous()
+    wk, wv = (kc.view(torch.uint8).clone(), ke.clone()), (vc.view(torch.uint8).clone(), ve.clone())
+    P.pi_rope_store8(P.rope_plan(dh, 0), P.page8_desc(kc, vc), None, k, v, i32([0] * T), torch.tensor(slots, device="cuda"),
+                     None, kc, vc, ke, ve)
+    for (c, e), x in ((wk, k), (wv, v)):
+        store_each(c, e, x.double(), slots, page)
+    assert torch.equal(ke, wk[1]) and torch.equal(ve, wv[1]) and P.pi_last_device_status() == 0
+    same_codes(kc, wk[0])
+    same_codes(vc, wv[0])
+
+
+def store_each(codes, exps, x, slots, page):
+    """R.store for tokens in blocks of their own, all at once (pages of one block)."""
+    keep = torch.tensor([s >= 0 for s in slots], device="cuda")
+    at = torch.tensor(slots, device="cuda")[keep]
+    y = x[keep]
+    e = torch.tensor([[R.exponent(z) for z in row] for row in y.abs().amax(-1).tolist()], device="cuda")
+    p, r = at // page, at % page
+    old = exps[p, :, 0].long()
+    new = torch.where(r[:, None] > 0, torch.maximum(e, old), e)
+    kept = codes[p]                                             # [tokens, heads, page, dh]
+    again = R.encode(R.VALUES.cuda()[kept.long()] * torch.exp2((old - new).double())[..., None, None])
+    stay = torch.arange(page, device="cuda")[None, :] < r[:, None]
+    codes[p] = torch.where(stay[:, None, :, None], again, kept)
+    codes[p, :, r] = R.encode(y / torch.exp2(new.double())[..., None])
+    exps[p, :, 0] = new.to(torch.int8)
