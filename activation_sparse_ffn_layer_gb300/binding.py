@@ -575,22 +575,26 @@ def page8_desc(kcache: torch.Tensor, vcache: torch.Tensor) -> pi_page8_desc:
     if st != [vcache.stride(i) if n > 1 else dh for i, n in enumerate((pages, heads, page))]:
         raise ValueError("expected key and value codes of the same strides")
     d = pi_page8_desc(heads, dh, page, pages, st[0], st[1], st[2])
-    d.like = (CODE8, kcache.shape, kcache.stride())   # what _cache8 compares first
+    # what _cache8 compares first: codes, and the shape of their exponents
+    d.like, d.exps = (CODE8, kcache.shape, kcache.stride()), torch.Size((pages, heads, page // 16))
     return d
 
 
 def _cache8(cache: pi_page8_desc, codes: torch.Tensor, exps: torch.Tensor, name: str) -> Tuple[int, int]:
     """Addresses of the codes and exponents that a page8_desc describes."""
-    if not codes.is_cuda or getattr(cache, "like", None) != (codes.dtype, codes.shape, codes.stride()):
-        if not codes.is_cuda or codes.dtype is not CODE8 or \
+    like = getattr(cache, "like", None)
+    if like is None or (codes.dtype, codes.shape, codes.stride()) != like:
+        if codes.dtype is not CODE8 or \
                 tuple(codes.shape) != (cache.num_pages, cache.kv_heads, cache.page_size, cache.head_dim) or \
                 (codes.shape[0] > 1 and codes.stride(0) != cache.page_stride) or \
                 (codes.shape[1] > 1 and codes.stride(1) != cache.head_stride) or \
                 codes.stride(2) != cache.token_stride or codes.stride(3) != 1:
             raise ValueError(f"{name}: not the codes that the page8_desc describes")
-    if exps.dtype is not torch.int8 or not exps.is_cuda or not exps.is_contiguous() or \
-            exps.shape != (cache.num_pages, cache.kv_heads, cache.page_size // 16):
-        raise ValueError(f"{name}: expected contiguous int8 exponents [pages, kv_heads, page_size / 16] on the GPU")
+    shape = cache.exps if like is not None else (cache.num_pages, cache.kv_heads, cache.page_size // 16)
+    if exps.dtype is not torch.int8 or exps.shape != shape or not exps.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous int8 exponents [pages, kv_heads, page_size / 16]")
+    if not codes.is_cuda or not exps.is_cuda:
+        raise ValueError(f"{name}: expected CUDA tensors")
     return codes.data_ptr(), exps.data_ptr()
 
 

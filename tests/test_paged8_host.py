@@ -146,3 +146,12 @@ def test_binding_refuses_other_tensors(P):
     from activation_sparse_ffn_layer_gb300.paged import PagedCache
     with pytest.raises(ValueError):
         PagedCache(2, 2, 64, 1, 16, 1, 1, bits=4, device="cpu")
+    for wrong in (torch.zeros(4, 2, 1, dtype=torch.uint8), torch.zeros(4, 2, 2, dtype=torch.int8),
+                  torch.zeros(1, 2, 4, dtype=torch.int8).transpose(0, 2)):
+        with pytest.raises(ValueError):
+            P.binding._cache8(d, codes, wrong, "kcache")
+    with pytest.raises(ValueError):                       # other strides than the description's
+        P.binding._cache8(d, torch.zeros(4, 16, 2, 64, dtype=R.CODE).transpose(1, 2), torch.zeros(4, 2, 1, dtype=torch.int8), "kcache")
+    bare = P.binding.pi_page8_desc(2, 64, 16, 4, 2048, 1024, 64)    # made by hand
+    with pytest.raises(ValueError):
+        P.binding._cache8(bare, codes, torch.zeros(4, 2, 2, dtype=torch.int8), "kcache")
