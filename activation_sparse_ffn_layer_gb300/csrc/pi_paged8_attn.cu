@@ -75,6 +75,7 @@ struct Few8Args {
     float* part_ml;    // [blocks][2][16][2]: a block's sums of such items
     float4* part_o;    // [blocks][2][chunks][32]
     float4* warp_o;    // [blocks][warps][2][chunks][32]: a warp's sums of items that warps share
+    void *wide_k, *wide_v;   // [num_pages, kv_heads, page_size, dh] in 16 bits, or null: no long requests
     int* status;
     long long timeout_ns;
 };
@@ -560,20 +561,125 @@ struct Run8 {
 PI_DEV float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
 PI_DEV float log_sum(float m, float l) { return l == 0.f ? -INFINITY : (m - kLift + log2f(l)) * kLn2; }
 
+// ------------------------------------------------ pages of long requests in 16 bits
+//
+// A unit is one KV head of one page that a request of many rows sees; a warp takes a
+// contiguous range of units, once it is done with the items of few rows.  Page p of the
+// cache is page p of the copy.  In a launch of its own this took 3.5 us more of a prompt
+// of 1999 tokens.
+
+// pages of a request that are widened: first and how many
+PI_DEV int seen_pages(const Few8Args& a, const Request8& r, int* first) {
+    const int hi = r.first + r.n, lo = a.window > 0 ? max(0, r.first - a.window + 1) : 0;
+    *first = lo >> a.c.page_shift;
+    if (r.n <= a.few || hi <= lo) return 0;
+    return ((hi + (1 << a.c.page_shift) - 1) >> a.c.page_shift) - *first;
+}
+
+// 8 codes times `scale` in 16 bits (fp16: finite ones past 65504 are that)
+PI_DEV void put_wide(__half* p, const uint2& c, float scale) {
+    const uint32_t w[2] = {c.x, c.y};
+    uint32_t o[4];
+    auto in = [](float x) { return fabsf(x) > 65504.f ? copysignf(65504.f, x) : x; };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 u = values2((w[i / 2] >> (16 * (i & 1))) & 0xffffu);
+        o[i] = half2_of(in(u.x * scale), in(u.y * scale));
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+PI_DEV void put_wide(__nv_bfloat16* p, const uint2& c, float scale) {
+    const uint32_t w[2] = {c.x, c.y};
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 u = values2((w[i / 2] >> (16 * (i & 1))) & 0xffffu);
+        const __nv_bfloat162 y = __floats2bfloat162_rn(u.x * scale, u.y * scale);
+        o[i] = *reinterpret_cast<const uint32_t*>(&y);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <typename T, int DH, int THREADS>
+PI_DEV void widen_pages(const Few8Args& a, long long* scratch, long long* before) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int per = (a.batch + THREADS - 1) / THREADS, b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
+    long long own = 0, U = 0;
+    bool bad = false;
+    int first;
+    for (int b = b0; b < b1; ++b) own += (long long)a.c.kv_heads * seen_pages(a, request8(a, b, &bad), &first);
+    before[tid] = scan_before<THREADS>(own, scratch, &U);
+    __syncthreads();
+    const long long warps = (long long)gridDim.x * (THREADS / 32), w = (long long)blockIdx.x * (THREADS / 32) + (tid >> 5);
+    const long long u0 = quotient(U * w, warps), u1 = quotient(U * (w + 1), warps);
+    if (u0 >= u1) return;
+    // where the range starts: the last thread whose requests' units start at or before u0, then its requests
+    int t = 0;
+    for (int d = 256; d > 0; d >>= 1)
+        if (t + d < THREADS && before[t + d] <= u0) t += d;
+    int b = min(t * per, a.batch), count = 0;
+    long long left = u0 - before[t];
+    for (; b < a.batch; ++b) {
+        count = seen_pages(a, request8(a, b, &bad), &first);
+        if (left < (long long)a.c.kv_heads * count) break;
+        left -= (long long)a.c.kv_heads * count;
+    }
+    if (b >= a.batch) return;   // (the lengths changed under the kernel)
+    int page = (int)quotient(left, a.c.kv_heads), head = (int)(left - (long long)page * a.c.kv_heads);
+    constexpr int POS = DH / 8, N = 16;                // pieces of 8 codes of a position; of a lane in flight
+    const int chunks = POS << a.c.page_shift;          // of a head
+    int id = -1, at = -1;        // page of the cache, and the column it was looked up for
+    for (long long u = u0; u < u1; ++u) {
+        const int col = first + page;
+        if (col != at) {
+            id = col < a.max_pages ? a.table[(size_t)b * a.max_pages + col] : -1;
+            at = col;
+        }
+        if (id >= 0 && id < a.c.num_pages) {   // (others read as zeros and are reported by the attention)
+            const long long src = id * a.c.page_stride + head * a.c.head_stride;
+            const long long ex = ((long long)id * a.c.kv_heads + head) << (a.c.page_shift - 4);
+            const long long dst = ((long long)id * a.c.kv_heads + head) * ((long long)DH << a.c.page_shift);
+            for (int i0 = lane; i0 < 2 * chunks; i0 += N * 32) {
+                uint2 y[N];
+                int e[N];
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const int i = i0 + 32 * j, x = i & (chunks - 1), pos = x / POS, c = x % POS;
+                    if (i >= 2 * chunks) break;
+                    const bool values = i >= chunks;
+                    y[j] = ld_stream8((values ? a.c.v : a.c.k) + src + pos * a.c.token_stride + c * 8);
+                    e[j] = (values ? a.c.ve : a.c.ke)[ex + pos / kBlock];
+                }
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const int i = i0 + 32 * j;
+                    if (i >= 2 * chunks) break;
+                    put_wide(static_cast<T*>(i >= chunks ? a.wide_v : a.wide_k) + dst + (long long)(i & (chunks - 1)) * 8, y[j], pow2(bounded(e[j])));
+                }
+            }
+        }
+        if (++head == a.c.kv_heads) {
+            head = 0;
+            if (++page >= count) {
+                page = 0;
+                at = -1;
+                do {
+                    if (++b >= a.batch) return;
+                    count = seen_pages(a, request8(a, b, &bad), &first);
+                } while (count == 0);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------ items of few rows
 template <typename T, int DH, bool HALF>
-__global__ void __launch_bounds__(Few8Cfg<DH, HALF>::THREADS, 1) k_attn8_few(const __grid_constant__ Few8Args a) {
-    pdl_entry();
+PI_DEV void few_items(const Few8Args& a, Few8Shared<DH, HALF>& sh) {
     using C = Few8Cfg<DH, HALF>;
     constexpr int KC = Slot8<DH>::KC, OC = DH / 8, CHUNKS = C::CHUNKS, RH = HALF ? 1 : 2, STAGES = C::STAGES;
     constexpr int W = C::WARPS, THREADS = C::THREADS;
-    extern __shared__ __align__(1024) unsigned char few_smem[];
-    Few8Shared<DH, HALF>& sh = *reinterpret_cast<Few8Shared<DH, HALF>*>(few_smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q4 = lane & 3, r8 = lane >> 2;
 
-    if ((su32(few_smem) & 1023u) != 0) {   // the copies' swizzle needs it; the whole block leaves
-        if (tid == 0) atomicExch(a.status, (int)PI_ERR_UNSUPPORTED);
-        return;
-    }
     if (lane == 0) {
         for (int i = 0; i < STAGES; ++i) bar_init(&sh.full[warp][i], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -933,121 +1039,19 @@ __global__ void __launch_bounds__(Few8Cfg<DH, HALF>::THREADS, 1) k_attn8_few(con
     }
 }
 
-// ------------------------------------------------ pages of long requests in 16 bits
-//
-// A unit is one KV head of one page that a request of many rows sees; a warp takes a
-// contiguous range of units.  Page p of the cache is page p of the copy.
-constexpr int kWidenThreads = 256, kWidenBlocks = 4;   // of a block; blocks of an SM
-
-struct Widen8Args {
-    Cache8 c;
-    const int32_t *table, *cu, *kv;
-    void *k, *v;       // [num_pages, kv_heads, page_size, dh] in 16 bits
-    int batch, max_tokens, max_new, max_pages, window, few, dh;
-    int* status;
-};
-
-// pages of a request that are widened: first and how many
-PI_DEV int seen_pages(const Widen8Args& a, const Request8& r, int* first) {
-    const int hi = r.first + r.n, lo = a.window > 0 ? max(0, r.first - a.window + 1) : 0;
-    *first = lo >> a.c.page_shift;
-    if (r.n <= a.few || hi <= lo) return 0;
-    return ((hi + (1 << a.c.page_shift) - 1) >> a.c.page_shift) - *first;
-}
-
-// 8 codes times `scale` in 16 bits (fp16: finite ones past 65504 are that)
-PI_DEV void put_wide(__half* p, const uint2& c, float scale) {
-    const uint32_t w[2] = {c.x, c.y};
-    uint32_t o[4];
-    auto in = [](float x) { return fabsf(x) > 65504.f ? copysignf(65504.f, x) : x; };
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 u = values2((w[i / 2] >> (16 * (i & 1))) & 0xffffu);
-        o[i] = half2_of(in(u.x * scale), in(u.y * scale));
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
-}
-PI_DEV void put_wide(__nv_bfloat16* p, const uint2& c, float scale) {
-    const uint32_t w[2] = {c.x, c.y};
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 u = values2((w[i / 2] >> (16 * (i & 1))) & 0xffffu);
-        const __nv_bfloat162 y = __floats2bfloat162_rn(u.x * scale, u.y * scale);
-        o[i] = *reinterpret_cast<const uint32_t*>(&y);
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kWidenThreads, kWidenBlocks) k_widen8(const __grid_constant__ Widen8Args a) {
+template <typename T, int DH, bool HALF>
+__global__ void __launch_bounds__(Few8Cfg<DH, HALF>::THREADS, 1) k_attn8_few(const __grid_constant__ Few8Args a) {
     pdl_entry();
-    __shared__ long long scratch[kWidenThreads / 32 + 1], before[kWidenThreads];
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int per = (a.batch + kWidenThreads - 1) / kWidenThreads, b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
-    long long own = 0, U = 0;
-    bool bad = false;
-    int first;
-    for (int b = b0; b < b1; ++b) own += (long long)a.c.kv_heads * seen_pages(a, request8(a, b, &bad), &first);
-    before[tid] = scan_before<kWidenThreads>(own, scratch, &U);
+    extern __shared__ __align__(1024) unsigned char few_smem[];
+    Few8Shared<DH, HALF>& sh = *reinterpret_cast<Few8Shared<DH, HALF>*>(few_smem);
+    if ((su32(few_smem) & 1023u) != 0) {   // the copies' swizzle needs it; the whole block leaves
+        if (threadIdx.x == 0) atomicExch(a.status, (int)PI_ERR_UNSUPPORTED);
+        return;
+    }
+    few_items<T, DH, HALF>(a, sh);
+    if (a.wide_k == nullptr) return;
     __syncthreads();
-    const long long warps = (long long)gridDim.x * (kWidenThreads / 32), w = (long long)blockIdx.x * (kWidenThreads / 32) + (tid >> 5);
-    const long long u0 = quotient(U * w, warps), u1 = quotient(U * (w + 1), warps);
-    if (u0 >= u1) return;
-    // where the range starts: the last thread whose requests' units start at or before u0, then its requests
-    int t = 0;
-    for (int d = kWidenThreads / 2; d > 0; d >>= 1)
-        if (before[t + d] <= u0) t += d;
-    int b = min(t * per, a.batch), count = 0;
-    long long left = u0 - before[t];
-    for (; b < a.batch; ++b) {
-        count = seen_pages(a, request8(a, b, &bad), &first);
-        if (left < (long long)a.c.kv_heads * count) break;
-        left -= (long long)a.c.kv_heads * count;
-    }
-    if (b >= a.batch) return;   // (the lengths changed under the kernel)
-    int page = (int)quotient(left, a.c.kv_heads), head = (int)(left - (long long)page * a.c.kv_heads);
-    const int pos_shift = a.dh == 128 ? 4 : 3, chunks = 1 << (pos_shift + a.c.page_shift);   // pieces of 8 codes: of a position, of a head
-    int id = -1, at = -1;        // page of the cache, and the column it was looked up for
-    for (long long u = u0; u < u1; ++u) {
-        const int col = first + page;
-        if (col != at) {
-            id = col < a.max_pages ? a.table[(size_t)b * a.max_pages + col] : -1;
-            at = col;
-        }
-        if (id >= 0 && id < a.c.num_pages) {   // (others read as zeros and are reported by the attention)
-            const long long src = id * a.c.page_stride + head * a.c.head_stride;
-            const long long ex = ((long long)id * a.c.kv_heads + head) << (a.c.page_shift - 4);
-            const long long dst = ((long long)id * a.c.kv_heads + head) * ((long long)a.dh << a.c.page_shift);
-            for (int i0 = lane; i0 < 2 * chunks; i0 += 8 * 32) {   // (2 chunks is a multiple of 256)
-                uint2 y[8];
-                int e[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int i = i0 + 32 * j, x = i & (chunks - 1), pos = x >> pos_shift, c = x & ((1 << pos_shift) - 1);
-                    const bool values = i >= chunks;
-                    y[j] = ld_stream8((values ? a.c.v : a.c.k) + src + pos * a.c.token_stride + c * 8);
-                    e[j] = (values ? a.c.ve : a.c.ke)[ex + pos / kBlock];
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int i = i0 + 32 * j;
-                    put_wide(static_cast<T*>(i >= chunks ? a.v : a.k) + dst + (long long)(i & (chunks - 1)) * 8, y[j], pow2(bounded(e[j])));
-                }
-            }
-        }
-        if (++head == a.c.kv_heads) {
-            head = 0;
-            if (++page >= count) {
-                page = 0;
-                at = -1;
-                do {
-                    if (++b >= a.batch) return;
-                    count = seen_pages(a, request8(a, b, &bad), &first);
-                } while (count == 0);
-            }
-        }
-    }
+    widen_pages<T, DH, Few8Cfg<DH, HALF>::THREADS>(a, sh.scratch, sh.before);
 }
 
 // ------------------------------------------------ host
@@ -1223,17 +1227,17 @@ pi_status pi_paged_attn8(const pi_paged_desc* desc, const pi_page8_desc* cache, 
     if (sms < 1 || a.status == nullptr || !codes_maps(&a, kcache, vcache, *cache)) return PI_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool f16 = dtype == PI_T_F16;
-    cudaError_t e = f16 ? launch_few<__half>(a, cache->head_dim, half, sms, s)
-                        : launch_few<__nv_bfloat16>(a, cache->head_dim, half, sms, s);
+    const bool some_long = has_long(desc->max_new, a.group);
+    if (some_long) {
+        a.wide_k = ws + lay.k;
+        a.wide_v = ws + lay.v;
+    }
+    const cudaError_t e = f16 ? launch_few<__half>(a, cache->head_dim, half, sms, s)
+                              : launch_few<__nv_bfloat16>(a, cache->head_dim, half, sms, s);
     if (e != cudaSuccess) return PI_ERR_CUDA;
-    if (!has_long(desc->max_new, a.group)) return PI_OK;
-    Widen8Args w{a.c, block_table, cu_new, kv_len, ws + lay.k, ws + lay.v, desc->batch, desc->max_tokens, desc->max_new,
-                 desc->max_pages, a.window, a.few, cache->head_dim, a.status};
-    e = f16 ? launch_pdl(k_widen8<__half>, kWidenBlocks * sms, kWidenThreads, 0, s, w)
-            : launch_pdl(k_widen8<__nv_bfloat16>, kWidenBlocks * sms, kWidenThreads, 0, s, w);
-    if (e != cudaSuccess) return PI_ERR_CUDA;
+    if (!some_long) return PI_OK;
     const pi_page_desc wide = wide_desc(*cache, dtype);
-    return paged_attn(desc, &wide, q, q_stride, w.k, w.v, block_table, cu_new, kv_len, out, out_stride, lse, ws + lay.wide,
+    return paged_attn(desc, &wide, q, q_stride, a.wide_k, a.wide_v, block_table, cu_new, kv_len, out, out_stride, lse, ws + lay.wide,
                       lay.wide_bytes, a.few, stream);
 }
 
