@@ -38,9 +38,10 @@ constexpr int kWindow = 16;              // tokens of a window at most
 constexpr int kQueryUnits = 2;           // units of a thread whose loads are in flight together
 constexpr int kQueryTokens = 16;         // tokens of a block at most
 // More blocks of queries than this go through pi_rope_store's kernel, in a launch of their
-// own: here they share registers with the keys' and values' blocks, two of which fit an SM
-// (16384 tokens of 64 + 2 x 8 heads, queries alone 84 us so, 160 here; 32 tokens all in one launch 5.4 us, in two 9).
-constexpr int kQueryBlocks = 608;
+// own: here they share registers and shared memory with the keys' and values' blocks, three
+// of which fit an SM.  64 + 2 x 8 heads: 32 tokens 4.4 us in one launch, 7.0 in two; 1024
+// decoding rows 17 and 21, 16384 prompt tokens 145 and 120.
+constexpr int kQueryBlocks = 4096;
 
 struct Store8Args {
     const void *q, *k, *v;
@@ -595,10 +596,12 @@ pi_status pi_rope_store8(const pi_rope_plan* plan, const pi_page8_desc* cache, c
     a.plan = *plan;
     if (a.status == nullptr) return PI_ERR_CUDA;
     // Windows of one token while that many blocks run at once, of 16 where there are many:
-    // tokens of a prompt share blocks of positions, and one in 16 begins one.
+    // tokens of a prompt share blocks of positions, and one in 16 begins one.  Windows of 1, 4
+    // and 16, two blocks a window: 64 decoding rows 4.9, 7.5 and 21 us, 512 12.6, 10.8 and 23,
+    // 4096 68, 58 and 67; eight blocks a window: a chunk of 1999 tokens 73, 42 and 35.
     a.shares = std::max(1, (2 * a.kv_heads + kStoreWarps - 1) / kStoreWarps);
     const long long ones = (long long)d.tokens * a.shares;
-    a.window = ones <= 608 ? 1 : ones <= 8 * 608 ? 4 : kWindow;
+    a.window = ones <= 608 ? 1 : ones <= 8192 ? 4 : kWindow;
     a.kv_blocks = has_kv ? (int)((d.tokens + a.window - 1) / a.window) * a.shares : 0;
     a.q_tokens = has_q ? std::min(kQueryTokens, std::max(1, kQueryUnits * kStoreThreads / (d.heads * (a.dh / 16)))) : 1;
     if (a.heads > 0 && (d.tokens + a.q_tokens - 1) / a.q_tokens > kQueryBlocks) {

@@ -1099,9 +1099,10 @@ bool codes_maps(Few8Args* a, const void* k, const void* v, const pi_page8_desc& 
 }
 
 // Whether a step may hold requests for the 16-bit kernel, and the tokens up to which one goes
-// through k_attn8_few: 64 rows (or a token) where all requests are that short, else 8, so that
-// decode steps beside prompts take the 8-row items (16 sequences that decode or take 100-700
-// tokens 177 us so, 186 with items of 16 rows for up to 64).
+// through k_attn8_few: 64 rows (or a token) where all requests are that short (24 sequences
+// with 64 rows each: 113 us so, 161 over widened pages; with 128 rows 194 and 164), else 8, so
+// that decode steps beside prompts take the 8-row items (16 sequences that decode or take
+// 100-700 tokens 177 us so, 186 with items of 16 rows for up to 64).
 bool has_long(int max_new, int group) { return max_new > std::max(1, kFewRows / group); }
 int few_tokens(int max_new, int group) { return std::max(1, (has_long(max_new, group) ? 8 : kFewRows) / group); }
 
