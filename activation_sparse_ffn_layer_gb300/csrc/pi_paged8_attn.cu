@@ -1,14 +1,15 @@
 // pi_paged8_attn.cu -- causal attention of new tokens over the 8-bit paged cache.
 //
 // Requests of few rows (tokens x query heads of a KV head; decode steps among
-// them) are bound by the bytes of codes, and go through k_attn8_few.  Requests
-// of many rows are bound by products: the pages that they see are widened to 16
-// bits in the workspace once (k_widen8), and the 16-bit cache's kernel takes
-// them from there on the tcgen05 tensor cores.  A step may hold both.
+// them) are bound by the bytes of codes, and k_attn8_few takes them straight from
+// the codes.  Requests of many rows are bound by products: the pages that they
+// see are widened to 16 bits in the workspace once (widen_pages, in the same
+// launch), and the 16-bit cache's kernel takes them from there on the tcgen05
+// tensor cores.  A step may hold both.
 //
-// k_attn8_few: an item is up to 16 rows of one request and KV head (row = token *
-// group + head in the group).  A warp takes 16 keys at a time, one block of the
-// cache, through a ring of its own in shared memory, three steps ahead:
+// k_attn8_few: an item is up to 8 or 16 rows of one request and KV head (row =
+// token * group + head in the group).  A warp takes 32 keys at a time, two blocks
+// of the cache:
 //     S = Q K^T           (codes as fp16, which holds them exactly; fp32 sums)
 //     x = c 2^ek S        (c = scale / ln 2; ek the exponent of the keys' block)
 //     P = 2^(x + ev - m)  (ev the exponent of the values' block)
@@ -19,13 +20,31 @@
 // weights down to 2^-32 of the largest survive the rounding).  A mma.sync
 // fragment wants 2 elements of a row at a time and has the lanes' columns
 // interleaved; which element of a head is which column is free as long as queries
-// and keys, or values and outputs, agree, so a lane takes 16 bytes in a row.
+// and keys, or values and outputs, agree, so a lane takes 16 bytes in a row.  With
+// 8 rows of work for each key the products are a quarter of what mma.sync can do
+// here, and tcgen05 would not pay: its smallest M is 64.
 //
-// Work split: the (item x tile of 64 keys) space is cut into equal contiguous
-// ranges per block, whatever the lengths; the four warps of a block share a
-// piece's keys.  An item cut by a border leaves unnormalised partials (m, l, O)
-// in the workspace, and the block that arrives last adds them in block order
-// (the order is fixed, who does it is not: same bits).
+// Work split: the (item x tile of 32 keys) space is cut into equal contiguous
+// ranges per block and then per warp, whatever the lengths; a warp goes through its
+// range by itself, with a ring of tiles of its own.  Items that warps of a block
+// share are added up once at its end; of an item that blocks share each leaves
+// unnormalised partials (m, l, O) in the workspace, and the block that arrives last
+// adds them in block order (the order is fixed, who does it is not: same bits).
+//
+// Bounds and figures (GB300, 64 query and 8 KV heads of 128 unless said):
+//  - four sequences with 120-131 thousand keys, bf16: 185-204 us, 5.1-5.6 TB/s; the
+//    memory and 10 us of start and joins.  Copies alone take 171 us of 182 (heads first).
+//  - 32 sequences with 500-8000 keys, fp16: 57 us, 4.0 TB/s.  The first tile is there
+//    after 10 us (3 to know the work, then every SM asks for 190 KB at once), the last
+//    after 50 (5.0 TB/s meanwhile), the joins take 8.
+//  - five tokens of each of 24 sequences, 200-6000 keys, bf16: 92 us.  40 rows are three
+//    items, each of which copies the keys from L2: 450 MB, which at the 22 bytes a cycle
+//    of an SM's copies take 70 us.
+//  - one sequence with 1001 keys: 14 us of latency: 3 to know the work, 1.5 for page and
+//    copies each, 1 for a tile, 5 for the two joins.
+//  - requests of many rows add the widening to the 16-bit kernel's time: 4096 tokens behind
+//    12288, 17 us of 1160; a prompt of 1999 (12 heads of 64) 5 of 39; in a mixed step of 16
+//    sequences (32 heads, window of 2000) 38 of 175, 0.92 of the memory's rate.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -51,8 +70,11 @@ using namespace pipe;
 constexpr int kRows = 16;            // rows of an item
 constexpr int kFewRows = 64;         // rows of a request up to which it goes through k_attn8_few (or one token's)
 constexpr int kTile = 32;            // keys of a unit of the work split
-constexpr int kLead = 5;             // units that an item counts besides its tiles
-constexpr int kMinUnits = 4;         // units of a block at least
+// Units that an item counts besides its tiles: of 2, 3, 5 and 8 a mixed step of 16 sequences
+// takes 189, 186, 184 and 181 us, 32 decoding sequences 60.5, 59.2, 59.4 and 59.2, 16 of 32
+// heads 109, 106, 109 and 109.
+constexpr int kLead = 5;
+constexpr int kMinUnits = 4;         // units of a block at least (one sequence with 1001 keys: 8 units 16.4 us, 4 15.7, 2 18.0)
 constexpr float kLift = 7.f;         // log2 of the factor that P, l and O share
 constexpr float kGrow = 8.f;         // growth (log2) of a maximum before m follows
 constexpr float kLn2 = 0.69314718055994531f;
@@ -235,11 +257,11 @@ PI_DEV uint32_t query2(uint32_t w, float, __half) { return w; }
 
 // The codes of a tile of 32 keys, a row a position, 16-byte pieces in the order that the
 // copies' swizzle gives them.  One copy brings keys and values of 32 positions (of 16 where
-// pages hold no more): a copy costs 60 cycles besides 4 for each row of 128 bytes, and with
-// copies of their own for keys and for values, of 16 rows each, 32 decoding sequences' codes
-// come at 5.0 TB/s.  Of the keys of a block a lane uses 8 j + lane / 4, elements 16 q .. and
-// 64 + 16 q .. (q = lane % 4); of the values 2 q, 2 q + 1, 2 q + 8, 2 q + 9, elements
-// (dh / 8) (lane / 4) ..
+// pages hold no more; with copies of their own for keys and for values 32 decoding sequences
+// take 58.4 us, so 57.4).  Plain asynchronous copies by the lanes, 16 bytes each, bring 5.2
+// TB/s at most, and some SMs get a third less than others: 68 us.  Of the keys of a block a
+// lane uses 8 j + lane / 4, elements 16 q .. and 64 + 16 q .. (q = lane % 4); of the values
+// 2 q, 2 q + 1, 2 q + 8, 2 q + 9, elements (dh / 8) (lane / 4) ..
 template <int DH>
 struct Slot8 {
     static constexpr int KC = DH / 64, VW = DH / 32;   // 16-byte pieces of a lane's key, words of its value
@@ -269,7 +291,8 @@ struct Slot8 {
     }
 };
 
-// Warps of a block, one block on an SM: what registers leave room for.
+// Warps of a block, one block on an SM: what registers leave room for.  (Items of 8 rows for
+// 24 x 40 rows: 116 us, of 16 rows 92; items of 16 on 12 warps, which spill: 97.)
 template <int DH, bool HALF>
 struct Few8Cfg {
     static constexpr int WARPS = HALF ? 12 : 8, THREADS = 32 * WARPS;
@@ -565,8 +588,8 @@ PI_DEV float log_sum(float m, float l) { return l == 0.f ? -INFINITY : (m - kLif
 //
 // A unit is one KV head of one page that a request of many rows sees; a warp takes a
 // contiguous range of units, once it is done with the items of few rows.  Page p of the
-// cache is page p of the copy.  In a launch of its own this took 3.5 us more of a prompt
-// of 1999 tokens.
+// cache is page p of the copy.  (In a launch of its own: a prompt of 1999 tokens 41.9 us a
+// call, so 38.8.)
 
 // pages of a request that are widened: first and how many
 PI_DEV int seen_pages(const Few8Args& a, const Request8& r, int* first) {

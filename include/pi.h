@@ -597,9 +597,14 @@ PI_API size_t pi_paged8_workspace_bytes(const pi_paged_desc *desc, const pi_page
  * ids are as for pi_paged_attn; a NaN in the cache reaches the tokens that see
  * it and no others.  The result does not depend on timing (bitwise
  * reproducible on one device).
+ *   Requests of more than 64 / (heads / kv_heads) tokens go over a 16-bit copy
+ * of the pages they see, made in the workspace by the call (c 2^e rounded to
+ * `dtype`, fp16 values past 65504 as that); a descriptor whose max_new allows
+ * them needs room for one of the whole cache, twice its bytes.  fp16 outputs that
+ * would round past 65504 are 65504.
  * workspace: pi_paged8_workspace_bytes, 16-byte aligned, zero-filled before its
  * first use (and again after a PI_ERR_TIMEOUT); one workspace serves any number
- * of layers whose calls are stream-ordered.
+ * of layers whose calls are stream-ordered, and a step of a smaller max_new.
  */
 PI_API pi_status pi_paged_attn8(const pi_paged_desc *desc, const pi_page8_desc *cache, int dtype, const void *q,
                                 long long q_stride, const void *kcache, const void *vcache, const int8_t *kexp,
