@@ -3,7 +3,8 @@
 The compute lives in ``libpi.so`` (hand-written CUDA for sm_103a behind the C
 ABI of ``include/pi.h``); :mod:`.binding` marshals torch CUDA tensors into it,
 :mod:`.runtime` holds layers and workspaces for whole decode steps, and
-:mod:`.paged` block tables and caches for serving over a paged cache.
+:mod:`.paged` block tables and caches for serving over a paged cache, in 16 or
+8 bits.
 """
 from .binding import (PiError, desc_of, layer_desc, lib, library_path, pi_compact,  # noqa: F401
                       pi_debug_set_wait_timeout, pi_debug_wait_timeout, pi_ffn_layer, pi_ffn_stack, pi_last_device_status,

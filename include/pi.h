@@ -597,10 +597,11 @@ PI_API size_t pi_paged8_workspace_bytes(const pi_paged_desc *desc, const pi_page
  * ids are as for pi_paged_attn; a NaN in the cache reaches the tokens that see
  * it and no others.  The result does not depend on timing (bitwise
  * reproducible on one device).
- *   Requests of more than 64 / (heads / kv_heads) tokens go over a 16-bit copy
- * of the pages they see, made in the workspace by the call (c 2^e rounded to
- * `dtype`, fp16 values past 65504 as that); a descriptor whose max_new allows
- * them needs room for one of the whole cache, twice its bytes.  fp16 outputs that
+ *   Where max_new is above 64 / (heads / kv_heads) (and 1), requests of more than
+ * 8 / (heads / kv_heads) tokens (and 1) go over a 16-bit copy of the pages they
+ * see, which the call makes in the workspace (c 2^e rounded to `dtype`, fp16
+ * values past 65504 as that); the workspace of such a descriptor has room for
+ * one of the whole cache, twice its bytes.  fp16 outputs that
  * would round past 65504 are 65504.
  * workspace: pi_paged8_workspace_bytes, 16-byte aligned, zero-filled before its
  * first use (and again after a PI_ERR_TIMEOUT); one workspace serves any number
