@@ -864,6 +864,7 @@ PI_DEV void few_items(const Few8Args& a, Few8Shared<DH, HALF>& sh) {
 
         // the next piece's first blocks are on their way while this one is put away
         run.start(a, sh.piece[warp][(n + 1) & 1], sh);
+        __syncwarp();   // (every lane has its copy of this piece)
         if (lane == 0) sh.piece[warp][n & 1] = sh.walk[warp].next(a);   // the piece after the next
 #pragma unroll
         for (int h = 0; h < RH; ++h) {
@@ -889,7 +890,8 @@ PI_DEV void few_items(const Few8Args& a, Few8Shared<DH, HALF>& sh) {
             const int slot = p.from == 0;   // a warp begins at most one piece that it does not end
             // the last piece's sums stay in the ring, which holds nothing any more
             static_assert(CHUNKS * 32 * sizeof(float4) <= sizeof(sh.ring[0]), "a ring holds a piece's sums");
-            const bool stays = run.tiles == 0;
+            // (an item of no keys asks for nothing either, but others may follow it)
+            const bool stays = sh.piece[warp][(n + 1) & 1].nt == 0;
             float4* const po = (stays ? reinterpret_cast<float4*>(&sh.ring[warp][0]) : a.warp_o + (((size_t)blockIdx.x * W + warp) * 2 + slot) * CHUNKS * 32) + lane;
 #pragma unroll
             for (int h = 0; h < RH; ++h) {

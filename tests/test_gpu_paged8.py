@@ -690,6 +690,17 @@ def test_attention_of_many_requests(P, B, long):
     check(P, H, G, dh, F16, page, "hnd", n, kv, seed=B, extra=1)
 
 
+@pytest.mark.parametrize("H,G,dh", [(8, 2, 64), (32, 2, 128)])
+@pytest.mark.parametrize("gap", [1, 3, 20])
+def test_attention_with_empty_requests_between(P, H, G, dh, gap):
+    """Requests without keys between others: a warp that ends a cut item goes on through them to items with keys."""
+    n, kv = [], []
+    for i in range(40):
+        n += [1] + [1] * gap
+        kv += [37 + 90 * (i * 7 % 23)] + [0] * gap
+    check(P, H, G, dh, F16, 16, "hnd", n, kv, seed=gap)
+
+
 @pytest.mark.parametrize("page", [16, 64])
 @pytest.mark.parametrize("dh", [64, 128])
 @pytest.mark.parametrize("how", ["keys first", "values first", "one array", "far apart"])
