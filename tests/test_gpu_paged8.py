@@ -849,3 +849,44 @@ def store_each(codes, exps, x, slots, page):
     codes[p] = torch.where(stay[:, None, :, None], again, kept)
     codes[p, :, r] = R.encode(y / torch.exp2(new.double())[..., None])
     exps[p, :, 0] = new.to(torch.int8)
+
+
+def test_caches_past_32_bits(P):
+    """Pages whose codes lie more than 2^32 bytes behind the start: stored, read back and attended to (few rows and many)
+    as in a small cache, with the same lengths and so the same bits."""
+    G, H, dh, page, pages = 8, 16, 128, 64, 66000
+    used, kv, n = 20, [700, 420], [1, 1]
+    far = [pages - 1 - 7 * i for i in range(used)]
+    assert min(far) * G * page * dh > 1 << 32
+    small = [torch.zeros(used, G, page, dh, dtype=torch.uint8, device="cuda").view(R.CODE) for _ in range(2)]
+    big = [torch.zeros(pages, G, page, dh, dtype=torch.uint8, device="cuda").view(R.CODE) for _ in range(2)]
+    ex = [torch.zeros(used, G, page // 16, dtype=torch.int8, device="cuda") for _ in range(2)]
+    bex = [torch.zeros(pages, G, page // 16, dtype=torch.int8, device="cuda") for _ in range(2)]
+    table = tables(kv, page, used, 5)
+    ftable = [[far[x] if x >= 0 else -1 for x in r] for r in table]
+    torch.manual_seed(2)
+    T = sum(kv)
+    x = torch.randn(T, (H + 2 * G) * dh, device="cuda").to(BF16)
+    q, k, v = (y.unflatten(1, (-1, dh)) for y in x.split([H * dh, G * dh, G * dh], dim=1))
+    pos = [p for c in kv for p in range(c)]
+    res = []
+    for (kc, vc), (ke, ve), tb in ((small, ex, table), (big, bex, ftable)):
+        slots = torch.tensor([tb[b][p // page] * page + p % page for b, c in enumerate(kv) for p in range(c)], device="cuda")
+        qo = torch.empty(T, H, dh, dtype=BF16, device="cuda")
+        P.pi_rope_store8(P.rope_plan(dh), P.page8_desc(kc, vc), q, k, v, i32(pos), slots, qo, kc, vc, ke, ve)
+        ko, vo = (torch.empty(T, G, dh, dtype=BF16, device="cuda") for _ in range(2))
+        P.pi_page_read8(P.read8_desc(2, len(tb[0]), T), P.page8_desc(kc, vc), kc, vc, ke, ve, i32(tb), None, i32(starts(kv)), ko, vo)
+        out = [qo, ko, vo]
+        for m in (n, [90, 300]):
+            out += attn(P, q[:sum(m)], kc, ke, vc, ve, tb, starts(m), kv)
+        res.append(out)
+    for a, b in zip(*res):
+        assert torch.equal(a, b)
+    assert P.pi_last_device_status() == 0 and float(res[0][2].float().std()) > 0.5
+
+
+@pytest.mark.parametrize("dh,H,G", [(64, 1, 1), (128, 128, 1), (128, 1024, 8), (64, 1024, 1024)])
+def test_the_ends_of_the_head_counts(P, dh, H, G):
+    """One head, the largest groups and the most heads, few rows and a long request."""
+    check(P, H, G, dh, F16, 16, "nhd", [1, 2], [33, 20], seed=dh)
+    check(P, H, G, dh, BF16, 16, "hnd", [70], [75], seed=dh + 1)
