@@ -18,7 +18,7 @@ VALUES = torch.tensor([(-1.0 if c & 128 else 1.0) * (math.nan if c & 127 == 127 
 def encode(y):
     """Codes (uint8) of 64-bit values: the nearest magnitude, ties to the even code; not finite: NaN (0x7f)."""
     grid = VALUES[:127].to(y.device)
-    m = y.abs().clamp(max=448.0).nan_to_num(0.0)
+    m = y.abs().clamp(max=448.0).nan_to_num(0.0).contiguous()
     hi = torch.searchsorted(grid, m).clamp(1, 126)          # grid[hi - 1] < m <= grid[hi]
     lo = hi - 1
     up, down = grid[hi] - m, m - grid[lo]
