@@ -245,10 +245,12 @@ bool rows_overlap(const void* a, long long a_stride, long long a_width, const vo
                   long long b_width, long long n);
 
 // pi_paged_attn for the requests of more than `few` tokens; the others' rows are left alone.
+// counters: kPagedArrivals for each block (SM), zeros between calls; null: at the workspace's start.
+constexpr int kPagedArrivals = 8;
 pi_status paged_attn(const pi_paged_desc* desc, const pi_page_desc* cache, const void* q, long long q_stride,
                      const void* kcache, const void* vcache, const int32_t* block_table, const int32_t* cu_new,
                      const int32_t* kv_len, void* out, long long out_stride, float* lse, void* workspace,
-                     size_t ws_bytes, int few, void* stream);
+                     size_t ws_bytes, int* counters, int few, void* stream);
 
 // Checks of a paged cache's description (sizes, strides, type).
 bool page_desc_ok(const pi_page_desc& c);

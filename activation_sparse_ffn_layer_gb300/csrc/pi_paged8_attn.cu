@@ -1137,15 +1137,17 @@ pi_page_desc wide_desc(const pi_page8_desc& c, int dtype) {
                         (long long)c.page_size * c.head_dim, c.head_dim};
 }
 
-// Workspace: arrival counters at offset 0 (the same place for every descriptor),
-// the partials of two items per block and per warp; for steps with long requests the 16-bit
-// attention's workspace and the copies of the caches' pages.
+// Workspace: the arrival counters of both kernels first, in the same place for every descriptor
+// (they have to be zeros between calls, and what lies behind them goes by head width, max_new
+// and pages); then the partials of two items per block and per warp; for steps with long requests
+// the 16-bit attention's workspace and the copies of the caches' pages.
 struct Layout8 {
-    size_t ml, o, warps, wide, wide_bytes, k, v, total;
+    size_t arrivals, ml, o, warps, wide, wide_bytes, k, v, total;
     Layout8(const pi_paged_desc& d, const pi_page8_desc& c, int sms) {
         auto up = [](size_t v) { return (v + 255) / 256 * 256; };
         const size_t blocks = std::max(1, sms), item = (size_t)kRows * c.head_dim * sizeof(float);
-        ml = up(blocks * sizeof(int));
+        arrivals = up(blocks * sizeof(int));
+        ml = up(arrivals + blocks * kPagedArrivals * sizeof(int));
         o = up(ml + blocks * 2 * kRows * sizeof(float2));
         warps = up(o + blocks * 2 * item);
         wide = up(warps + blocks * kMostWarps * 2 * item);
@@ -1264,7 +1266,7 @@ pi_status pi_paged_attn8(const pi_paged_desc* desc, const pi_page8_desc* cache, 
     if (!some_long) return PI_OK;
     const pi_page_desc wide = wide_desc(*cache, dtype);
     return paged_attn(desc, &wide, q, q_stride, a.wide_k, a.wide_v, block_table, cu_new, kv_len, out, out_stride, lse, ws + lay.wide,
-                      lay.wide_bytes, a.few, stream);
+                      lay.wide_bytes, reinterpret_cast<int*>(ws + lay.arrivals), a.few, stream);
 }
 
 }  // extern "C"

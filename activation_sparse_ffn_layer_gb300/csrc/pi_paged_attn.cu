@@ -126,7 +126,7 @@ struct PagedArgs {
     int part_rows;            // rows of a partial
     int few;                  // requests of this many tokens or fewer are left alone
     float scale;
-    int* counters;            // [blocks][8] arrivals at a cut item
+    int* counters;            // [blocks][kPagedArrivals] arrivals at a cut item, of a warp each
     float* part_ml;           // [blocks][2][2][part_rows][2]
     float* part_o;            // [blocks][2][DH / 4][part_rows][4]
     int* status;
@@ -950,7 +950,7 @@ PI_DEV void softmax_role(const PagedArgs& a, PagedShared<DH>& sh, unsigned tmem,
             const bool whole = p.parts == 1;
             const int blk = (int)blockIdx.x * 2 + p.own;
             float* po = a.part_o + (size_t)blk * DH * a.part_rows;
-            int* const arrivals = a.counters + p.block0 * 8 + warp;
+            int* const arrivals = a.counters + p.block0 * kPagedArrivals + warp;
             // Of two parts, the one that finds the other there adds the two on the
             // spot (in block order, as join_parts does); where both finish together,
             // the last to arrive does so with its sums still in tensor memory.
@@ -1613,7 +1613,7 @@ struct PagedLayout {
         const int group = d.heads / c.kv_heads, tile_tokens = kTileRows / group;
         rows = d.max_new > tile_tokens ? 2 * kTileRows : (d.max_new * group + 31) / 32 * 32;
         auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-        ml = up((size_t)blocks * 8 * sizeof(int));
+        ml = up((size_t)blocks * kPagedArrivals * sizeof(int));
         o = up(ml + (size_t)blocks * 2 * 2 * rows * 2 * sizeof(float));
         total = up(o + (size_t)blocks * 2 * c.head_dim * rows * sizeof(float));
     }
@@ -1669,7 +1669,7 @@ cudaError_t launch_paged(const PagedArgs& a, int blocks, cudaStream_t s) {
 pi_status paged_attn(const pi_paged_desc* desc, const pi_page_desc* cache, const void* q, long long q_stride,
                      const void* kcache, const void* vcache, const int32_t* block_table, const int32_t* cu_new,
                      const int32_t* kv_len, void* out, long long out_stride, float* lse, void* workspace,
-                     size_t ws_bytes, int few, void* stream) {
+                     size_t ws_bytes, int* counters, int few, void* stream) {
     if (!desc || !cache || !paged_ok(*desc, *cache)) return PI_ERR_INVALID_ARG;
     const long long width = (long long)desc->heads * cache->head_dim;
     if (q_stride % 8 != 0 || q_stride < width || out_stride % 8 != 0 || out_stride < width) return PI_ERR_INVALID_ARG;
@@ -1715,7 +1715,7 @@ pi_status paged_attn(const pi_paged_desc* desc, const pi_page_desc* cache, const
     a.part_rows = lay.rows;
     a.few = few;
     a.scale = desc->scale > 0.f ? desc->scale : 1.0f / sqrtf((float)cache->head_dim);
-    a.counters = reinterpret_cast<int*>(ws);
+    a.counters = counters != nullptr ? counters : reinterpret_cast<int*>(ws);
     a.part_ml = reinterpret_cast<float*>(ws + lay.ml);
     a.part_o = reinterpret_cast<float*>(ws + lay.o);
     a.status = status_word();
@@ -1750,7 +1750,7 @@ pi_status pi_paged_attn(const pi_paged_desc* desc, const pi_page_desc* cache, co
                         const int32_t* kv_len, void* out, long long out_stride, float* lse, void* workspace,
                         size_t ws_bytes, void* stream) {
     return paged_attn(desc, cache, q, q_stride, kcache, vcache, block_table, cu_new, kv_len, out, out_stride, lse, workspace,
-                      ws_bytes, 0, stream);
+                      ws_bytes, nullptr, 0, stream);
 }
 
 }  // extern "C"

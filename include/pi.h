@@ -605,7 +605,8 @@ PI_API size_t pi_paged8_workspace_bytes(const pi_paged_desc *desc, const pi_page
  * would round past 65504 are 65504.
  * workspace: pi_paged8_workspace_bytes, 16-byte aligned, zero-filled before its
  * first use (and again after a PI_ERR_TIMEOUT); one workspace serves any number
- * of layers whose calls are stream-ordered, and a step of a smaller max_new.
+ * of calls that are stream-ordered, whatever their descriptors, where it has the
+ * bytes of each.
  */
 PI_API pi_status pi_paged_attn8(const pi_paged_desc *desc, const pi_page8_desc *cache, int dtype, const void *q,
                                 long long q_stride, const void *kcache, const void *vcache, const int8_t *kexp,

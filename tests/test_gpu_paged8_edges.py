@@ -1,0 +1,39 @@
+"""The 8-bit paged cache at its edges: workspaces that heads of both widths share."""
+import random
+
+import pytest
+import torch
+
+from tests import paged8_ref as R
+from tests import paged_ref as R16
+from tests.test_gpu_paged8 import BF16, F16, P, attn, i32, quantised, starts, tables  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ one workspace for heads of both widths
+
+@pytest.mark.parametrize("dt", [F16, BF16])
+def test_heads_of_both_widths_on_one_workspace(P, dt):
+    """Prompts, chunks and decode steps with heads of 64 and of 128 in turn on one workspace that is filled with zeros
+    once: items that many blocks share in each, copies of pages and partials over most of the workspace between them."""
+    r = random.Random(1)
+    wide64 = (16, 8, 64, 16, [60] * 40, [60 + r.randint(0, 200) for _ in range(40)])
+    long64 = (4, 2, 64, 32, [300] * 9 + [1], [300 + r.randint(0, 900) for _ in range(9)] + [700])
+    long128 = (4, 2, 128, 32, [200] * 13 + [1], [200 + r.randint(0, 900) for _ in range(13)] + [700])
+    few64 = (64, 8, 64, 16, [1] * 300, [r.randint(200, 700) for _ in range(300)])
+    few128 = (64, 8, 128, 16, [1] * 300, [r.randint(200, 700) for _ in range(300)])
+    some128 = (64, 8, 128, 16, [2] * 120, [r.randint(200, 700) for _ in range(120)])
+    ws = torch.zeros(1 << 28, dtype=torch.uint8, device="cuda")
+    for i, (H, G, dh, page, n, kv) in enumerate([wide64, long128, few128, long64, some128, wide64, few64, long128, long64]):
+        used = sum(-(-x // page) for x in kv)
+        kc, ke = quantised(used, G, page, dh, "hnd", 1)
+        vc, ve = quantised(used, G, page, dh, "hnd", 2)
+        torch.manual_seed(i)
+        q = torch.randn(sum(n), H, dh, device="cuda").to(dt)
+        table, cu = tables(kv, page, used, i), starts(n)
+        out, lse = attn(P, q, kc, ke, vc, ve, table, cu, kv, ws=ws)
+        want, wl, tol, ltol = R.attention(q, kc, ke, vc, ve, i32(table), cu, kv)
+        R16.check(out, want, tol, f"step {i}: out")
+        R16.check(lse, wl, ltol, f"step {i}: lse")
+    assert P.pi_last_device_status() == 0
