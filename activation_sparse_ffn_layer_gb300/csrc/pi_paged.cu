@@ -606,7 +606,7 @@ pi_status pi_rope_store(const pi_rope_plan* plan, const pi_page_desc* cache, con
         d.dtype > PI_T_F32)
         return PI_ERR_INVALID_ARG;
     const bool has_q = q || q_out, has_kv = k || v || kcache || vcache || slots;
-    if (!has_q && !has_kv) return PI_ERR_INVALID_ARG;
+    if (!has_q && !has_kv) return d.tokens == 0 ? PI_OK : PI_ERR_INVALID_ARG;   // (empty tensors have no address)
     auto stride_ok = [&](long long s, int heads) {
         return s % 8 == 0 && s >= (long long)heads * cache->head_dim && s <= (1ll << 36);
     };

@@ -552,7 +552,7 @@ pi_status pi_rope_store8(const pi_rope_plan* plan, const pi_page8_desc* cache, c
         d.dtype > PI_T_F32)
         return PI_ERR_INVALID_ARG;
     const bool has_q = q || q_out, has_kv = k || v || kcache || vcache || kexp || vexp || slots;
-    if (!has_q && !has_kv) return PI_ERR_INVALID_ARG;
+    if (!has_q && !has_kv) return d.tokens == 0 ? PI_OK : PI_ERR_INVALID_ARG;   // (empty tensors have no address)
     auto stride_ok = [&](long long s, int heads) {
         return s % 8 == 0 && s >= (long long)heads * cache->head_dim && s <= (1ll << 36);
     };
@@ -636,6 +636,7 @@ pi_status pi_page_read8(const pi_read8_desc* desc, const pi_page8_desc* cache, c
     if (d.batch < 1 || d.batch > 4096 || d.max_pages < 1 || (long long)d.max_pages * cache->page_size > (1ll << 30) ||
         d.max_rows < 0 || d.max_rows > (1 << 30) || d.dtype < PI_T_F16 || d.dtype > PI_T_F32)
         return PI_ERR_INVALID_ARG;
+    if (d.max_rows == 0) return PI_OK;   // (empty tensors have no address)
     const long long width = (long long)cache->kv_heads * cache->head_dim;
     auto array_ok = [&](const void* codes, const void* exps, const void* out, long long stride) {
         if (!out) return !codes && !exps;
@@ -645,7 +646,6 @@ pi_status pi_page_read8(const pi_read8_desc* desc, const pi_page8_desc* cache, c
         return PI_ERR_INVALID_ARG;
     if (!block_table || !cu_rows || !aligned(block_table, 4) || !aligned(cu_rows, 4) || !aligned(start, 4))
         return PI_ERR_INVALID_ARG;
-    if (d.max_rows == 0) return PI_OK;
     const long long size = d.dtype == PI_T_F32 ? 4 : 2;
     if (rows_overlap(k_out, size * d.k_stride, size * width, v_out, size * d.v_stride, size * width, d.max_rows))
         return PI_ERR_INVALID_ARG;

@@ -1,4 +1,4 @@
-"""The 8-bit paged cache at its edges: workspaces that heads of both widths share."""
+"""The 8-bit paged cache at its edges: workspaces that heads of both widths share, rows of no request."""
 import random
 
 import pytest
@@ -6,7 +6,7 @@ import torch
 
 from tests import paged8_ref as R
 from tests import paged_ref as R16
-from tests.test_gpu_paged8 import BF16, F16, P, attn, i32, quantised, starts, tables  # noqa: F401
+from tests.test_gpu_paged8 import BF16, F16, P, attn, i32, make_cache, quantised, starts, tables  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +37,23 @@ def test_heads_of_both_widths_on_one_workspace(P, dt):
         R16.check(out, want, tol, f"step {i}: out")
         R16.check(lse, wl, ltol, f"step {i}: lse")
     assert P.pi_last_device_status() == 0
+
+
+# ------------------------------------------------------------------ rows of no request
+
+def test_calls_of_no_rows(P):
+    """Nothing to rotate, store, read or attend to: nothing is done, and nothing refused."""
+    kc, ke = make_cache(4, 2, 16, 64, "hnd", 1)
+    cache, plan = P.page8_desc(kc, kc), P.rope_plan(64)
+    none, slots = torch.empty(0, 2, 64, dtype=F16, device="cuda"), torch.empty(0, dtype=torch.int64, device="cuda")
+    pos, before = i32([]), kc.view(torch.uint8).clone()
+    P.pi_rope_store8(plan, cache, none, None, None, pos, None, none, None, None, None, None)
+    P.pi_rope_store8(plan, cache, none, none, none, pos, slots, none, kc, kc, ke, ke)
+    other = torch.zeros(4, 2, 16, 64, dtype=F16, device="cuda")
+    P.pi_rope_store(plan, P.page_desc(other, other), none, None, None, pos, None, none, None, None)
+    P.pi_page_read8(P.read8_desc(1, 4, 0), cache, kc, kc, ke, ke, i32([[0, 1, 2, 3]]), None, i32([0, 0]), none, none)
+    from activation_sparse_ffn_layer_gb300.paged import PagedCache
+    c = PagedCache(4, 2, 64, 2, 64, 8, 16, bits=8)
+    k, v = c.read(0, None, i32([0, 0, 0]), 0)
+    assert k.shape == v.shape == (0, 2, 64) and k.dtype is F16
+    assert torch.equal(kc.view(torch.uint8), before) and P.pi_last_device_status() == 0
