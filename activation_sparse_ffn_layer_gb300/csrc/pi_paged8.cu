@@ -417,42 +417,54 @@ template <typename O>
 __global__ void __launch_bounds__(256) k_page_read8(const __grid_constant__ Read8Args a) {
     pdl_entry();
     __shared__ long long code_at[kReadRows], exp_at[kReadRows];   // -1: zeros, -2: no row
-    const int row0 = blockIdx.x * a.rows;
-    if ((int)threadIdx.x < a.rows) {
-        const int row = row0 + threadIdx.x;
-        long long code = -2, ex = 0;
-        if (row < a.max_rows) {
-            // the last request that starts at or before the row
-            int lo = 0, hi = a.batch;
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) / 2;
-                if (a.cu[mid] <= row) lo = mid;
-                else hi = mid;
-            }
-            const int first = a.cu[lo], end = a.cu[lo + 1];
-            if (first >= 0 && first <= row && row < end && end <= a.max_rows) {
-                const long long pos = (long long)(a.start ? a.start[lo] : 0) + (row - first);
-                code = -1;
-                if (pos >= 0 && pos < (long long)a.max_pages << a.c.page_shift) {
-                    const int id = a.table[(size_t)lo * a.max_pages + (size_t)(pos >> a.c.page_shift)];
-                    const int in_page = (int)(pos & ((1 << a.c.page_shift) - 1));
-                    if (id >= 0 && id < a.c.num_pages) {
-                        code = id * a.c.page_stride + in_page * a.c.token_stride;
-                        ex = ((long long)id * a.c.kv_heads << (a.c.page_shift - 4)) + in_page / kBlock;
-                    }
-                }
-                if (code < 0) atomicExch(a.status, (int)PI_ERR_INVALID_ARG);
+    const int row0 = blockIdx.x * a.rows, row = row0 + threadIdx.x;
+    const bool mine = (int)threadIdx.x < a.rows && row < a.max_rows;
+    auto holds = [&](int b) {   // request b is consistent, and the row one of its
+        const int first = a.cu[b], end = a.cu[b + 1];
+        return first >= 0 && first <= row && row < end && end <= a.max_rows;
+    };
+    auto find = [&](int b) {    // where the row's codes are, as one of request b's
+        const long long pos = (long long)(a.start ? a.start[b] : 0) + (row - a.cu[b]);
+        long long code = -1, ex = 0;
+        if (pos >= 0 && pos < (long long)a.max_pages << a.c.page_shift) {
+            const int id = a.table[(size_t)b * a.max_pages + (size_t)(pos >> a.c.page_shift)];
+            const int in_page = (int)(pos & ((1 << a.c.page_shift) - 1));
+            if (id >= 0 && id < a.c.num_pages) {
+                code = id * a.c.page_stride + in_page * a.c.token_stride;
+                ex = ((long long)id * a.c.kv_heads << (a.c.page_shift - 4)) + in_page / kBlock;
             }
         }
+        if (code < 0) atomicExch(a.status, (int)PI_ERR_INVALID_ARG);
         code_at[threadIdx.x] = code;
         exp_at[threadIdx.x] = ex;
+    };
+    bool open = false;   // a row whose request is not found
+    if (mine) {
+        // the last request that starts at or before the row
+        int lo = 0, hi = a.batch;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (a.cu[mid] <= row) lo = mid;
+            else hi = mid;
+        }
+        open = !holds(lo);
+        if (!open) find(lo);
     }
-    if (blockIdx.x == 0) {
+    if ((int)threadIdx.x < a.rows && (!mine || open)) code_at[threadIdx.x] = -2;
+    if (__syncthreads_or(open) || blockIdx.x == 0) {
         bool bad = false;
         for (int b = threadIdx.x; b < a.batch; b += 256) bad |= a.cu[b] < 0 || a.cu[b + 1] < a.cu[b] || a.cu[b + 1] > a.max_rows;
-        if (bad) atomicExch(a.status, (int)PI_ERR_INVALID_ARG);
+        if (__syncthreads_or(bad)) {
+            // cu_rows is not in order everywhere, and the search may have missed: one by one
+            if (bad) atomicExch(a.status, (int)PI_ERR_INVALID_ARG);
+            for (int b = 0; open && b < a.batch; ++b)
+                if (holds(b)) {
+                    find(b);
+                    open = false;
+                }
+            __syncthreads();
+        }
     }
-    __syncthreads();
     // a thread keeps its piece of the rows (of keys or values) and goes from row to row
     const int first_array = a.k_out ? 0 : 1, pieces = ((a.k_out ? 1 : 0) + (a.v_out ? 1 : 0)) * a.per_row;
     const int beside = max(1, 256 / pieces), r0 = pieces < 256 ? threadIdx.x / pieces : 0;   // rows that a pass takes

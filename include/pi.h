@@ -579,8 +579,8 @@ typedef struct {
  * would round past 65504 are 65504).  Rows past cu_rows[batch] are left alone.
  * A position outside 0 .. max_pages * page_size - 1 or a page id outside the
  * cache reads as zeros, and an inconsistent request (cu_rows decreasing,
- * negative or past max_rows) is not read; each sets the device status to
- * PI_ERR_INVALID_ARG.  k_out or v_out may be NULL (with its codes and exponents).
+ * negative or past max_rows) is not read, while the others are (a row of several
+ * becomes one of theirs); each sets the device status to PI_ERR_INVALID_ARG.  k_out or v_out may be NULL (with its codes and exponents).
  */
 PI_API pi_status pi_page_read8(const pi_read8_desc *desc, const pi_page8_desc *cache, const void *kcache,
                                const void *vcache, const int8_t *kexp, const int8_t *vexp,

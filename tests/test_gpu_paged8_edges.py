@@ -1,4 +1,5 @@
-"""The 8-bit paged cache at its edges: workspaces that heads of both widths share, rows of no request."""
+"""The 8-bit paged cache at its edges: workspaces that heads of both widths share, rows of no request, reads
+beside requests that are not consistent."""
 import random
 
 import pytest
@@ -57,3 +58,23 @@ def test_calls_of_no_rows(P):
     k, v = c.read(0, None, i32([0, 0, 0]), 0)
     assert k.shape == v.shape == (0, 2, 64) and k.dtype is F16
     assert torch.equal(kc.view(torch.uint8), before) and P.pi_last_device_status() == 0
+
+
+@pytest.mark.parametrize("cu,rows", [([0, 100, 8, 12], 20), ([0, 5, 3, 9], 12), ([0, -4, 2, 7], 8), ([-3, 6, 11, 13], 14),
+                                     ([0, 4, 30, 5, 9], 10), ([4, 7, 7, 9], 10)])
+def test_read_back_beside_inconsistent_requests(P, cu, rows):
+    """Requests whose rows are in order are read, whatever others of the same call ask for."""
+    G, dh, page = 2, 64, 16
+    kc, ke = make_cache(8, G, page, dh, "hnd", 1)
+    val, B = R.values(kc, ke).float(), len(cu) - 1
+    out = torch.full((rows, G, dh), 7.0, device="cuda")
+    P.pi_page_read8(P.read8_desc(B, 1, rows), P.page8_desc(kc, kc), kc, None, ke, None, i32([[b] for b in range(B)]), None,
+                    i32(cu), out, None)
+    fine = [b for b in range(B) if 0 <= cu[b] <= cu[b + 1] <= rows]
+    assert P.pi_last_device_status() == (1 if len(fine) < B else 0)
+    for row in range(rows):
+        mine = [val[b, :, row - cu[b]] for b in fine if cu[b] <= row < cu[b + 1]]
+        if mine:
+            assert any(torch.equal(out[row], x) for x in mine), row
+        else:
+            assert bool((out[row] == 7).all()), row
