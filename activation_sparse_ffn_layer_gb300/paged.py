@@ -40,6 +40,8 @@ class PagedCache:
                  device="cuda", bits: int = 16):
         if bits not in (8, 16):
             raise ValueError("bits: expected 8 or 16")
+        if dtype not in (torch.float16, torch.bfloat16):
+            raise ValueError("dtype: expected float16 or bfloat16")
         per_row = -(-max_seq // page_size)
         pages = batch * per_row if num_pages is None else num_pages
         self.batch, self.heads, self.kv_heads, self.head_dim = batch, heads, kv_heads, head_dim

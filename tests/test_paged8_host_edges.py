@@ -1,5 +1,8 @@
-"""The 8-bit paged cache on the host: calls of no rows."""
+"""The 8-bit paged cache on the host: calls of no rows, and types that a cache is not made for."""
 import ctypes as C
+
+import pytest
+import torch
 
 from tests.test_paged8_host import P, _page  # noqa: F401
 
@@ -21,3 +24,12 @@ def test_calls_of_no_rows_need_no_tensors(P):
     assert L.pi_rope_store8(C.byref(P.rope_plan(128)), C.byref(pg), C.byref(none), 0, *[None] * 11) == 1
     assert L.pi_page_read8(C.byref(B.pi_read8_desc(0, 3, 0, 0, 128, 128)), C.byref(pg), *[None] * 10) == 1
     assert L.pi_page_read8(C.byref(B.pi_read8_desc(2, 3, 0, 3, 128, 128)), C.byref(pg), *[None] * 10) == 1
+
+
+@pytest.mark.parametrize("bits", [8, 16])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float64, torch.int8])
+def test_a_cache_of_other_types_is_refused(P, bits, dtype):
+    """Queries and outputs are fp16 or bf16 with either cache: refused when the cache is made, not at the first step."""
+    from activation_sparse_ffn_layer_gb300.paged import PagedCache
+    with pytest.raises(ValueError):
+        PagedCache(2, 2, 64, 1, 16, 1, 1, dtype=dtype, device="cpu", bits=bits)
