@@ -45,7 +45,7 @@ constexpr int kQueryUnits = 2;           // units of a thread whose loads are in
 constexpr int kQueryTokens = 16;         // tokens of a block at most
 // More blocks of queries than this go through pi_rope_store's kernel, in a launch of their
 // own: here they share registers and shared memory with the keys' and values' blocks, three
-// of which fit an SM.  64 + 2 x 8 heads: 32 tokens 4.4 us in one launch, 7.0 in two; 1024
+// of which fit an SM (by registers; of fp32 rows of 128 elements two, by shared memory).  64 + 2 x 8 heads: 32 tokens 4.4 us in one launch, 7.0 in two; 1024
 // decoding rows 17 and 21, 16384 prompt tokens 145 and 120.
 constexpr int kQueryBlocks = 4096;
 
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kStoreThreads, 3) k_rope_store8(const __grid_c
 // Bound by HBM: 48 requests of 100-8000 positions (8 heads of 128, bf16) 150 us, 6.4 TB/s; 1001
 // rows of 12 heads of 64 take 5-7 us, a chain of four loads (and a call 9 on the host).
 constexpr int kReadRows = 32;
-constexpr int kReadBlocks = 608;    // rows are shared out over this many blocks, where there are enough
+constexpr int kReadBlocks = 4 * 152;   // rows are shared out over this many blocks (four on each SM), where there are enough
 
 struct Read8Args {
     Cache8 c;
@@ -615,8 +615,8 @@ pi_status pi_rope_store8(const pi_rope_plan* plan, const pi_page8_desc* cache, c
     a.status = status_word();
     a.plan = *plan;
     if (a.status == nullptr) return PI_ERR_CUDA;
-    // Windows of one token while that many blocks run at once, of 16 where there are many:
-    // tokens of a prompt share blocks of positions, and one in 16 begins one.  Windows of 1, 4
+    // Windows of one token while that many blocks run at once (four on each of 152 SMs), of 16
+    // where there are many: tokens of a prompt share blocks of positions, and one in 16 begins one.  Windows of 1, 4
     // and 16, two blocks a window: 64 decoding rows 4.9, 7.5 and 21 us, 512 12.6, 10.8 and 23,
     // 4096 68, 58 and 67; eight blocks a window: a chunk of 1999 tokens 73, 42 and 35.
     a.shares = std::max(1, (2 * a.kv_heads + kStoreWarps - 1) / kStoreWarps);

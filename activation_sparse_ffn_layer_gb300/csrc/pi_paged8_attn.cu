@@ -40,8 +40,9 @@
 //  - five tokens of each of 24 sequences, 200-6000 keys, bf16: 92 us.  40 rows are three
 //    items, each of which copies the keys from L2: 450 MB, which at the 22 bytes a cycle
 //    of an SM's copies take 70 us.
-//  - one sequence with 1001 keys: 14 us of latency: 3 to know the work, 1.5 for page and
-//    copies each, 1 for a tile, 5 for the two joins.
+//  - one sequence with 1001 keys: 14-15 us of latency: 3 to know the work, 1.5 for page and
+//    copies each, 1 for a tile, 5 for the two joins.  (Codes straight into registers took 11 us here,
+//    and 73 instead of 57 for the 32 sequences, 261 instead of 190 for the long ones.)
 //  - requests of many rows add the widening to the 16-bit kernel's time: 4096 tokens behind
 //    12288, 17 us of 1160; a prompt of 1999 (12 heads of 64) 5 of 39; in a mixed step of 16
 //    sequences (32 heads, window of 2000) 38 of 175, 0.92 of the memory's rate.
@@ -70,11 +71,15 @@ using namespace pipe;
 constexpr int kRows = 16;            // rows of an item
 constexpr int kFewRows = 64;         // rows of a request up to which it goes through k_attn8_few (or one token's)
 constexpr int kTile = 32;            // keys of a unit of the work split
-// Units that an item counts besides its tiles: of 2, 3, 5 and 8 a mixed step of 16 sequences
-// takes 189, 186, 184 and 181 us, 32 decoding sequences 60.5, 59.2, 59.4 and 59.2, 16 of 32
-// heads 109, 106, 109 and 109.
+// Units that an item counts besides its tiles.  Of 2, 3, 5 and 8 (replayed, L2 flushed) a mixed
+// step of 16 sequences takes 176, 174, 173 and 170 us, 32 decoding sequences 62.2, 61.2, 60.7 and
+// 60.7, 16 of 32 heads 111, 111, 110.5 and 110, five tokens of 24 sequences 95.6, 92.7, 92.7 and
+// 93.0, one sequence 14.6, 15.6, 15.1 and 14.1: fewer cost the steps of many items, more than 5
+// gain 2 % of the mixed step and of the shortest call and nothing elsewhere.
 constexpr int kLead = 5;
-constexpr int kMinUnits = 4;         // units of a block at least (one sequence with 1001 keys: 8 units 16.4 us, 4 15.7, 2 18.0)
+// Units of a block at least: with 2, 3, 4, 6 and 8 one sequence with 1001 keys takes 17.7, 16.7,
+// 15.1, 15.6 and 16.2 us (replayed); steps that fill the blocks anyway do not change.
+constexpr int kMinUnits = 4;
 constexpr float kLift = 7.f;         // log2 of the factor that P, l and O share
 constexpr float kGrow = 8.f;         // growth (log2) of a maximum before m follows
 constexpr float kLn2 = 0.69314718055994531f;
@@ -1127,7 +1132,14 @@ bool codes_maps(Few8Args* a, const void* k, const void* v, const pi_page8_desc& 
 // through k_attn8_few: 64 rows (or a token) where all requests are that short (24 sequences
 // with 64 rows each: 113 us so, 161 over widened pages; with 128 rows 194 and 164), else 8, so
 // that decode steps beside prompts take the 8-row items (16 sequences that decode or take
-// 100-700 tokens 177 us so, 186 with items of 16 rows for up to 64).
+// 100-700 tokens, a head to a KV head: 173 us so, 184 with items of 16 rows for up to 64).
+//   The one border stands for two things, the height of the items and who goes over widened
+// pages, and where requests of a few tokens stand beside a prompt it is low: their caches are
+// widened for 9-64 rows.  24 sequences with 1, 2, 5 and 8 tokens behind 200-6000 beside a chunk
+// of 512 (64 query and 8 KV heads): 122, 207, 206 and 208 us so; 126, 129, 174 and 196 with 64
+// rows and items of 16; 122, 139, 204 and 267 with 64 rows and items of 8.  16 sequences with 8,
+// 16, 40 and 64 tokens beside one (32 heads): 185, 418, 424 and 426 so, 196, 191, 300 and 393, 184,
+// 244, 370 and 574.  What gives both its gains is a height of the items by request.
 bool has_long(int max_new, int group) { return max_new > std::max(1, kFewRows / group); }
 int few_tokens(int max_new, int group) { return std::max(1, (has_long(max_new, group) ? 8 : kFewRows) / group); }
 

@@ -32,7 +32,9 @@ class PagedCache:
     ``num_pages`` pages of ``page_size`` positions serve all rows; a row holds at
     most ``max_seq`` positions and receives at most ``max_new`` tokens a step, the
     rows together at most ``max_tokens``.  ``dtype`` is the type of queries and outputs,
-    and of the caches where ``bits`` is 16; with 8 they hold codes."""
+    and of the caches where ``bits`` is 16; with 8 they hold codes, and where ``max_new`` is
+    above 64 * kv_heads / heads (and 1) the workspace has room for one layer's pages in
+    16 bits, which requests of many tokens go over."""
 
     def __init__(self, heads: int, kv_heads: int, head_dim: int, batch: int, max_seq: int, max_new: int,
                  max_tokens: int, layers: int = 1, page_size: int = 16, num_pages: Optional[int] = None,
@@ -86,8 +88,11 @@ class PagedCache:
         ended, its pages go back).  Rows that cannot be served (the pool ran out,
         the row is full, a negative keep) have kv_len 0 afterwards and hold their
         pages and the positions they kept; the latter two set the device status.
-        All state is updated in place, so a captured step goes on from where the
-        last replay ended."""
+        In 8 bits a position that is given back may leave a mark on those kept: the
+        exponent of its block of 16 does not fall again, and the codes under it have
+        been rounded to it, so steps with proposals that are taken back need not leave
+        the bits of steps without.  All state is updated in place, so a captured step
+        goes on from where the last replay ended."""
         if tokens > self.max_tokens or max_new > self.max_new:
             raise ValueError("more tokens than the cache was made for")
         cached = self.cached if keep is None else torch.minimum(keep, self.cached)
@@ -122,7 +127,8 @@ class PagedCache:
              dtype: Optional[torch.dtype] = None):
         """Keys and values of one layer of an 8-bit cache as rows [rows, kv_heads, head_dim]
         (``dtype``: that of the queries unless given): request b's positions start[b] .. (None:
-        from 0) are rows cu_rows[b] .. cu_rows[b + 1] - 1, for a request that goes elsewhere."""
+        from 0) are rows cu_rows[b] .. cu_rows[b + 1] - 1, for a request that goes elsewhere.
+        Rows of no request are zeros, which both tensors are filled with first."""
         if self.bits != 8:
             raise ValueError("read: expected a cache of 8 bits")
         k = torch.zeros(rows, self.kv_heads, self.head_dim, dtype=dtype or self.q.dtype, device=self.q.device)

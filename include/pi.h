@@ -601,8 +601,9 @@ PI_API size_t pi_paged8_workspace_bytes(const pi_paged_desc *desc, const pi_page
  * 8 / (heads / kv_heads) tokens (and 1) go over a 16-bit copy of the pages they
  * see, which the call makes in the workspace (c 2^e rounded to `dtype`, fp16
  * values past 65504 as that); the workspace of such a descriptor has room for
- * one of the whole cache, twice its bytes.  fp16 outputs that
- * would round past 65504 are 65504.
+ * one of the whole cache, twice its bytes.  max_new is the descriptor's: a step
+ * whose requests are all short is quicker with a descriptor that says so.  fp16
+ * outputs that would round past 65504 are 65504.
  * workspace: pi_paged8_workspace_bytes, 16-byte aligned, zero-filled before its
  * first use (and again after a PI_ERR_TIMEOUT); one workspace serves any number
  * of calls that are stream-ordered, whatever their descriptors, where it has the
